@@ -43,7 +43,7 @@ def listed():
         # eight experts, bound by latency and by reading eight experts' weights
         _case("gemm_token_1", "gemm", 1, 8, 128, 128, 1, True, K=768, N=2048),
         # a decode batch of 256 tokens: about 16 rows in every expert, all weights read once
-        _case("gemm_tokens_256", "gemm", 256, 8, 128, 128, 1, True, K=768, N=2048, out="f32"),
+        _case("gemm_tokens_256", "gemm", 256, 8, 128, 128, 1, True, K=768, N=2048),
         # a prefill chunk of that layer, about 256 rows per expert
         _case("gemm_tokens_4096", "gemm", 4096, 8, 128, 128, 16, False, K=768, N=2048),
         # a large batch of an H = 4096 layer, all experts local, about 1024 rows per expert
@@ -95,7 +95,7 @@ def draw(rng):
             K = 128 * int(round(math.exp(rng.uniform(math.log(2), math.log(32)))))
             if op == "gemm":
                 N = 8 * int(round(math.exp(rng.uniform(math.log(8), math.log(512)))))
-                out = rng.choice(("bf16", "bf16", "f32"))
+                out = "bf16"
             else:
                 N = 128 * int(round(math.exp(rng.uniform(0, math.log(16)))))
                 out = rng.choice(("bf16", "fp8"))
