@@ -6,10 +6,13 @@ the C entry points one for one; before passing a pointer they check that each
 tensor lives on the GPU, is contiguous, has the expected dtype and is large
 enough for what the call will write (the C ABI takes plain pointers and cannot).
 The convenience functions at the bottom (``alloc_handle``, ``route``,
-``dispatch``, ``dispatch_fp8``, ``combine``, ``combine_bwd``, ``dispatch_bwd``)
-only add output allocation.  ``PreparedDispatch``, ``PreparedCombine`` and
-``PreparedCombineBwd`` check reused buffers once and then take only the step's
-row count; ``KernelTimer`` times one call's kernels.
+``dispatch``, ``dispatch_fp8``, ``combine``, ``combine_bwd``, ``dispatch_bwd``,
+``combine_weighted``, ``combine_weighted_bwd``, ``expert_gemm_fp8``,
+``expert_swiglu_fp8``) only add output allocation.  ``PreparedDispatch``,
+``PreparedCombine``, ``PreparedCombineBwd``, ``PreparedCombineWeighted``,
+``PreparedCombineWeightedBwd``, ``PreparedExpertGemmFp8`` and
+``PreparedExpertSwigluFp8`` check reused buffers once and then take only the
+step's row count; ``KernelTimer`` times one call's kernels.
 
 The library is loaded on first use; if it has not been built this raises
 (there is no fallback path).
@@ -36,6 +39,8 @@ MOE_NOALLOC_SCRATCH_BYTES = 4194304  # the fixed route scratch of moe_route_buil
 EXPORTS = ("moe_capacity_min", "moe_route_workspace_size", "moe_route_build",
            "moe_route_build_noalloc", "moe_route_dispatch", "moe_dispatch",
            "moe_dispatch_fp8", "moe_combine", "moe_combine_bwd", "moe_dispatch_bwd",
+           "moe_combine_weighted", "moe_combine_weighted_bwd", "moe_expert_gemm_fp8",
+           "moe_expert_swiglu_fp8",
            "moe_last_error", "moe_device_check", "moe_time_next_call")
 
 
@@ -91,6 +96,14 @@ def lib() -> ctypes.CDLL:
         L.moe_combine_bwd.restype = ctypes.c_int
         L.moe_dispatch_bwd.argtypes = [pd, ph, vp, i32, i64, vp, vp, i32, vp, vp]
         L.moe_dispatch_bwd.restype = ctypes.c_int
+        L.moe_combine_weighted.argtypes = [pd, ph, vp, i32, vp, i64, vp, i32, vp]
+        L.moe_combine_weighted.restype = ctypes.c_int
+        L.moe_combine_weighted_bwd.argtypes = [pd, ph, vp, vp, i32, vp, i64, vp, vp, vp]
+        L.moe_combine_weighted_bwd.restype = ctypes.c_int
+        L.moe_expert_gemm_fp8.argtypes = [pd, ph, vp, vp, i32, i64, vp, vp, i32, vp, vp]
+        L.moe_expert_gemm_fp8.restype = ctypes.c_int
+        L.moe_expert_swiglu_fp8.argtypes = [pd, ph, vp, vp, i32, i64, vp, vp, i32, vp, vp, vp]
+        L.moe_expert_swiglu_fp8.restype = ctypes.c_int
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = ctypes.c_char_p
         L.moe_device_check.argtypes = [ctypes.c_int]
@@ -506,6 +519,198 @@ def moe_dispatch_bwd(desc: Desc, handle: Handle, grad_rows: torch.Tensor, H: int
                                          int(f32), p_tw, _stream(stream)))
 
 
+# The calls below launch on the current device, so every tensor must be there
+# (each pointer is only valid on its own device).
+def _here(*tensors):
+    cur = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != cur:
+            raise MoeError(MOE_ERR_ARG, f"a tensor is on {t.device}, the call runs on the current "
+                                        f"device cuda:{cur}")
+
+
+def _handle_here(handle: Handle, desc: Desc):
+    hd = handle.desc
+    if hd is not desc and (hd.T, hd.k, hd.num_local) != (desc.T, desc.k, desc.num_local):
+        raise MoeError(MOE_ERR_ARG, "the handle belongs to another description "
+                                    "(T, k or num_local differ)")
+    _here(handle.tokens_per_expert, handle.padded_offsets, handle.row_of_slot, handle.status,
+          handle.workspace)
+
+
+def _int32(name: str, v) -> int:
+    if not 0 <= v < 1 << 31:
+        raise MoeError(MOE_ERR_ARG, f"{name} must be in [0, 2^31) (got {v})")
+    return int(v)
+
+
+_FP8 = (torch.uint8, torch.float8_e4m3fn)
+_BF16_F32 = (torch.bfloat16, torch.float32)
+
+
+def _weighted_ptrs(desc, handle, Y, H, cap, topk_w, out):
+    _handle_here(handle, desc)
+    _here(Y, topk_w, out)
+    H = _int32("H", H)
+    p_y = _dev(Y, "Y", _BF16, cap * H) if cap else None
+    p_w = _dev(topk_w, "topk_w", _F32, desc.T * desc.k) if desc.T else None
+    p_o = _dev(out, "out", _BF16_F32, desc.T * H) if desc.T else None
+    return p_y, p_w, p_o
+
+
+def moe_combine_weighted(desc: Desc, handle: Handle, Y: torch.Tensor, H: int, R: int,
+                         topk_w: torch.Tensor, out: torch.Tensor, stream=None) -> int:
+    p_y, p_w, p_o = _weighted_ptrs(desc, handle, Y, H, R, topk_w, out)
+    return _check(lib().moe_combine_weighted(ctypes.byref(desc), handle.cref(), p_y, H, p_w, R, p_o,
+                                             int(out.dtype == torch.float32), _stream(stream)))
+
+
+def _weighted_bwd_ptrs(desc, handle, grad_out, Y, H, cap, topk_w, grad_rows, dw):
+    _handle_here(handle, desc)
+    _here(grad_out, Y, topk_w, grad_rows, dw)
+    H = _int32("H", H)
+    n = desc.T * desc.k
+    p_g = _dev(grad_out, "grad_out", _BF16, desc.T * H) if desc.T else None
+    p_y = _dev(Y, "Y", _BF16, cap * H) if cap else None
+    p_w = _dev(topk_w, "topk_w", _F32, n) if desc.T else None
+    p_gr = _dev(grad_rows, "grad_rows", _BF16, cap * H) if cap else None
+    p_dw = _dev(dw, "dw", _F32, n) if desc.T else None
+    return p_g, p_y, p_w, p_gr, p_dw
+
+
+def moe_combine_weighted_bwd(desc: Desc, handle: Handle, grad_out: torch.Tensor, Y: torch.Tensor,
+                             H: int, R: int, topk_w: torch.Tensor, grad_rows: torch.Tensor,
+                             dw: torch.Tensor, stream=None) -> int:
+    p_g, p_y, p_w, p_gr, p_dw = _weighted_bwd_ptrs(desc, handle, grad_out, Y, H, R, topk_w,
+                                                   grad_rows, dw)
+    return _check(lib().moe_combine_weighted_bwd(ctypes.byref(desc), handle.cref(), p_g, p_y, H,
+                                                 p_w, R, p_gr, p_dw, _stream(stream)))
+
+
+def _product_ptrs(desc, handle, rows_q, row_scale, K, cap, w_q, w_scale, n):
+    """Checked pointers of a product with n weight rows per expert."""
+    _handle_here(handle, desc)
+    _here(rows_q, row_scale, w_q, w_scale)
+    K, EL = _int32("K", K), desc.num_local
+    if not cap:
+        return None, None, None, None
+    return (_dev(rows_q, "rows_q", _FP8, cap * K),
+            _dev(row_scale, "row_scale", _F32, cap * (K // 128)),
+            _dev(w_q, "w_q", _FP8, EL * n * K),
+            _dev(w_scale, "w_scale", _F32, EL * -(-n // 128) * (K // 128)))
+
+
+def moe_expert_gemm_fp8(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scale: torch.Tensor,
+                        K: int, R: int, w_q: torch.Tensor, w_scale: torch.Tensor, N: int,
+                        out: torch.Tensor, stream=None) -> int:
+    """out [R,N] bf16 = every expert's E4M3 rows times its E4M3 weights [EL,N,K]."""
+    p = _product_ptrs(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, _int32("N", N))
+    _here(out)
+    p_o = _dev(out, "out", _BF16, R * N) if R else None
+    return _check(lib().moe_expert_gemm_fp8(ctypes.byref(desc), handle.cref(), p[0], p[1], K, R,
+                                            p[2], p[3], N, p_o, _stream(stream)))
+
+
+def _swiglu_out(out, out_scale, cap, I):
+    _here(out, out_scale)
+    if (out.dtype == torch.bfloat16) != (out_scale is None):
+        raise MoeError(MOE_ERR_ARG, "out is bfloat16 without out_scale, or E4M3 codes "
+                                    "(float8_e4m3fn or uint8) with it")
+    if not cap:  # nothing to write
+        return None, None
+    p_o = _dev(out, "out", _BF16 if out_scale is None else _FP8, cap * I)
+    return p_o, _dev(out_scale, "out_scale", _F32, cap * (I // 128), optional=True)
+
+
+def moe_expert_swiglu_fp8(desc: Desc, handle: Handle, rows_q: torch.Tensor,
+                          row_scale: torch.Tensor, K: int, R: int, w_q: torch.Tensor,
+                          w_scale: torch.Tensor, I: int, out: torch.Tensor,
+                          out_scale: torch.Tensor | None = None, stream=None) -> int:
+    """h = silu(gate) * up of the product with w_q [EL,2I,K] (gate rows first): out [R,I] bf16,
+    or, with out_scale [R,I/128], out [R,I] E4M3 codes."""
+    p = _product_ptrs(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, 2 * _int32("I", I))
+    p_o, p_s = _swiglu_out(out, out_scale, R, I)
+    return _check(lib().moe_expert_swiglu_fp8(ctypes.byref(desc), handle.cref(), p[0], p[1], K, R,
+                                              p[2], p[3], I, p_o, p_s, _stream(stream)))
+
+
+class _Prepared:
+    """A call over buffers that a loop reuses on every step, checked once against
+    the buffers' capacity; each call passes only the step's row count R.  Same
+    contract as PreparedCombine."""
+
+    def _bind(self, fn, desc, handle, head, tail, capacity, keep):
+        self.capacity = capacity
+        self._fn = fn
+        self._desc = Desc.from_buffer_copy(desc)
+        self._head = (ctypes.byref(self._desc), handle.cref(), *head)
+        self._tail = tail
+        self._keep = (handle, *keep)
+
+    def __call__(self, R: int) -> int:
+        if not 0 <= R <= self.capacity:
+            raise MoeError(MOE_ERR_ARG, f"R={R} outside [0, {self.capacity}] rows of the buffers")
+        return _check(self._fn(*self._head, R, *self._tail))
+
+
+def _positive(name, v):
+    if v <= 0:
+        raise MoeError(MOE_ERR_ARG, f"{name} must be positive (got {v})")
+    return v
+
+
+class PreparedCombineWeighted(_Prepared):
+    """moe_combine_weighted of up to Y.shape[0] rows into `out`, checked once."""
+
+    def __init__(self, desc: Desc, handle: Handle, Y: torch.Tensor, H: int, topk_w: torch.Tensor,
+                 out: torch.Tensor, stream=None):
+        cap = Y.numel() // _positive("H", H)
+        p_y, p_w, p_o = _weighted_ptrs(desc, handle, Y, H, cap, topk_w, out)
+        self._bind(lib().moe_combine_weighted, desc, handle, (p_y, H, p_w),
+                   (p_o, int(out.dtype == torch.float32), _stream(stream)), cap, (Y, topk_w, out))
+
+
+class PreparedCombineWeightedBwd(_Prepared):
+    """moe_combine_weighted_bwd over up to min(Y, grad_rows) rows, checked once."""
+
+    def __init__(self, desc: Desc, handle: Handle, grad_out: torch.Tensor, Y: torch.Tensor, H: int,
+                 topk_w: torch.Tensor, grad_rows: torch.Tensor, dw: torch.Tensor, stream=None):
+        cap = min(Y.numel(), grad_rows.numel()) // _positive("H", H)
+        p_g, p_y, p_w, p_gr, p_dw = _weighted_bwd_ptrs(desc, handle, grad_out, Y, H, cap, topk_w,
+                                                       grad_rows, dw)
+        self._bind(lib().moe_combine_weighted_bwd, desc, handle, (p_g, p_y, H, p_w),
+                   (p_gr, p_dw, _stream(stream)), cap, (grad_out, Y, topk_w, grad_rows, dw))
+
+
+class PreparedExpertGemmFp8(_Prepared):
+    """moe_expert_gemm_fp8 over up to min(rows_q, out) rows, checked once."""
+
+    def __init__(self, desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scale: torch.Tensor,
+                 K: int, w_q: torch.Tensor, w_scale: torch.Tensor, N: int, out: torch.Tensor,
+                 stream=None):
+        cap = min(rows_q.numel() // _positive("K", K), out.numel() // _positive("N", N))
+        p = _product_ptrs(desc, handle, rows_q, row_scale, K, cap, w_q, w_scale, N)
+        _here(out)
+        p_o = _dev(out, "out", _BF16, cap * N) if cap else None
+        self._bind(lib().moe_expert_gemm_fp8, desc, handle, (p[0], p[1], K),
+                   (p[2], p[3], N, p_o, _stream(stream)), cap,
+                   (rows_q, row_scale, w_q, w_scale, out))
+
+
+class PreparedExpertSwigluFp8(_Prepared):
+    """moe_expert_swiglu_fp8 over up to min(rows_q, out) rows, checked once."""
+
+    def __init__(self, desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scale: torch.Tensor,
+                 K: int, w_q: torch.Tensor, w_scale: torch.Tensor, I: int, out: torch.Tensor,
+                 out_scale: torch.Tensor | None = None, stream=None):
+        cap = min(rows_q.numel() // _positive("K", K), out.numel() // _positive("I", I))
+        p = _product_ptrs(desc, handle, rows_q, row_scale, K, cap, w_q, w_scale, 2 * I)
+        p_o, p_s = _swiglu_out(out, out_scale, cap, I)
+        self._bind(lib().moe_expert_swiglu_fp8, desc, handle, (p[0], p[1], K),
+                   (p[2], p[3], I, p_o, p_s, _stream(stream)), cap,
+                   (rows_q, row_scale, w_q, w_scale, out, out_scale))
+
+
 def moe_device_check(device: int = 0) -> int:
     return _check(lib().moe_device_check(device))
 
@@ -676,3 +881,55 @@ def dispatch_bwd(desc: Desc, handle: Handle, grad_rows: torch.Tensor,
            if grad_row_w is not None else None)
     moe_dispatch_bwd(desc, handle, grad_rows, H, R, gx, grad_row_w, gtw, stream=stream)
     return gx, gtw
+
+
+def combine_weighted(desc: Desc, handle: Handle, Y: torch.Tensor, topk_w: torch.Tensor,
+                     out_dtype=torch.bfloat16, stream=None):
+    """moe_combine_weighted with a fresh output [T,H]."""
+    R, H = Y.shape
+    out = torch.empty((desc.T, H), dtype=out_dtype, device=Y.device)
+    moe_combine_weighted(desc, handle, Y, H, R, topk_w, out, stream=stream)
+    return out
+
+
+def combine_weighted_bwd(desc: Desc, handle: Handle, grad_out: torch.Tensor, Y: torch.Tensor,
+                         topk_w: torch.Tensor, stream=None):
+    """moe_combine_weighted_bwd with fresh outputs: (grad_rows, dw)."""
+    R, H = Y.shape
+    grad_rows = torch.empty_like(Y)
+    dw = torch.empty((desc.T, desc.k), dtype=torch.float32, device=Y.device)
+    moe_combine_weighted_bwd(desc, handle, grad_out, Y, H, R, topk_w, grad_rows, dw, stream=stream)
+    return grad_rows, dw
+
+
+def expert_gemm_fp8(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scale: torch.Tensor,
+                    w_q: torch.Tensor, w_scale: torch.Tensor, stream=None):
+    """moe_expert_gemm_fp8 with a fresh output [R,N] bf16 (its rows past the total are not written)."""
+    (R, K), N = rows_q.shape, w_q.shape[1]
+    _same_k(rows_q, w_q)
+    out = torch.empty((R, N), dtype=torch.bfloat16, device=rows_q.device)
+    moe_expert_gemm_fp8(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, N, out, stream=stream)
+    return out
+
+
+def expert_swiglu_fp8(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scale: torch.Tensor,
+                      w_q: torch.Tensor, w_scale: torch.Tensor, out_dtype=torch.float8_e4m3fn,
+                      stream=None):
+    """moe_expert_swiglu_fp8 with fresh outputs (rows past the total are not written): (h [R,I]
+    float8_e4m3fn, h_scale [R,I/128]), or with out_dtype=torch.bfloat16 (h, None)."""
+    (R, K), I = rows_q.shape, w_q.shape[1] // 2
+    _same_k(rows_q, w_q)
+    if w_q.shape[1] % 2:
+        raise MoeError(MOE_ERR_ARG, f"w_q needs 2I rows per expert (got {w_q.shape[1]})")
+    out = torch.empty((R, I), dtype=out_dtype, device=rows_q.device)
+    out_scale = (None if out_dtype == torch.bfloat16 else
+                 torch.empty((R, I // 128), dtype=torch.float32, device=rows_q.device))
+    moe_expert_swiglu_fp8(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, I, out, out_scale,
+                          stream=stream)
+    return out, out_scale
+
+
+def _same_k(rows_q, w_q):
+    if w_q.dim() != 3 or w_q.shape[2] != rows_q.shape[1]:
+        raise MoeError(MOE_ERR_ARG, f"w_q must be [EL,N,K] with K={rows_q.shape[1]} "
+                                    f"(got {tuple(w_q.shape)})")

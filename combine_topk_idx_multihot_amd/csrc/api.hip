@@ -254,6 +254,55 @@ moe::RowArgs dispatch_args(const moe_desc *desc, const moe_handle *handle, const
     return a;
 }
 
+// Argument rules shared by the experts' products.
+int check_product(const moe_desc *desc, const moe_handle *handle, const uint8_t *rows_q,
+                  const float *row_scale, int32_t K, int64_t R, const uint8_t *w_q,
+                  const float *w_scale)
+{
+    int rc;
+    if ((rc = check_desc(desc)) != MOE_OK)
+        return rc;
+    if ((rc = check_handle(desc, handle)) != MOE_OK)
+        return rc;
+    if ((rc = check_rows(desc, R)) != MOE_OK)
+        return rc;
+    if (K <= 0 || K % 128 != 0)
+        return fail(MOE_ERR_ARG, "K must be a positive multiple of 128 (got %d)", K);
+    if (R > 0 && (!rows_q || !aligned16(rows_q)))
+        return fail(MOE_ERR_ARG, "rows_q must be a non-NULL, 16-byte aligned [R,K] byte tensor");
+    if (R > 0 && (!row_scale || !aligned16(row_scale)))
+        return fail(MOE_ERR_ARG, "row_scale must be a non-NULL, 16-byte aligned [R,K/128] fp32 "
+                                 "tensor");
+    if (R > 0 && (!w_q || !aligned16(w_q)))
+        return fail(MOE_ERR_ARG, "w_q must be a non-NULL, 16-byte aligned [EL,N,K] byte tensor");
+    if (R > 0 && (!w_scale || !aligned16(w_scale)))
+        return fail(MOE_ERR_ARG, "w_scale must be a non-NULL, 16-byte aligned fp32 tensor");
+    return MOE_OK;
+}
+
+// The arguments that both products share.  The groups hold at most R rows and
+// at most the worst case of the description, whatever capacity the caller chose.
+moe::ExpertArgs product_args(const moe_desc *desc, const moe_handle *handle, const uint8_t *rows_q,
+                             const float *row_scale, int32_t K, int64_t R, const uint8_t *w_q,
+                             const float *w_scale)
+{
+    moe::ExpertArgs a;
+    a.a = rows_q;
+    a.sa = row_scale;
+    a.w = w_q;
+    a.sw = w_scale;
+    a.off = handle->padded_offsets;
+    a.status = handle->status;
+    a.R = R;
+    const int64_t worst = cap_min(desc);
+    a.rows_max = R < worst ? R : worst;
+    a.rows_mean = (desc->T * desc->k + desc->E - 1) / desc->E;
+    a.K = K;
+    a.EL = desc->num_local;
+    a.eager = desc->mode == MOE_EAGER;
+    return a;
+}
+
 // One launch of the dispatch.
 int launch_dispatch(const moe_desc *desc, const moe_handle *handle, const uint16_t *x, int32_t H,
                     const float *topk_w, int64_t R, uint16_t *rows, uint8_t *rows_q,
@@ -757,6 +806,163 @@ int moe_dispatch_bwd(const moe_desc *desc, const moe_handle *handle, const uint1
     hipError_t e = moe::launch_combine(a, static_cast<hipStream_t>(stream));
     if (e != hipSuccess)
         return hip_fail(e, "dispatch_bwd launch");
+    return ok();
+}
+
+int moe_combine_weighted(const moe_desc *desc, const moe_handle *handle, const uint16_t *Y,
+                         int32_t H, const float *topk_w, int64_t R, void *out,
+                         int32_t out_is_f32, void *stream)
+{
+    TimingScope timing_scope;
+    int rc;
+    if ((rc = check_desc(desc)) != MOE_OK)
+        return rc;
+    if ((rc = check_handle(desc, handle)) != MOE_OK)
+        return rc;
+    if ((rc = check_hidden(H)) != MOE_OK)
+        return rc;
+    if ((rc = check_rows(desc, R)) != MOE_OK)
+        return rc;
+    if (out_is_f32 != 0 && out_is_f32 != 1)
+        return fail(MOE_ERR_ARG, "out_is_f32 must be 0 or 1 (got %d)", out_is_f32);
+    if (R > 0 && (!Y || !aligned16(Y)))
+        return fail(MOE_ERR_ARG, "Y must be a non-NULL, 16-byte aligned [R,H] bf16 tensor");
+    if (desc->T > 0 && !topk_w)
+        return fail(MOE_ERR_ARG, "topk_w must be a non-NULL [T,k] fp32 tensor (moe_combine adds "
+                                 "rows without weights)");
+    if (desc->T > 0 && (!out || !aligned16(out)))
+        return fail(MOE_ERR_ARG, "out must be a non-NULL, 16-byte aligned [T,H] tensor");
+
+    moe::CombineArgs a;
+    a.Y = Y;
+    a.topk_w = topk_w;
+    a.out = out;
+    a.row_of_slot = handle->row_of_slot;
+    a.grad_row_w = nullptr;
+    a.grad_w = nullptr;
+    a.status = handle->status;
+    a.T = desc->T;
+    a.R = R;
+    a.k = desc->k;
+    a.H = H;
+    a.out_f32 = out_is_f32;
+    a.eager = desc->mode == MOE_EAGER;
+    hipError_t e = moe::launch_combine(a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess)
+        return hip_fail(e, "combine_weighted launch");
+    return ok();
+}
+
+int moe_combine_weighted_bwd(const moe_desc *desc, const moe_handle *handle,
+                             const uint16_t *grad_out, const uint16_t *Y, int32_t H,
+                             const float *topk_w, int64_t R, uint16_t *grad_rows, float *dw,
+                             void *stream)
+{
+    TimingScope timing_scope;
+    int rc;
+    if ((rc = check_desc(desc)) != MOE_OK)
+        return rc;
+    if ((rc = check_handle(desc, handle)) != MOE_OK)
+        return rc;
+    if ((rc = check_hidden(H)) != MOE_OK)
+        return rc;
+    if ((rc = check_rows(desc, R)) != MOE_OK)
+        return rc;
+    if (desc->T > 0 && (!grad_out || !aligned16(grad_out)))
+        return fail(MOE_ERR_ARG, "grad_out must be a non-NULL, 16-byte aligned [T,H] bf16 tensor");
+    if (R > 0 && (!Y || !aligned16(Y)))
+        return fail(MOE_ERR_ARG, "Y must be a non-NULL, 16-byte aligned [R,H] bf16 tensor");
+    if (R > 0 && (!grad_rows || !aligned16(grad_rows)))
+        return fail(MOE_ERR_ARG, "grad_rows must be a non-NULL, 16-byte aligned [R,H] bf16 tensor");
+    if (desc->T > 0 && !topk_w)
+        return fail(MOE_ERR_ARG, "topk_w must be a non-NULL [T,k] fp32 tensor");
+    if (desc->T > 0 && !dw)
+        return fail(MOE_ERR_ARG, "dw must be a non-NULL [T,k] fp32 tensor");
+
+    moe::RowArgs a;
+    a.src = grad_out;
+    a.topk_w = topk_w;
+    a.F = Y;
+    a.rows = grad_rows;
+    a.rows_q = nullptr;
+    a.row_scale = nullptr;
+    a.row_w = nullptr;
+    a.row_token = nullptr;
+    a.row_expert = nullptr;
+    a.dw = desc->T > 0 ? dw : nullptr;
+    a.weighted = 1;
+    a.row_of_slot = handle->row_of_slot;
+    a.tpe = handle->tokens_per_expert;
+    a.off = handle->padded_offsets;
+    a.status = handle->status;
+    a.T = desc->T;
+    a.R = R;
+    a.k = desc->k;
+    a.EL = desc->num_local;
+    a.E_total = desc->E;
+    a.P = desc->pad_multiple;
+    a.H = H;
+    a.eager = desc->mode == MOE_EAGER;
+    a.pairs = handle_pairs(desc, handle, a.pg);
+    moe::row_shape(a);
+    hipError_t e = moe::launch_move_rows(a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess)
+        return hip_fail(e, "combine_weighted_bwd launch");
+    return ok();
+}
+
+int moe_expert_gemm_fp8(const moe_desc *desc, const moe_handle *handle, const uint8_t *rows_q,
+                        const float *row_scale, int32_t K, int64_t R, const uint8_t *w_q,
+                        const float *w_scale, int32_t N, uint16_t *out, void *stream)
+{
+    TimingScope timing_scope;
+    int rc;
+    if ((rc = check_product(desc, handle, rows_q, row_scale, K, R, w_q, w_scale)) != MOE_OK)
+        return rc;
+    if (N <= 0 || N % 8 != 0 || N > (1 << 30))
+        return fail(MOE_ERR_ARG, "N must be a positive multiple of 8 up to 2^30 (got %d)", N);
+    if (R > 0 && (!out || !aligned16(out)))
+        return fail(MOE_ERR_ARG, "out must be a non-NULL, 16-byte aligned [R,N] bf16 tensor");
+    moe::ExpertArgs a = product_args(desc, handle, rows_q, row_scale, K, R, w_q, w_scale);
+    a.out = out;
+    a.out_scale = nullptr;
+    a.N = N;
+    a.NB = (N + 127) / 128;
+    a.gated = 0;
+    if (a.rows_max == 0)
+        return ok();
+    hipError_t e = moe::launch_expert_product(a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess)
+        return hip_fail(e, "expert_gemm_fp8 launch");
+    return ok();
+}
+
+int moe_expert_swiglu_fp8(const moe_desc *desc, const moe_handle *handle, const uint8_t *rows_q,
+                          const float *row_scale, int32_t K, int64_t R, const uint8_t *w_q,
+                          const float *w_scale, int32_t I, void *out, float *out_scale,
+                          void *stream)
+{
+    TimingScope timing_scope;
+    int rc;
+    if ((rc = check_product(desc, handle, rows_q, row_scale, K, R, w_q, w_scale)) != MOE_OK)
+        return rc;
+    if (I <= 0 || I % 128 != 0 || I > (1 << 29))
+        return fail(MOE_ERR_ARG, "I must be a positive multiple of 128 up to 2^29 (got %d)", I);
+    if (R > 0 && (!out || !aligned16(out)))
+        return fail(MOE_ERR_ARG, "out must be a non-NULL, 16-byte aligned [R,I] tensor");
+    if (out_scale && !aligned16(out_scale))
+        return fail(MOE_ERR_ARG, "out_scale must be 16-byte aligned");
+    moe::ExpertArgs a = product_args(desc, handle, rows_q, row_scale, K, R, w_q, w_scale);
+    a.out = out;
+    a.out_scale = out_scale;
+    a.N = I;
+    a.NB = I / 64;
+    a.gated = 1;
+    if (a.rows_max == 0)
+        return ok();
+    hipError_t e = moe::launch_expert_product(a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess)
+        return hip_fail(e, "expert_swiglu_fp8 launch");
     return ok();
 }
 

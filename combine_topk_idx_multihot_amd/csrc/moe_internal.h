@@ -118,6 +118,7 @@ struct RowArgs {
     PairGeom pg;
     int64_t npair_blocks = 0;  // workgroups walking the row list (4 entries each)
     int64_t nzero_blocks = 0;  // combine backward from the list: dw of slots without a row
+    int32_t weighted = 0;      // combine backward: grad rows carry their row's weight (topk_w)
 };
 
 // Row movement: dispatch (x -> rows, or with rows_q set x -> E4M3 rows and
@@ -146,6 +147,7 @@ hipError_t launch_route_move_tiny(const RowArgs &a, const RouteArgs &r, hipStrea
 
 struct CombineArgs {
     const uint16_t *Y;          // [R,H]
+    const float *topk_w = nullptr; // [T,k] weights of the rows (weighted combine) or null
     void *out;                  // [T,H] bf16 or f32
     const int32_t *row_of_slot; // [T,k]
     const float *grad_row_w;    // [R] or null (dispatch backward: per-row weight gradients)
@@ -160,6 +162,27 @@ struct CombineArgs {
 // Combine; with grad_w set it is also the dispatch backward (the weight
 // gradients of the slots are gathered from their rows).
 hipError_t launch_combine(const CombineArgs &a, hipStream_t s);
+
+// The experts' products on E4M3 rows (experts.hip).
+struct ExpertArgs {
+    const uint8_t *a;       // [R,K] E4M3 rows
+    const float *sa;        // [R,K/128] their scales
+    const uint8_t *w;       // [EL,N,K] E4M3 weights (gated: [EL,2N,K], gate rows first)
+    const float *sw;        // [EL,NB,K/128] their scales
+    void *out;              // [R,N] bf16, or E4M3 with out_scale
+    float *out_scale;       // [R,N/128] or null
+    const int32_t *off;     // [EL+1]
+    int32_t *status;
+    int64_t R;
+    int64_t rows_max;       // most rows the groups can hold: min(R, the worst case)
+    int64_t rows_mean;      // expected rows of one expert under uniform routing, rounded up
+    int32_t K, N, EL;
+    int32_t NB;             // scale rows of one expert
+    int32_t ntn;            // column tiles (set by the launcher)
+    int32_t gated;          // silu(gate) * up of a [2N] product
+    int32_t eager;
+};
+hipError_t launch_expert_product(const ExpertArgs &a, hipStream_t s);
 
 // Kernel timing request of the calling host thread (moe_time_next_call).
 // The events ride on the kernels' own dispatch packets: the first kernel of

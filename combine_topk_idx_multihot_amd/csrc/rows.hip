@@ -137,6 +137,8 @@ constexpr int64_t kZeroTask = 4096;  // 16-byte chunks (64 KiB) per zero-fill wa
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -296,6 +298,37 @@ __device__ __forceinline__ void zero_rows(const RowArgs &a, int64_t r0, int64_t 
     }
 }
 
+// The weight of each first slot's row: its own plus its repeats', in slot
+// order (lanes that are no first slot hold their own).
+__device__ __forceinline__ float merged_weight(const float *__restrict__ topk_w, const Slots &sl,
+                                               int64_t t, int k, int lane)
+{
+    const bool prim = sl.valid && sl.first == lane;
+    const float myw = sl.valid ? topk_w[t * k + lane] : 0.f;
+    float W = myw;
+    if (sl.dup_mask) {
+        for (int q = 0; q < k; ++q) {
+            const int rq = __builtin_amdgcn_readlane(sl.row, q);
+            const float wq = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(myw), q));
+            if (prim && q > lane && rq == sl.row)
+                W = W + wq;
+        }
+    }
+    return W;
+}
+
+// A chunk of 8 bf16 values times an fp32 weight, rounded once to bf16.
+__device__ __forceinline__ u32x4 scale_chunk(const u32x4 &v, float w)
+{
+    u32x4 o;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const f32x2 p = {bf16_lo(v[q]) * w, bf16_hi(v[q]) * w};
+        o[q] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf16x2));
+    }
+    return o;
+}
+
 // Token and weight of each of the token's rows (dispatch): the row of a
 // repeated id carries the first slot's weight plus the later ones', in slot
 // order.
@@ -331,7 +364,9 @@ __device__ __forceinline__ void write_row_meta(const RowArgs &a, const Slots &sl
 // dispatch (x -> rows) and the grad rows of the combine backward (grad_out ->
 // rows): a token's row read once, written to each of its local rows
 // ---------------------------------------------------------------------------
-template <int SEG>
+// WT: every row gets the token's row times its weight (the weighted combine's
+// backward).
+template <int SEG, bool WT = false>
 __device__ __forceinline__ void move_token(const RowArgs &a, int64_t bid)
 {
     const int lane = threadIdx.x & (kWave - 1);
@@ -353,6 +388,9 @@ __device__ __forceinline__ void move_token(const RowArgs &a, int64_t bid)
     const int nseg = (nch + SPAN - 1) / SPAN;
     if (!sl.prim_mask)
         return;
+    float W = 0.f;
+    if constexpr (WT)
+        W = merged_weight(a.topk_w, sl, t, a.k, lane);
     for (int sg = wt; sg < nseg; sg += nwt) {
         const int c0 = sg * SPAN;
         u32x4 v[SEG];
@@ -364,11 +402,13 @@ __device__ __forceinline__ void move_token(const RowArgs &a, int64_t bid)
             for (int b = 0; b < kCopyBatch; ++b) {
                 if (b < bt.n) {
                     u32x4 *__restrict__ dst = reinterpret_cast<u32x4 *>(a.rows + bt.row[b] * a.H);
+                    const float w =
+                        WT ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(W), bt.lane[b])) : 0.f;
 #pragma unroll
                     for (int i = 0; i < SEG; ++i) {
                         const int c = c0 + i * kWave + lane;
                         if (c < nch)
-                            put16<MOE_NT_COPY_ROWS != 0>(dst + c, v[i]);
+                            put16<MOE_NT_COPY_ROWS != 0>(dst + c, WT ? scale_chunk(v[i], w) : v[i]);
                     }
                 }
             }
@@ -678,12 +718,13 @@ __device__ __forceinline__ void list_dispatch(const RowArgs &a, int64_t pb)
     }
 }
 
-// The combine backward's step on one 16-byte chunk: grad_out's chunk stored
-// to the grad row and multiplied with the expert output's into the fp64 sum.
+// The combine backward's step on one 16-byte chunk: grad_out's chunk (WT:
+// times the row's weight) stored to the grad row and multiplied with the expert output's into the fp64 sum.
+template <bool WT>
 __device__ __forceinline__ void list_bwd_chunk(u32x4 *__restrict__ dst, const u32x4 &g, const u32x4 &f,
-                                               double &acc)
+                                               float w, double &acc)
 {
-    put16<MOE_NT_COPY_ROWS != 0>(dst, g);
+    put16<MOE_NT_COPY_ROWS != 0>(dst, WT ? scale_chunk(g, w) : g);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         acc = fma(static_cast<double>(bf16_lo(g[q])), static_cast<double>(bf16_lo(f[q])), acc);
@@ -692,9 +733,10 @@ __device__ __forceinline__ void list_bwd_chunk(u32x4 *__restrict__ dst, const u3
 }
 
 // N chunk pairs per lane, all present, loads first (as list_copy_n).
-template <int N>
+template <int N, bool WT>
 __device__ __forceinline__ void list_bwd_n(const u32x4 *__restrict__ src, u32x4 *__restrict__ dst,
-                                           const u32x4 *__restrict__ frow, int c0, int lane, double &acc)
+                                           const u32x4 *__restrict__ frow, int c0, int lane, float w,
+                                           double &acc)
 {
     u32x4 g[N], f[N];
 #pragma unroll
@@ -704,17 +746,18 @@ __device__ __forceinline__ void list_bwd_n(const u32x4 *__restrict__ src, u32x4 
     }
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        list_bwd_chunk(dst + c0 + i * kWave + lane, g[i], f[i], acc);
+        list_bwd_chunk<WT>(dst + c0 + i * kWave + lane, g[i], f[i], w, acc);
 }
 
-template <int N>
+template <int N, bool WT>
 __device__ __forceinline__ void list_bwd_upto(int n, const u32x4 *__restrict__ src, u32x4 *__restrict__ dst,
-                                              const u32x4 *__restrict__ frow, int c0, int lane, double &acc)
+                                              const u32x4 *__restrict__ frow, int c0, int lane, float w,
+                                              double &acc)
 {
     if (n == N)
-        list_bwd_n<N>(src, dst, frow, c0, lane, acc);
+        list_bwd_n<N, WT>(src, dst, frow, c0, lane, w, acc);
     else if constexpr (N > 1)
-        list_bwd_upto<N - 1>(n, src, dst, frow, c0, lane, acc);
+        list_bwd_upto<N - 1, WT>(n, src, dst, frow, c0, lane, w, acc);
 }
 
 // Combine backward of one row from the list (launched with dw; expert_out is
@@ -722,6 +765,7 @@ __device__ __forceinline__ void list_bwd_upto(int n, const u32x4 *__restrict__ s
 // and its dot with the expert-output row (exact products, fp64 sums: each
 // lane's elements in order, then a fixed butterfly) given to every slot of
 // the token that names the row.
+template <bool WT>
 __device__ __forceinline__ void list_bwd(const RowArgs &a, int64_t pb)
 {
     const int lane = threadIdx.x & (kWave - 1);
@@ -735,6 +779,20 @@ __device__ __forceinline__ void list_bwd(const RowArgs &a, int64_t pb)
     const int k = a.k;
     const int64_t s = static_cast<int64_t>(t) * k + lane;
     const int rj = lane < k ? a.row_of_slot[s] : -1;
+    float W = 0.f;
+    if constexpr (WT) {
+        // the row's weight: its slots' weights added in slot order
+        const float wj = rj == r ? a.topk_w[s] : 0.f;
+        uint64_t m = __ballot(rj == r);
+        bool first = true;
+        while (m) {
+            const int j = __builtin_ctzll(m);
+            m &= m - 1;
+            const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wj), j));
+            W = first ? v : W + v;
+            first = false;
+        }
+    }
     const int nch = a.H >> 3;
     const u32x4 *__restrict__ src = reinterpret_cast<const u32x4 *>(a.src + static_cast<int64_t>(t) * a.H);
     u32x4 *__restrict__ dst = reinterpret_cast<u32x4 *>(a.rows + static_cast<int64_t>(r) * a.H);
@@ -745,12 +803,13 @@ __device__ __forceinline__ void list_bwd(const RowArgs &a, int64_t pb)
     int n = nch / kWave;
     int c0 = 0;
     for (; n > kListBwdMax; n -= kListBwdMax, c0 += kListBwdMax * kWave)
-        list_bwd_n<kListBwdMax>(src, dst, frow, c0, lane, acc);
+        list_bwd_n<kListBwdMax, WT>(src, dst, frow, c0, lane, W, acc);
     if (n > 0)
-        list_bwd_upto<kListBwdMax>(n, src, dst, frow, c0, lane, acc);
+        list_bwd_upto<kListBwdMax, WT>(n, src, dst, frow, c0, lane, W, acc);
     c0 += n * kWave;
     if (c0 + lane < nch)
-        list_bwd_chunk(dst + c0 + lane, src[c0 + lane], __builtin_nontemporal_load(frow + c0 + lane), acc);
+        list_bwd_chunk<WT>(dst + c0 + lane, src[c0 + lane], __builtin_nontemporal_load(frow + c0 + lane), W,
+                           acc);
 #pragma unroll
     for (int o = kWave / 2; o >= 1; o >>= 1)
         acc += __shfl_xor(acc, o);
@@ -787,6 +846,7 @@ __global__ void __launch_bounds__(kRowThreads) k_rows_list(RowArgs a)
 }
 
 // Grid: [sentinel blocks][list blocks][dw-zero blocks][expert blocks].
+template <bool WT>
 __global__ void __launch_bounds__(kRowThreads) k_bwd_list(RowArgs a)
 {
     int64_t bid = blockIdx.x;
@@ -796,7 +856,7 @@ __global__ void __launch_bounds__(kRowThreads) k_bwd_list(RowArgs a)
     }
     bid -= a.nsent_blocks;
     if (bid < a.npair_blocks) {
-        list_bwd(a, bid);
+        list_bwd<WT>(a, bid);
         return;
     }
     bid -= a.npair_blocks;
@@ -1227,7 +1287,7 @@ __host__ __device__ __forceinline__ int64_t bwd_mid_blocks(const RowArgs &a)
 
 // Grid: [sentinel blocks][periods of (waves_per_token copy blocks, dot_wpt
 // dot blocks), 4 tokens each][expert blocks].
-template <int SEG, int DSEG>
+template <int SEG, int DSEG, bool WT>
 __global__ void __launch_bounds__(kRowThreads) k_bwd_split(RowArgs a)
 {
     int64_t bid = blockIdx.x;
@@ -1249,7 +1309,7 @@ __global__ void __launch_bounds__(kRowThreads) k_bwd_split(RowArgs a)
         if (period >= a.ndot_blocks)
             return;
         if (pos < a.waves_per_token)
-            move_token<SEG>(a, period * a.waves_per_token + pos);
+            move_token<SEG, WT>(a, period * a.waves_per_token + pos);
         else
             dot_tokens<DSEG>(a, period * a.dot_wpt + (pos - a.waves_per_token));
         return;
@@ -1404,7 +1464,8 @@ __global__ void __launch_bounds__(kRowThreads) k_dispatch_fp8(RowArgs a)
 // workgroup read all segments of a token's rows at about the same time
 // ---------------------------------------------------------------------------
 // GW: the dispatch backward (also gathers the weight gradients of the slots).
-template <int SEG, bool OUT_F32, bool GW>
+// WT: every row enters with its weight, by one fma per element.
+template <int SEG, bool OUT_F32, bool GW, bool WT = false>
 __global__ void __launch_bounds__(kRowThreads) k_combine(CombineArgs a)
 {
     const int lane = threadIdx.x & (kWave - 1);
@@ -1427,6 +1488,9 @@ __global__ void __launch_bounds__(kRowThreads) k_combine(CombineArgs a)
         for (int q = 0; q < 8; ++q)
             acc[i][q] = 0.f;
     bool first = true;
+    float W = 0.f;
+    if constexpr (WT)
+        W = merged_weight(a.topk_w, sl, t, a.k, lane);
     uint64_t mrest = sl.prim_mask;
     while (mrest) {
         const Batch<kCombBatch> bt = take_batch<kCombBatch>(mrest, sl.row);
@@ -1438,12 +1502,19 @@ __global__ void __launch_bounds__(kRowThreads) k_combine(CombineArgs a)
 #pragma unroll
         for (int b = 0; b < kCombBatch; ++b) {
             if (b < bt.n) {
+                const float w =
+                    WT ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(W), bt.lane[b])) : 0.f;
 #pragma unroll
                 for (int i = 0; i < SEG; ++i) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const float lo = bf16_lo(f[b][i][q]);
                         const float hi = bf16_hi(f[b][i][q]);
+                        if constexpr (WT) {
+                            acc[i][2 * q] = first ? lo * w : fmaf(lo, w, acc[i][2 * q]);
+                            acc[i][2 * q + 1] = first ? hi * w : fmaf(hi, w, acc[i][2 * q + 1]);
+                            continue;
+                        }
                         acc[i][2 * q] = first ? lo : acc[i][2 * q] + lo;
                         acc[i][2 * q + 1] = first ? hi : acc[i][2 * q + 1] + hi;
                     }
@@ -1631,6 +1702,22 @@ static int list_waves(int32_t H, int64_t flight)
     return static_cast<int>(w < 2 ? 2 : (w > 8 ? 8 : w));
 }
 
+template <bool WT>
+static void launch_split(const RowArgs &a, dim3 g, dim3 blk, hipStream_t s)
+{
+    switch (a.seg * 8 + a.dot_seg) {
+    case 1 * 8 + 1: launch(k_bwd_split<1, 1, WT>, g, blk, 0, s, a); break;
+    case 1 * 8 + 2: launch(k_bwd_split<1, 2, WT>, g, blk, 0, s, a); break;
+    case 1 * 8 + 4: launch(k_bwd_split<1, 4, WT>, g, blk, 0, s, a); break;
+    case 2 * 8 + 1: launch(k_bwd_split<2, 1, WT>, g, blk, 0, s, a); break;
+    case 2 * 8 + 2: launch(k_bwd_split<2, 2, WT>, g, blk, 0, s, a); break;
+    case 2 * 8 + 4: launch(k_bwd_split<2, 4, WT>, g, blk, 0, s, a); break;
+    case 4 * 8 + 1: launch(k_bwd_split<4, 1, WT>, g, blk, 0, s, a); break;
+    case 4 * 8 + 2: launch(k_bwd_split<4, 2, WT>, g, blk, 0, s, a); break;
+    default: launch(k_bwd_split<4, 4, WT>, g, blk, 0, s, a); break;
+    }
+}
+
 bool move_rows_fits(const RowArgs &a)
 {
     // the sync-free tail's launch and the rows' launch, each within the limit
@@ -1655,7 +1742,8 @@ hipError_t launch_move_rows(const RowArgs &a0, hipStream_t s)
             return hipSuccess;
         const dim3 gl(static_cast<unsigned>(nbl));
         if (a.dw)
-            launch(k_bwd_list, gl, dim3(kRowThreads), lds_cap(list_waves(a.H, MOE_LIST_FLIGHT_BWD)), s, a);
+            launch(a.weighted ? k_bwd_list<true> : k_bwd_list<false>, gl, dim3(kRowThreads),
+                   lds_cap(list_waves(a.H, MOE_LIST_FLIGHT_BWD)), s, a);
         else
             launch(k_rows_list, gl, dim3(kRowThreads), lds_cap(list_waves(a.H, MOE_LIST_FLIGHT_COPY)), s,
                    a);
@@ -1674,17 +1762,7 @@ hipError_t launch_move_rows(const RowArgs &a0, hipStream_t s)
         default: launch(k_dispatch_fp8<4>, g, blk, 0, s, a); break;
         }
     } else if (a.dw) {
-        switch (a.seg * 8 + a.dot_seg) {
-        case 1 * 8 + 1: launch(k_bwd_split<1, 1>, g, blk, 0, s, a); break;
-        case 1 * 8 + 2: launch(k_bwd_split<1, 2>, g, blk, 0, s, a); break;
-        case 1 * 8 + 4: launch(k_bwd_split<1, 4>, g, blk, 0, s, a); break;
-        case 2 * 8 + 1: launch(k_bwd_split<2, 1>, g, blk, 0, s, a); break;
-        case 2 * 8 + 2: launch(k_bwd_split<2, 2>, g, blk, 0, s, a); break;
-        case 2 * 8 + 4: launch(k_bwd_split<2, 4>, g, blk, 0, s, a); break;
-        case 4 * 8 + 1: launch(k_bwd_split<4, 1>, g, blk, 0, s, a); break;
-        case 4 * 8 + 2: launch(k_bwd_split<4, 2>, g, blk, 0, s, a); break;
-        default: launch(k_bwd_split<4, 4>, g, blk, 0, s, a); break;
-        }
+        a.weighted ? launch_split<true>(a, g, blk, s) : launch_split<false>(a, g, blk, s);
     } else {
         switch (a.seg) {
         case 1: launch(k_move_rows<1>, g, blk, 0, s, a); break;
@@ -1719,13 +1797,13 @@ hipError_t launch_route_move_tiny(const RowArgs &a, const RouteArgs &r, hipStrea
     return hipGetLastError();
 }
 
-template <bool F32, bool GW>
+template <bool F32, bool GW, bool WT = false>
 static void launch_comb(int seg, dim3 g, const CombineArgs &a, hipStream_t s)
 {
     switch (seg) {
-    case 1: launch(k_combine<1, F32, GW>, g, dim3(kRowThreads), 0, s, a); break;
-    case 2: launch(k_combine<2, F32, GW>, g, dim3(kRowThreads), 0, s, a); break;
-    default: launch(k_combine<4, F32, GW>, g, dim3(kRowThreads), 0, s, a); break;
+    case 1: launch(k_combine<1, F32, GW, WT>, g, dim3(kRowThreads), 0, s, a); break;
+    case 2: launch(k_combine<2, F32, GW, WT>, g, dim3(kRowThreads), 0, s, a); break;
+    default: launch(k_combine<4, F32, GW, WT>, g, dim3(kRowThreads), 0, s, a); break;
     }
 }
 
@@ -1742,7 +1820,9 @@ hipError_t launch_combine(const CombineArgs &a, hipStream_t s)
         return hipErrorInvalidConfiguration;
     const dim3 g(static_cast<unsigned>(nb));
     const bool gw = a.grad_w != nullptr;
-    if (a.out_f32)
+    if (a.topk_w)
+        a.out_f32 ? launch_comb<true, false, true>(seg, g, a, s) : launch_comb<false, false, true>(seg, g, a, s);
+    else if (a.out_f32)
         gw ? launch_comb<true, true>(seg, g, a, s) : launch_comb<true, false>(seg, g, a, s);
     else
         gw ? launch_comb<false, true>(seg, g, a, s) : launch_comb<false, false>(seg, g, a, s);

@@ -26,6 +26,17 @@ step runs in the HIP library:
   combine(Y, <handle tensors>, num_experts, local_begin, pad_multiple,
           capacity) -> out [T,H] bf16
       backward: combine_bwd (moe_combine_bwd, the cached dispatch of grad_out)
+  combine_weighted(Y, topk_w, <handle tensors>, num_experts, local_begin,
+                   pad_multiple, capacity) -> out [T,H] bf16
+      every row enters with its routing weight; backward: combine_weighted_bwd
+      (moe_combine_weighted_bwd) -> (grad_rows, grad_topk_w)
+  expert_gemm_fp8(rows_q, row_scale, w_q, w_scale, <handle tensors>,
+                  num_experts, local_begin, pad_multiple, capacity)
+      -> out [R,N] bf16: every expert's E4M3 rows times its E4M3 weights
+  expert_swiglu_fp8(same arguments)
+      -> (h_q [R,I] float8_e4m3fn, h_scale [R,I/128]): silu(gate) * up,
+      requantized for a following expert_gemm_fp8; neither has autograd (the
+      rows are codes).  Their rows past the routed total are not written.
 
 <handle tensors> = routing_map, tokens_per_expert, padded_offsets, row_of_slot,
 status, workspace, in that order.  The workspace carries the route's row list
@@ -33,7 +44,8 @@ status, workspace, in that order.  The workspace carries the route's row list
 of the tokens.  The handle fields the ops need but do not carry (T, k, the
 number of local experts) are read off the tensors' shapes.
 
-``moe_layer`` strings the ops together around a caller-supplied expert.
+``moe_layer`` strings the ops together around a caller-supplied expert;
+``moe_layer_fp8`` is the FP8 layer for serving, dispatch to combine.
 """
 from __future__ import annotations
 
@@ -268,6 +280,112 @@ combine.register_autograd(_combine_backward, setup_context=_combine_setup)
 
 
 # ---------------------------------------------------------------------------
+# weighted combine, with autograd through moe_combine_weighted_bwd
+# ---------------------------------------------------------------------------
+@torch.library.custom_op(f"{_NS}::combine_weighted", mutates_args=())
+def combine_weighted(Y: torch.Tensor, topk_w: torch.Tensor, routing_map: torch.Tensor,
+                     tokens_per_expert: torch.Tensor, padded_offsets: torch.Tensor,
+                     row_of_slot: torch.Tensor, status: torch.Tensor, workspace: torch.Tensor,
+                     num_experts: int, local_begin: int, pad_multiple: int, capacity: int
+                     ) -> torch.Tensor:
+    desc, h = _rebuild(routing_map, tokens_per_expert, padded_offsets, row_of_slot, status,
+                       workspace, num_experts, local_begin, pad_multiple, capacity)
+    R, H = Y.shape
+    out = Y.new_empty((row_of_slot.shape[0], H))
+    B.moe_combine_weighted(desc, h, Y.contiguous(), H, R, topk_w.contiguous(), out)
+    return out
+
+
+@combine_weighted.register_fake
+def _(Y, topk_w, routing_map, tokens_per_expert, padded_offsets, row_of_slot, status, workspace,
+      num_experts, local_begin, pad_multiple, capacity):
+    return Y.new_empty((row_of_slot.shape[0], Y.shape[1]))
+
+
+@torch.library.custom_op(f"{_NS}::combine_weighted_bwd", mutates_args=())
+def combine_weighted_bwd(grad_out: torch.Tensor, Y: torch.Tensor, topk_w: torch.Tensor,
+                         routing_map: torch.Tensor, tokens_per_expert: torch.Tensor,
+                         padded_offsets: torch.Tensor, row_of_slot: torch.Tensor,
+                         status: torch.Tensor, workspace: torch.Tensor, num_experts: int,
+                         local_begin: int, pad_multiple: int, capacity: int
+                         ) -> tuple[torch.Tensor, torch.Tensor]:
+    desc, h = _rebuild(routing_map, tokens_per_expert, padded_offsets, row_of_slot, status,
+                       workspace, num_experts, local_begin, pad_multiple, capacity)
+    R, H = Y.shape
+    grad_rows = Y.new_empty((R, H))
+    dw = Y.new_empty(tuple(row_of_slot.shape), dtype=torch.float32)
+    B.moe_combine_weighted_bwd(desc, h, grad_out.contiguous(), Y.contiguous(), H, R,
+                               topk_w.contiguous(), grad_rows, dw)
+    return grad_rows, dw
+
+
+@combine_weighted_bwd.register_fake
+def _(grad_out, Y, topk_w, routing_map, tokens_per_expert, padded_offsets, row_of_slot, status,
+      workspace, num_experts, local_begin, pad_multiple, capacity):
+    return (Y.new_empty(tuple(Y.shape)),
+            Y.new_empty(tuple(row_of_slot.shape), dtype=torch.float32))
+
+
+def _combine_weighted_setup(ctx, inputs, output):
+    Y, topk_w, *handle, E, lb, P, cap = inputs
+    ctx.save_for_backward(Y, topk_w, *handle)
+    ctx.args = (E, lb, P, cap)
+
+
+def _combine_weighted_backward(ctx, grad_out):
+    Y, topk_w, *handle = ctx.saved_tensors
+    grad_rows, dw = combine_weighted_bwd(grad_out, Y, topk_w, *handle, *ctx.args)
+    return (grad_rows, dw) + (None,) * 10
+
+
+combine_weighted.register_autograd(_combine_weighted_backward,
+                                   setup_context=_combine_weighted_setup)
+
+
+# ---------------------------------------------------------------------------
+# the experts' products on E4M3 rows
+# ---------------------------------------------------------------------------
+@torch.library.custom_op(f"{_NS}::expert_gemm_fp8", mutates_args=())
+def expert_gemm_fp8(rows_q: torch.Tensor, row_scale: torch.Tensor, w_q: torch.Tensor,
+                    w_scale: torch.Tensor, routing_map: torch.Tensor,
+                    tokens_per_expert: torch.Tensor, padded_offsets: torch.Tensor,
+                    row_of_slot: torch.Tensor, status: torch.Tensor, workspace: torch.Tensor,
+                    num_experts: int, local_begin: int, pad_multiple: int, capacity: int
+                    ) -> torch.Tensor:
+    desc, h = _rebuild(routing_map, tokens_per_expert, padded_offsets, row_of_slot, status,
+                       workspace, num_experts, local_begin, pad_multiple, capacity)
+    return B.expert_gemm_fp8(desc, h, rows_q.contiguous(), row_scale.contiguous(),
+                             w_q.contiguous(), w_scale.contiguous())
+
+
+@expert_gemm_fp8.register_fake
+def _(rows_q, row_scale, w_q, w_scale, routing_map, tokens_per_expert, padded_offsets,
+      row_of_slot, status, workspace, num_experts, local_begin, pad_multiple, capacity):
+    return rows_q.new_empty((rows_q.shape[0], w_q.shape[1]), dtype=torch.bfloat16)
+
+
+@torch.library.custom_op(f"{_NS}::expert_swiglu_fp8", mutates_args=())
+def expert_swiglu_fp8(rows_q: torch.Tensor, row_scale: torch.Tensor, w_q: torch.Tensor,
+                      w_scale: torch.Tensor, routing_map: torch.Tensor,
+                      tokens_per_expert: torch.Tensor, padded_offsets: torch.Tensor,
+                      row_of_slot: torch.Tensor, status: torch.Tensor, workspace: torch.Tensor,
+                      num_experts: int, local_begin: int, pad_multiple: int, capacity: int
+                      ) -> tuple[torch.Tensor, torch.Tensor]:
+    desc, h = _rebuild(routing_map, tokens_per_expert, padded_offsets, row_of_slot, status,
+                       workspace, num_experts, local_begin, pad_multiple, capacity)
+    return B.expert_swiglu_fp8(desc, h, rows_q.contiguous(), row_scale.contiguous(),
+                               w_q.contiguous(), w_scale.contiguous())
+
+
+@expert_swiglu_fp8.register_fake
+def _(rows_q, row_scale, w_q, w_scale, routing_map, tokens_per_expert, padded_offsets,
+      row_of_slot, status, workspace, num_experts, local_begin, pad_multiple, capacity):
+    R, I = rows_q.shape[0], w_q.shape[1] // 2
+    return (rows_q.new_empty((R, I), dtype=torch.float8_e4m3fn),
+            rows_q.new_empty((R, I // 128), dtype=torch.float32))
+
+
+# ---------------------------------------------------------------------------
 # a whole expert-parallel layer on one GPU's share
 # ---------------------------------------------------------------------------
 def moe_layer(x, topk_idx, topk_w, experts, num_experts, local_begin=0, num_local=None,
@@ -285,3 +403,21 @@ def moe_layer(x, topk_idx, topk_w, experts, num_experts, local_begin=0, num_loca
                                           pad_multiple, capacity, R)
     Y = experts(rows, row_w, row_expert)
     return combine(Y, *handle, num_experts, local_begin, pad_multiple, capacity)
+
+
+def moe_layer_fp8(x, topk_idx, topk_w, w1_q, w1_scale, w2_q, w2_scale, num_experts, local_begin=0,
+                  pad_multiple=1, capacity=0):
+    """The layer with SwiGLU experts on E4M3 rows and weights: route, FP8 dispatch, gate/up product
+    with its activation and requantization, down product, weighted combine.
+
+    x [T,H] bf16; w1_q [EL,2I,H] (gate rows first) and w2_q [EL,H,I] E4M3 codes with one fp32 scale
+    per 128 x 128 block (w1_scale [EL,2I/128,H/128], w2_scale [EL,ceil(H/128),I/128]).  For serving:
+    no autograd (the rows are codes).  capacity as for moe_layer."""
+    num_local = w1_q.shape[0]
+    *handle, host = route(topk_idx, num_experts, local_begin, num_local, pad_multiple, capacity)
+    R = capacity if capacity > 0 else int(host[0])
+    where = (*handle, num_experts, local_begin, pad_multiple, capacity)
+    rows_q, row_scale, *_ = dispatch_fp8(x, topk_w, *where, R)
+    h_q, h_scale = expert_swiglu_fp8(rows_q, row_scale, w1_q, w1_scale, *where)
+    Y = expert_gemm_fp8(h_q, h_scale, w2_q, w2_scale, *where)
+    return combine_weighted(Y, topk_w, *where)

@@ -1,0 +1,342 @@
+"""GPU: the experts' products on E4M3 rows (moe_expert_gemm_fp8, moe_expert_swiglu_fp8) against
+64-bit references, at group sizes around the kernels' tiles, empty groups, odd column counts, one
+token and none, eager and sync-free; rows past the total left as they were; NaN rows kept to
+themselves; a side stream, graph replays and the FP8 layer made of them."""
+import pytest
+import torch
+
+import expert_ref as ref
+from combine_topk_idx_multihot_amd import binding as B
+from combine_topk_idx_multihot_amd import ops
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    B.moe_device_check(0)
+    yield
+
+
+class Layer:
+    """A routed layer whose expert e has counts[e] tokens (top-1), or random top-k routing."""
+
+    def __init__(self, K, counts=None, T=0, E=0, k=1, lb=0, EL=None, P=1, sync_free=False, seed=0,
+                 empty=0.0, extra=0):
+        g = self.g = torch.Generator(device="cuda").manual_seed(seed)
+        if counts is not None:
+            E = len(counts)
+            idx = torch.repeat_interleave(torch.arange(E), torch.tensor(counts))
+            T, k = len(idx), 1
+            idx = idx[torch.randperm(T, generator=torch.Generator().manual_seed(seed))].view(T, 1)
+        else:
+            cpu = torch.Generator().manual_seed(seed)
+            idx = torch.rand((T, E), generator=cpu).topk(k, 1).indices
+            idx[torch.rand((T, k), generator=cpu) < empty] = -1
+        EL = E if EL is None else EL
+        d = B.make_desc(T, k, E, lb, EL, P)
+        if sync_free:
+            d = B.make_desc(T, k, E, lb, EL, P, B.MOE_SYNC_FREE, False,
+                            B.moe_capacity_min(d) + extra)
+        self.d, self.K, self.EL = d, K, EL
+        self.h, _ = B.route(d, idx.to(torch.int32).cuda())
+        self.off = self.h.padded_offsets.tolist()
+        self.total = self.off[-1]
+        self.R = B.rows_for(d, self.h)
+        # E4M3 rows of tokens; the rows past the total hold NaN codes and NaN scales, which
+        # nothing may read into a result
+        x = torch.randn((max(T, 1), K), generator=g, device="cuda")
+        x = x * torch.exp(torch.randn(K, generator=g, device="cuda"))
+        q, s = ref.quant_rows(x)
+        self.rows_q = torch.full((self.R, K), 0x7F, dtype=torch.uint8, device="cuda")
+        self.row_scale = torch.full((self.R, K // 128), float("nan"), device="cuda")
+        tpe = self.h.tokens_per_expert.tolist()
+        for e in range(EL):
+            r0, n = self.off[e], tpe[e]
+            pick = torch.randint(0, max(T, 1), (n,), generator=g, device="cuda")
+            self.rows_q[r0:r0 + n] = q.view(torch.uint8)[pick]
+            self.row_scale[r0:r0 + n] = s[pick]
+            self.rows_q[r0 + n:self.off[e + 1]] = 0
+            self.row_scale[r0 + n:self.off[e + 1]] = 0
+        self.rows_q = self.rows_q.view(torch.float8_e4m3fn)
+
+    def exact(self, w_q, w_scale):
+        return ref.product(self.rows_q, self.row_scale, w_q, w_scale, self.off)
+
+
+def fill(shape, dtype):
+    """A buffer of a value no result has, to see what a call leaves."""
+    if dtype == torch.float8_e4m3fn:
+        return torch.full(shape, 0x55, dtype=torch.uint8, device="cuda").view(dtype)
+    return torch.full(shape, -12345.0, dtype=dtype, device="cuda")
+
+
+def untouched(t, r):
+    t = t[r:]
+    return bool((t.view(torch.uint8) == 0x55).all() if t.dtype == torch.float8_e4m3fn
+                else (t == torch.tensor(-12345.0, dtype=t.dtype)).all())
+
+
+def check_gemm(L, w_q, w_scale, what):
+    N = w_q.shape[1]
+    out = fill((L.R + 3, N), torch.bfloat16)
+    B.moe_expert_gemm_fp8(L.d, L.h, L.rows_q, L.row_scale, L.K, L.R, w_q, w_scale, N, out)
+    torch.cuda.synchronize()
+    ref.check_bf16(out[:L.total], *L.exact(w_q, w_scale), what)
+    assert untouched(out, L.total), what
+
+
+def check_swiglu(L, w_q, w_scale, fp8, what):
+    I = w_q.shape[1] // 2
+    out = fill((L.R + 3, I), torch.float8_e4m3fn if fp8 else torch.bfloat16)
+    sc = fill((L.R + 3, I // 128), torch.float32) if fp8 else None
+    B.moe_expert_swiglu_fp8(L.d, L.h, L.rows_q, L.row_scale, L.K, L.R, w_q, w_scale, I, out, sc)
+    torch.cuda.synchronize()
+    h, err = ref.swiglu(*L.exact(w_q, w_scale))
+    if fp8:
+        ref.check_fp8(out[:L.total], sc[:L.total], h, err, what)
+        assert untouched(sc, L.total), what
+    else:
+        ref.check_bf16(out[:L.total], h, err, what)
+    assert untouched(out, L.total), what
+    return out, sc
+
+
+# group sizes around 16, 32, 64, 128 and 256 rows, with few and with many rows per expert on average
+EDGES = [0, 1, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 0, 300]
+LAYERS = {
+    "edges": dict(counts=EDGES),
+    "edges_padded": dict(counts=EDGES, P=16),
+    "edges_few_per_expert": dict(counts=EDGES + [0] * 110),
+    "edges_middle": dict(counts=EDGES + [0] * 22, P=3),
+    "large_groups": dict(counts=[511, 0, 513, 700, 1]),
+    "one_group": dict(counts=[1000]),
+    "one_token": dict(T=1, E=128, k=8, sync_free=True, extra=5),
+    "two_tokens": dict(T=2, E=4, k=4),
+    "decode": dict(T=77, E=32, k=4, sync_free=True, P=8, empty=0.2),
+    "share": dict(T=700, E=32, k=8, lb=5, EL=7, sync_free=True, extra=100),
+    "single_local": dict(T=90, E=16, k=3, lb=15, EL=1),
+    "many_experts": dict(T=300, E=1024, k=6, lb=1, EL=1000, P=2),
+}
+SHAPES = [(128, 8), (256, 136), (384, 512), (768, 200), (2048, 264)]
+
+
+@pytest.mark.parametrize("K,N", SHAPES)
+@pytest.mark.parametrize("name", LAYERS)
+def test_gemm(name, K, N):
+    L = Layer(K, seed=K + N, **LAYERS[name])
+    if name == "many_experts" and K * N > 200_000:
+        K, N = 256, 136
+        L = Layer(K, seed=K + N, **LAYERS[name])
+    w = ref.make_weights(L.EL, N, K, L.g)
+    check_gemm(L, *w, f"{name} {K} {N}")
+
+
+@pytest.mark.parametrize("K,I", [(128, 128), (640, 256), (2048, 384)])
+@pytest.mark.parametrize("name", LAYERS)
+def test_swiglu(name, K, I):
+    if name == "many_experts":
+        K, I = min(K, 256), min(I, 128)
+    L = Layer(K, seed=K + I, **LAYERS[name])
+    w = ref.make_weights(L.EL, 2 * I, K, L.g)
+    check_swiglu(L, *w, True, f"{name} {K} {I} fp8")
+    check_swiglu(L, *w, False, f"{name} {K} {I} bf16")
+
+
+def test_swiglu_saturated_gates():
+    """Gates far on both sides: silu(g) -> g and -> 0; a row whose h is 0 takes the floor scale."""
+    L = Layer(256, counts=[40, 3])
+    w_q, w_s = ref.make_weights(2, 256, 256, L.g)
+    w_s[0] *= 30.0
+    w_q[1, 128:] = 0.0
+    out, sc = check_swiglu(L, w_q, w_s, True, "saturated")
+    assert (out[40:43].float() == 0).all() and (sc[40:43] == torch.tensor(1e-4) / 448.0).all()
+    check_swiglu(L, w_q, w_s, False, "saturated bf16")
+
+
+@pytest.mark.parametrize("counts", [[5, 9, 0], [200, 300, 0], [1200, 600]])
+def test_nan_row_stays_alone(counts):
+    L = Layer(256, counts=counts)
+    w = ref.make_weights(L.EL, 256, 256, L.g)
+    clean = B.expert_gemm_fp8(L.d, L.h, L.rows_q, L.row_scale, *w)
+    h_clean, _ = B.expert_swiglu_fp8(L.d, L.h, L.rows_q, L.row_scale, *w, torch.bfloat16)
+    bad = L.rows_q.clone()
+    bad.view(torch.uint8)[3, 7] = 0x7F
+    scale = L.row_scale.clone()
+    scale[counts[0] + 1, 1] = float("inf")
+    y = B.expert_gemm_fp8(L.d, L.h, bad, scale, *w)
+    h, _ = B.expert_swiglu_fp8(L.d, L.h, bad, scale, *w, torch.bfloat16)
+    keep = torch.ones(L.total, dtype=torch.bool, device="cuda")
+    keep[[3, counts[0] + 1]] = False
+    assert torch.equal(y[keep], clean[keep]) and torch.equal(h[keep], h_clean[keep])
+    assert torch.isnan(y[3]).all() and not torch.isfinite(y[counts[0] + 1]).any()
+
+
+def test_repeats_and_prepared_give_equal_bits():
+    L = Layer(768, T=1500, E=16, k=2, P=16)
+    w = ref.make_weights(16, 512, 768, L.g)
+    a = B.expert_gemm_fp8(L.d, L.h, L.rows_q, L.row_scale, *w)
+    out = torch.empty_like(a)
+    call = B.PreparedExpertGemmFp8(L.d, L.h, L.rows_q, L.row_scale, 768, *w, 512, out)
+    for _ in range(3):
+        out.fill_(7.0)
+        call(L.R)
+        assert torch.equal(out, a)
+    q, s = B.expert_swiglu_fp8(L.d, L.h, L.rows_q, L.row_scale, *w)
+    q2, s2 = torch.empty_like(q), torch.empty_like(s)
+    B.PreparedExpertSwigluFp8(L.d, L.h, L.rows_q, L.row_scale, 768, *w, 256, q2, s2)(L.R)
+    assert torch.equal(q2.view(torch.uint8), q.view(torch.uint8)) and torch.equal(s2, s)
+
+
+def test_eager_fewer_rows_than_routed():
+    """R below the device's total: only rows [0, R) are computed and the mismatch is flagged."""
+    L = Layer(256, counts=[30, 50, 20])
+    w = ref.make_weights(3, 128, 256, L.g)
+    out = fill((L.R, 128), torch.bfloat16)
+    R = 61
+    B.moe_expert_gemm_fp8(L.d, L.h, L.rows_q, L.row_scale, 256, R, *w, 128, out)
+    y, bound = L.exact(*w)
+    ref.check_bf16(out[:R], y[:R], bound[:R], "short")
+    assert untouched(out, R)
+    assert int(L.h.status[1]) & B.MOE_FLAG_ROWS_MISMATCH
+
+
+def test_no_tokens_and_no_rows():
+    d = B.make_desc(0, 2, 4)
+    h, _ = B.route(d, torch.empty((0, 2), dtype=torch.int32, device="cuda"))
+    w_q, w_s = ref.make_weights(4, 256, 128, torch.Generator(device="cuda"))
+    e8 = torch.empty((0, 128), dtype=torch.float8_e4m3fn, device="cuda")
+    es = torch.empty((0, 1), device="cuda")
+    assert B.expert_gemm_fp8(d, h, e8, es, w_q, w_s).shape == (0, 256)
+    assert B.expert_swiglu_fp8(d, h, e8, es, w_q, w_s)[0].shape == (0, 128)
+    L = Layer(128, T=50, E=4, k=2, sync_free=True, empty=1.1)  # every slot empty
+    assert L.total == 0 and L.R > 0
+    check_empty = fill((L.R, 256), torch.bfloat16)
+    B.moe_expert_gemm_fp8(L.d, L.h, L.rows_q, L.row_scale, 128, L.R, w_q, w_s, 256, check_empty)
+    assert untouched(check_empty, 0)
+
+
+def test_dgrad_is_the_product_with_transposed_weights():
+    L = Layer(384, counts=[70, 10], seed=3)
+    w_q, w_s = ref.make_weights(2, 384, 256, L.g)  # forward [N=384, K=256]; rows are dY [R, 384]
+    wt, st = w_q.view(torch.uint8).transpose(1, 2).contiguous().view(torch.float8_e4m3fn), w_s.transpose(1, 2).contiguous()
+    dx = B.expert_gemm_fp8(L.d, L.h, L.rows_q, L.row_scale, wt, st)
+    _, bound = L.exact(wt, st)
+    b = torch.arange(384, device="cuda") // 128
+    for e in range(2):
+        r = slice(L.off[e], L.off[e + 1])
+        dy = L.rows_q[r].double() * L.row_scale[r].double()[:, b]
+        w = w_q[e].double() * w_s[e].double()[b][:, torch.arange(256, device="cuda") // 128]
+        ref.check_bf16(dx[r], dy @ w, bound[r], "dgrad")
+
+
+def fp8_layer_inputs(T, H, I, E, EL, k, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((T, H), generator=g, device="cuda").to(torch.bfloat16)
+    idx = torch.rand((T, E), generator=g, device="cuda").topk(k, 1).indices.to(torch.int32)
+    idx[torch.rand((T, k), generator=g, device="cuda") < 0.1] = -1
+    w = torch.rand((T, k), generator=g, device="cuda")
+    return (x, idx, w, *ref.make_weights(EL, 2 * I, H, g), *ref.make_weights(EL, H, I, g))
+
+
+@pytest.mark.parametrize("T,k,capacity", [(300, 4, 0), (300, 4, 1500), (1, 8, 64), (40, 2, 0)])
+def test_fp8_layer(T, k, capacity):
+    """ops.moe_layer_fp8: the calls it is made of, each step held to its reference."""
+    H, I, E, lb, EL, P = 512, 256, 16, 2, 12, 4
+    x, idx, w, w1, s1, w2, s2 = fp8_layer_inputs(T, H, I, E, EL, k, T + k)
+    out = ops.moe_layer_fp8(x, idx, w, w1, s1, w2, s2, E, lb, P, capacity)
+    d = B.make_desc(T, k, E, lb, EL, P, B.MOE_SYNC_FREE if capacity else B.MOE_EAGER, False,
+                    capacity)
+    h, _ = B.route(d, idx)
+    rows_q, row_scale, *_ = B.dispatch_fp8(d, h, x)
+    off = h.padded_offsets.tolist()
+    n = off[-1]
+    hq, hs = B.expert_swiglu_fp8(d, h, rows_q, row_scale, w1, s1)
+    ref.check_fp8(hq[:n], hs[:n], *ref.swiglu(*ref.product(rows_q, row_scale, w1, s1, off)), "h")
+    Y = B.expert_gemm_fp8(d, h, hq, hs, w2, s2)
+    ref.check_bf16(Y[:n], *ref.product(hq, hs, w2, s2, off), "Y")
+    assert torch.equal(out, B.combine_weighted(d, h, Y, w))
+    ros = h.row_of_slot.long()
+    y = Y.double()[ros.clamp_min(0)] * torch.where(ros >= 0, w, torch.zeros_like(w)).double()[:, :, None]
+    y[ros < 0] = 0
+    ref.check_bf16(out, y.sum(1), k * ref.U * y.abs().sum(1), "out")
+
+
+def test_fp8_layer_no_rows():
+    x, idx, w, *weights = fp8_layer_inputs(9, 256, 128, 8, 4, 2, 1)
+    idx.fill_(-1)
+    for capacity in (0, 40):
+        assert (ops.moe_layer_fp8(x, idx, w, *weights, 8, 0, 1, capacity) == 0).all()
+
+
+def test_fp8_layer_graph_replays():
+    """The sync-free layer captured once and replayed on new inputs, eager work in between."""
+    T, H, I, E, k, C = 64, 512, 256, 16, 4, 64 * 4 + 16
+    x, idx, w, *weights = fp8_layer_inputs(T, H, I, E, E, k, 5)
+    run = lambda: ops.moe_layer_fp8(x, idx, w, *weights, E, 0, 2, C)  # noqa: E731
+    run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for seed in range(4):
+        x2, idx2, w2, *_ = fp8_layer_inputs(T, H, I, E, E, k, 50 + seed)
+        x.copy_(x2), idx.copy_(idx2), w.copy_(w2)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        assert torch.equal(got, run()), seed
+
+
+def test_side_stream():
+    L = Layer(256, T=500, E=8, k=2)
+    w = ref.make_weights(8, 256, 256, L.g)
+    want = B.expert_gemm_fp8(L.d, L.h, L.rows_q, L.row_scale, *w)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = torch.empty_like(want)
+    out2 = torch.empty_like(want)
+    B.moe_expert_gemm_fp8(L.d, L.h, L.rows_q, L.row_scale, 256, L.R, *w, 256, out, stream=s)
+    B.moe_expert_gemm_fp8(L.d, L.h, L.rows_q, L.row_scale, 256, L.R, *w, 256, out2)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(out2, want)
+
+
+def test_torch_ops_check():
+    L = Layer(256, T=30, E=4, k=2)
+    h = L.h
+    where = (h.routing_map, h.tokens_per_expert, h.padded_offsets, h.row_of_slot, h.status,
+             h.workspace, 4, 0, 1, 0)
+    w = ref.make_weights(4, 256, 256, L.g)
+    utils = ("test_faketensor",)  # the schema check multiplies its inputs, which torch has not for E4M3
+    torch.library.opcheck(ops.expert_gemm_fp8, (L.rows_q, L.row_scale, *w, *where),
+                          test_utils=utils)
+    torch.library.opcheck(ops.expert_swiglu_fp8, (L.rows_q, L.row_scale, *w, *where),
+                          test_utils=utils)
+
+
+def test_rows_past_four_gib():
+    """Row and weight offsets past 2^32 bytes: the last rows of a 5 GiB row array and the last
+    expert's weights."""
+    K, N = 4096, 128
+    R = (5 << 30) // K
+    d = B.make_desc(R, 1, 3)
+    idx = torch.repeat_interleave(torch.tensor([0, 2], dtype=torch.int32), torch.tensor([R - 40, 40]))
+    h, _ = B.route(d, idx.view(R, 1).cuda())
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rows = torch.zeros((R, K), dtype=torch.uint8, device="cuda")
+    scale = torch.zeros((R, K // 128), device="cuda")
+    pick = torch.tensor([0, 1, R // 2, R - 41, R - 40, R - 1], device="cuda")
+    q, s = ref.quant_rows(torch.randn((6, K), generator=g, device="cuda"))
+    rows[pick], scale[pick] = q.view(torch.uint8), s
+    w = ref.make_weights(3, N, K, g)
+    out = B.expert_gemm_fp8(d, h, rows.view(torch.float8_e4m3fn), scale, *w)
+    ref.check_bf16(out[pick], *ref.product(q, s, *w, [0, 4, 4, 6]), "far rows")
+    out[pick] = 0
+    assert not out.any()
