@@ -266,8 +266,8 @@ int check_product(const moe_desc *desc, const moe_handle *handle, const uint8_t 
         return rc;
     if ((rc = check_rows(desc, R)) != MOE_OK)
         return rc;
-    if (K <= 0 || K % 128 != 0)
-        return fail(MOE_ERR_ARG, "K must be a positive multiple of 128 (got %d)", K);
+    if (K <= 0 || K % 128 != 0 || K > (1 << 23))
+        return fail(MOE_ERR_ARG, "K must be a positive multiple of 128 up to 2^23 (got %d)", K);
     if (R > 0 && (!rows_q || !aligned16(rows_q)))
         return fail(MOE_ERR_ARG, "rows_q must be a non-NULL, 16-byte aligned [R,K] byte tensor");
     if (R > 0 && (!row_scale || !aligned16(row_scale)))

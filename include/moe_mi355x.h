@@ -367,7 +367,8 @@ int moe_combine_weighted_bwd(const moe_desc *desc, const moe_handle *handle,
  * local expert e's group, padded_offsets[e] <= r < padded_offsets[e+1], gets
  *   out[r,n] = sum over k of (rows_q[r,k] * row_scale[r,k/128])
  *                          * (w_q[e,n,k] * w_scale[e,n/128,k/128]).
- *   rows_q      device [R,K] uint8 E4M3 codes, K a positive multiple of 128.
+ *   rows_q      device [R,K] uint8 E4M3 codes, K a positive multiple of 128
+ *               (at most 2^23).
  *   row_scale   device [R,K/128] fp32.
  *   w_q         device [EL,N,K] uint8 E4M3 codes, N a positive multiple of 8.
  *   w_scale     device [EL,ceil(N/128),K/128] fp32: one scale per block of 128

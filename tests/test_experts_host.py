@@ -77,7 +77,7 @@ def test_weights_are_required():
     assert combine_bwd(w=None) == B.MOE_ERR_ARG and combine_bwd(dw=None) == B.MOE_ERR_ARG
 
 
-@pytest.mark.parametrize("K", [0, -128, 64, 200])
+@pytest.mark.parametrize("K", [0, -128, 64, 200, (1 << 23) + 128])
 def test_product_depth(K):
     assert gemm(K=K) == B.MOE_ERR_ARG and swiglu(K=K) == B.MOE_ERR_ARG
     assert "128" in B.last_error()
