@@ -296,6 +296,8 @@ moe::ExpertArgs product_args(const moe_desc *desc, const moe_handle *handle, con
     a.R = R;
     const int64_t worst = cap_min(desc);
     a.rows_max = R < worst ? R : worst;
+    const int64_t P = desc->pad_multiple, group = (desc->T + P - 1) / P * P; // a row per token at most
+    a.group_max = group < a.rows_max ? group : a.rows_max;
     a.rows_mean = (desc->T * desc->k + desc->E - 1) / desc->E;
     a.K = K;
     a.EL = desc->num_local;

@@ -42,13 +42,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float x, float y)
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
-// c + a * b^T over 128 columns: a and b hold 16 rows each, lane l the row
-// l % 16 and a quarter of its columns (any quarter, the same one in both).
-__device__ __forceinline__ f32x4 mfma128(const i32x8 &a, const i32x8 &b, const f32x4 &c)
-{
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
-}
-
 __device__ __forceinline__ i32x8 join(const u32x4 &lo, const u32x4 &hi)
 {
     i32x8 v;
@@ -58,15 +51,6 @@ __device__ __forceinline__ i32x8 join(const u32x4 &lo, const u32x4 &hi)
         v[4 + i] = static_cast<int>(hi[i]);
     }
     return v;
-}
-
-// A lane's quarter of 128 columns at p: 16 bytes of each 64-byte half, so
-// that the four lanes of a row read whole 64-byte runs.
-__device__ __forceinline__ i32x8 load_quarter(const uint8_t *p, int quarter)
-{
-    const u32x4 lo = *reinterpret_cast<const u32x4 *>(p + quarter * 16);
-    const u32x4 hi = *reinterpret_cast<const u32x4 *>(p + 64 + quarter * 16);
-    return join(lo, hi);
 }
 
 // The tile of rows and output columns that a workgroup computes.
@@ -80,76 +64,6 @@ struct Tile {
 __device__ __forceinline__ int64_t group_begin(const ExpertArgs &a, int e)
 {
     return max<int64_t>(0, min<int64_t>(a.off[e], a.R));
-}
-
-// Tile number `id` of the list: experts in order, within one the row tiles in
-// groups of 8, within a group the column tiles with the row tiles of each side
-// by side (they read the same weights, and the next column tile the same rows).  The
-// group sizes are on the device only, so the grid covers the most tiles that
-// R rows can make and workgroups past the real count find none.  Consecutive
-// workgroups run on different XCDs; each XCD takes a run of consecutive tiles
-// of its own, so that its L2 holds what they share.  Every wave computes this
-// by itself: a lane sums the tiles of EL / 64 experts, a wave scan follows.
-template <int BM>
-__device__ __forceinline__ Tile find_tile(const ExpertArgs &a, int64_t bid)
-{
-    const int lane = threadIdx.x & (kWave - 1);
-    const int per = (a.EL + kWave - 1) / kWave;
-    const int e0 = min(a.EL, lane * per), e1 = min(a.EL, e0 + per);
-    int64_t mine = 0;
-    for (int e = e0; e < e1; ++e) {
-        const int64_t lo = group_begin(a, e), hi = max(lo, group_begin(a, e + 1));
-        mine += (hi - lo + BM - 1) / BM;
-    }
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-        const int64_t v = __shfl_up(incl, o);
-        if (lane >= o)
-            incl += v;
-    }
-    const int64_t total = __shfl(incl, kWave - 1) * a.ntn;
-    Tile t = {-1, 0, 0, 0};
-    const int64_t chunk = (total + kXcds - 1) / kXcds;
-    const int64_t pos = bid / kXcds;
-    const int64_t id = (bid % kXcds) * chunk + pos;
-    if (pos >= chunk || id >= total)
-        return t;
-    const uint64_t m = __ballot(incl * a.ntn > id);
-    const int src = __builtin_ctzll(m); // total > id: some lane holds it
-    int64_t rest = id - __shfl(incl - mine, src) * a.ntn;
-    int e = min(a.EL, src * per);
-    const int eend = min(a.EL, e + per);
-    for (; e < eend; ++e) {
-        const int64_t lo = group_begin(a, e), hi = max(lo, group_begin(a, e + 1));
-        const int64_t mt = (hi - lo + BM - 1) / BM;
-        if (rest < mt * a.ntn) {
-            const int64_t grp = rest / (8 * a.ntn);
-            const int64_t gm = min<int64_t>(8, mt - 8 * grp);
-            rest -= grp * 8 * a.ntn;
-            const int64_t ni = rest / gm;
-            t.e = e;
-            t.ni = static_cast<int>(ni);
-            t.r0 = lo + (8 * grp + rest - ni * gm) * BM;
-            t.rows = static_cast<int>(min<int64_t>(BM, hi - t.r0));
-            break;
-        }
-        rest -= mt * a.ntn;
-    }
-    return t;
-}
-
-// The tile in scalar registers: it is the same in every lane, which the
-// compiler cannot see (R, and so a row, fits 31 bits).
-template <int BM>
-__device__ __forceinline__ Tile uniform_tile(const ExpertArgs &a)
-{
-    Tile t = find_tile<BM>(a, blockIdx.x);
-    t.e = __builtin_amdgcn_readfirstlane(t.e);
-    t.ni = __builtin_amdgcn_readfirstlane(t.ni);
-    t.r0 = __builtin_amdgcn_readfirstlane(static_cast<int>(t.r0));
-    t.rows = __builtin_amdgcn_readfirstlane(t.rows);
-    return t;
 }
 
 __device__ __forceinline__ void flag_mismatch(const ExpertArgs &a)
@@ -178,159 +92,114 @@ __device__ __forceinline__ int pack_e4m3(const f32x4 &h, float inv)
 }
 
 // ---------------------------------------------------------------------------
-// product, one wave per 16 output columns and 16 * MT rows
+// Products of a few tokens: a workgroup takes 32 output columns of one expert
+// that has rows, each of its kSplit waves every kSplit-th step of 128 columns,
+// from HBM to registers; the waves' sums are added in the order of the waves
+// through LDS.  16 rows at a time; more rows read the weights again, from L2.
+// What counts here is the time from the launch to the first and from the last
+// load, not their rate: 4.2 MB of weights in K = 512 columns each take 4.6 us,
+// where the kernels below, which first list their tiles, take 13.
 // ---------------------------------------------------------------------------
-constexpr int kProdWaves = 4;
+constexpr int kSplit = 4;
+constexpr int kRowsCols = 32;
 
-template <int MT>
-__global__ void __launch_bounds__(kProdWaves * kWave) k_expert_gemm(ExpertArgs a)
+// c + a * b^T over 128 columns: a and b hold 16 rows each, lane l the row
+// l % 16 and a quarter of its columns (any quarter, the same one in both).
+__device__ __forceinline__ f32x4 mfma128(const i32x8 &a, const i32x8 &b, const f32x4 &c)
 {
-    flag_mismatch(a);
-    const Tile t = uniform_tile<16 * MT>(a);
-    if (t.e < 0)
-        return;
-    const int lane = threadIdx.x & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int n0 = (t.ni * kProdWaves + wave) * 16;
-    if (n0 >= a.N)
-        return;
-    const int l16 = lane & 15, quarter = lane >> 4;
-    const int KB = a.K >> 7;
-    const uint8_t *__restrict__ w =
-        a.w + (static_cast<int64_t>(t.e) * a.N + min(n0 + l16, a.N - 1)) * a.K;
-    const float *__restrict__ sw =
-        a.sw + (static_cast<int64_t>(t.e) * a.NB + (n0 >> 7)) * KB;
-    const uint8_t *x[MT];
-    const float *sx[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int64_t r = t.r0 + min(m * 16 + l16, t.rows - 1);
-        x[m] = a.a + r * a.K;
-        sx[m] = a.sa + r * KB;
-    }
-    f32x4 acc[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-        acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int b = 0; b < KB; ++b) {
-        const i32x8 wf = load_quarter(w + b * 128, quarter);
-        const float swb = sw[b];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const i32x8 xf = load_quarter(x[m] + b * 128, quarter);
-            const float s = sx[m][b] * swb;
-            const f32x4 p = mfma128(wf, xf, f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                acc[m][i] = fmaf(p[i], s, acc[m][i]);
-        }
-    }
-    const int n = n0 + quarter * 4;
-    if (n >= a.N)
-        return;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int row = m * 16 + l16;
-        if (row >= t.rows)
-            continue;
-        const int64_t at = (t.r0 + row) * a.N + n;
-        const u32x2 v = {pack_bf16(acc[m][0], acc[m][1]), pack_bf16(acc[m][2], acc[m][3])};
-        *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) + at) = v;
-    }
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
 }
 
-// ---------------------------------------------------------------------------
-// gated product: a workgroup of 8 waves computes 128 columns of h, wave v the
-// gate and the up columns 16 v .. 16 v + 15 of them, so that each lane holds
-// both factors; the row's largest magnitude (for the E4M3 output) is the
-// maximum over the four lanes that share the row and, through LDS, the waves.
-// ---------------------------------------------------------------------------
-constexpr int kGatedWaves = 8;
-
-template <int MT, bool OUT_FP8>
-__global__ void __launch_bounds__(kGatedWaves * kWave) k_expert_swiglu(ExpertArgs a)
+// A lane's quarter of 128 columns at p: 16 bytes of each 64-byte half, so that
+// the four lanes of a row read 64 bytes together (a load's cost goes with the
+// cache lines that it touches).
+__device__ __forceinline__ i32x8 load_quarter(const uint8_t *p, int quarter)
 {
-    __shared__ float amax[kGatedWaves][16 * MT];
+    return join(*reinterpret_cast<const u32x4 *>(p + quarter * 16),
+                *reinterpret_cast<const u32x4 *>(p + 64 + quarter * 16));
+}
+
+// The local expert of the s-th group that has rows, -1 if there are not so many.
+__device__ __forceinline__ int nonempty_expert(const ExpertArgs &a, int s)
+{
+    const int lane = threadIdx.x & (kWave - 1);
+    for (int base = 0; base < a.EL; base += kWave) {
+        const int e = base + lane;
+        const bool some = e < a.EL && group_begin(a, e + 1) > group_begin(a, e);
+        const uint64_t m = __ballot(some);
+        const int n = __popcll(m);
+        if (s < n) {
+            const int rank = __popcll(m & ((1ull << lane) - 1));
+            return base + __builtin_ctzll(__ballot(some && rank == s));
+        }
+        s -= n;
+    }
+    return -1;
+}
+
+__global__ void __launch_bounds__(kSplit * kWave) k_expert_rows(ExpertArgs a)
+{
+    __shared__ f32x4 part[kSplit - 1][2][kWave];
     flag_mismatch(a);
-    const Tile t = uniform_tile<16 * MT>(a);
-    if (t.e < 0)
+    const int slot = blockIdx.x / a.ntn, ni = blockIdx.x - slot * a.ntn;
+    // as many slots as experts, or as rows where those are fewer
+    const int e = __builtin_amdgcn_readfirstlane(a.rows_max < a.EL ? nonempty_expert(a, slot) : slot);
+    if (e < 0)
+        return;
+    const int64_t r0 = group_begin(a, e), r1 = group_begin(a, e + 1);
+    if (r1 <= r0)
         return;
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int n0 = t.ni * 128 + wave * 16; // columns of h
     const int l16 = lane & 15, quarter = lane >> 4;
     const int KB = a.K >> 7;
-    const int64_t wrow = static_cast<int64_t>(t.e) * 2 * a.N + n0 + l16;
-    const uint8_t *__restrict__ wg = a.w + wrow * a.K;
-    const uint8_t *__restrict__ wu = a.w + (wrow + a.N) * a.K;
-    const float *__restrict__ sg = a.sw + (static_cast<int64_t>(t.e) * a.NB + t.ni) * KB;
-    const float *__restrict__ su = sg + static_cast<int64_t>(a.N >> 7) * KB;
-    const uint8_t *x[MT];
-    const float *sx[MT];
+    const int n0 = ni * kRowsCols;
+    const uint8_t *__restrict__ w[2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int64_t r = t.r0 + min(m * 16 + l16, t.rows - 1);
-        x[m] = a.a + r * a.K;
-        sx[m] = a.sa + r * KB;
-    }
-    f32x4 ag[MT], au[MT];
+    for (int j = 0; j < 2; ++j)
+        w[j] = a.w + (static_cast<int64_t>(e) * a.N + min(n0 + j * 16 + l16, a.N - 1)) * a.K;
+    const float *__restrict__ sw = a.sw + (static_cast<int64_t>(e) * a.NB + (n0 >> 7)) * KB;
+    for (int64_t r = r0; r < r1; r += 16) {
+        const int rows = static_cast<int>(min<int64_t>(16, r1 - r));
+        const int64_t mine = r + min(l16, rows - 1);
+        const uint8_t *__restrict__ x = a.a + mine * a.K;
+        const float *__restrict__ sx = a.sa + mine * KB;
+        f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        for (int b = wave; b < KB; b += kSplit) {
+            i32x8 wf[2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-        ag[m] = au[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int b = 0; b < KB; ++b) {
-        const i32x8 gf = load_quarter(wg + b * 128, quarter);
-        const i32x8 uf = load_quarter(wu + b * 128, quarter);
-        const float sgb = sg[b], sub = su[b];
+            for (int j = 0; j < 2; ++j)
+                wf[j] = load_quarter(w[j] + b * 128, quarter);
+            const i32x8 xf = load_quarter(x + b * 128, quarter);
+            const float f = sx[b] * sw[b];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const i32x8 xf = load_quarter(x[m] + b * 128, quarter);
-            const float s = sx[m][b];
-            const f32x4 pg = mfma128(gf, xf, f32x4{0.f, 0.f, 0.f, 0.f});
-            const f32x4 pu = mfma128(uf, xf, f32x4{0.f, 0.f, 0.f, 0.f});
+            for (int j = 0; j < 2; ++j) {
+                const f32x4 q = mfma128(wf[j], xf, f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                ag[m][i] = fmaf(pg[i], s * sgb, ag[m][i]);
-                au[m][i] = fmaf(pu[i], s * sub, au[m][i]);
+                for (int i = 0; i < 4; ++i)
+                    acc[j][i] = fmaf(q[i], f, acc[j][i]);
             }
         }
-    }
-    f32x4 h[MT];
+        if (wave > 0) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            h[m][i] = gated(ag[m][i], au[m][i]);
-    const int n = n0 + quarter * 4;
-    if (OUT_FP8) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            float v = fmaxf(fmaxf(fabsf(h[m][0]), fabsf(h[m][1])), fmaxf(fabsf(h[m][2]), fabsf(h[m][3])));
-            v = fmaxf(v, __shfl_xor(v, 16));
-            v = fmaxf(v, __shfl_xor(v, 32));
-            if (quarter == 0)
-                amax[wave][m * 16 + l16] = v;
+            for (int j = 0; j < 2; ++j)
+                part[wave - 1][j][lane] = acc[j];
         }
         __syncthreads();
-    }
+        if (wave == 0) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int row = m * 16 + l16;
-        if (row >= t.rows)
-            continue;
-        const int64_t r = t.r0 + row;
-        if (OUT_FP8) {
-            float v = kAmaxFloor;
+            for (int j = 0; j < 2; ++j) {
 #pragma unroll
-            for (int q = 0; q < kGatedWaves; ++q)
-                v = fmaxf(v, amax[q][row]);
-            const float inv = __fdiv_rn(kE4M3Max, v);
-            *reinterpret_cast<int *>(static_cast<uint8_t *>(a.out) + r * a.N + n) = pack_e4m3(h[m], inv);
-            if (wave == 0 && quarter == 0)
-                a.out_scale[r * (a.N >> 7) + t.ni] = __fdiv_rn(v, kE4M3Max);
-        } else {
-            const u32x2 q = {pack_bf16(h[m][0], h[m][1]), pack_bf16(h[m][2], h[m][3])};
-            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) + r * a.N + n) = q;
+                for (int p = 0; p < kSplit - 1; ++p)
+                    acc[j] += part[p][j][lane];
+                const u32x2 v = {pack_bf16(acc[j][0], acc[j][1]), pack_bf16(acc[j][2], acc[j][3])};
+                const int n = n0 + j * 16 + quarter * 4;
+                if (l16 < rows && n < a.N)
+                    *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) + (r + l16) * a.N + n) = v;
+            }
         }
+        if (r + 16 < r1)
+            __syncthreads(); // the sums are read: room for the next rows'
     }
 }
 
@@ -447,17 +316,21 @@ __device__ __forceinline__ f32x16 mfma64(const i32x8 &a, const i32x8 &b, const f
 // A value that is the same in every lane, in a scalar register.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// A group of g rows is cut into the fewest tiles, of equal height but for
-// rounding up to whole blocks of 64.
-__device__ __forceinline__ int row_tiles(int g) { return (g + kTileRows - 1) / kTileRows; }
+// A group of g rows is cut into the fewest tiles of up to BM rows, of equal
+// height but for rounding up to whole blocks of 64 (or BM).
+template <int BM>
+__device__ __forceinline__ int row_tiles(int g) { return (g + BM - 1) / BM; }
+template <int BM>
 __device__ __forceinline__ int tile_height(int g, int mt)
 {
-    return ((g + mt - 1) / mt + 63) / 64 * 64;
+    constexpr int kBlock = BM < 64 ? BM : 64;
+    return ((g + mt - 1) / mt + kBlock - 1) / kBlock * kBlock;
 }
 
 // Tables of the tile list, by wave 0: tiles (row tiles * column tiles) before
 // each expert, and the groups' first rows, clamped into [0, R].
-__device__ void tile_tables(const ExpertArgs &a)
+template <int BM>
+__device__ void tile_tables(const ExpertArgs &a, uint32_t pre, uint32_t off)
 {
     const int lane = threadIdx.x & (kWave - 1);
     const int per = (a.EL + kWave - 1) / kWave;
@@ -465,7 +338,7 @@ __device__ void tile_tables(const ExpertArgs &a)
     int mine = 0;
     for (int e = e0; e < e1; ++e) {
         const int lo = static_cast<int>(group_begin(a, e));
-        mine += row_tiles(max(0, static_cast<int>(group_begin(a, e + 1)) - lo)) * a.ntn;
+        mine += row_tiles<BM>(max(0, static_cast<int>(group_begin(a, e + 1)) - lo)) * a.ntn;
     }
     int incl = mine;
 #pragma unroll
@@ -477,30 +350,31 @@ __device__ void tile_tables(const ExpertArgs &a)
     int run = incl - mine;
     for (int e = e0; e < e1; ++e) {
         const int lo = static_cast<int>(group_begin(a, e)), hi = static_cast<int>(group_begin(a, e + 1));
-        *lds_at<lds_int>(TileLds::kPre + e * 4) = run;
-        *lds_at<lds_int>(TileLds::kOff + e * 4) = lo;
-        run += row_tiles(max(0, hi - lo)) * a.ntn;
+        *lds_at<lds_int>(pre + e * 4) = run;
+        *lds_at<lds_int>(off + e * 4) = lo;
+        run += row_tiles<BM>(max(0, hi - lo)) * a.ntn;
     }
     if (lane == kWave - 1) {
-        *lds_at<lds_int>(TileLds::kPre + a.EL * 4) = incl;
-        *lds_at<lds_int>(TileLds::kOff + a.EL * 4) = static_cast<int>(group_begin(a, a.EL));
+        *lds_at<lds_int>(pre + a.EL * 4) = incl;
+        *lds_at<lds_int>(off + a.EL * 4) = static_cast<int>(group_begin(a, a.EL));
     }
 }
 
 // Tile number `id` of the list: experts in order, within one the row tiles in
 // groups of 8, within a group the column tiles with the row tiles of each side
 // by side (they read the same weights, and the next column tile the same rows).
-__device__ __forceinline__ Tile list_tile(const ExpertArgs &a, int id)
+template <int BM>
+__device__ __forceinline__ Tile list_tile(const ExpertArgs &a, int id, uint32_t pre, uint32_t off)
 {
     const int lane = threadIdx.x & (kWave - 1);
     int e = 0; // experts whose tiles all come before
     for (int x = lane; x < (a.EL + kWave - 1) / kWave * kWave; x += kWave)
-        e += __popcll(__ballot(x < a.EL && *lds_at<lds_int>(TileLds::kPre + (x + 1) * 4) <= id));
+        e += __popcll(__ballot(x < a.EL && *lds_at<lds_int>(pre + (x + 1) * 4) <= id));
     e = uniform(e);
-    int rest = id - uniform(*lds_at<lds_int>(TileLds::kPre + e * 4));
-    const int lo = uniform(*lds_at<lds_int>(TileLds::kOff + e * 4));
-    const int g = max(1, uniform(*lds_at<lds_int>(TileLds::kOff + e * 4 + 4)) - lo);
-    const int mt = row_tiles(g), bm = tile_height(g, mt);
+    int rest = id - uniform(*lds_at<lds_int>(pre + e * 4));
+    const int lo = uniform(*lds_at<lds_int>(off + e * 4));
+    const int g = max(1, uniform(*lds_at<lds_int>(off + e * 4 + 4)) - lo);
+    const int mt = row_tiles<BM>(g), bm = tile_height<BM>(g, mt);
     const int grp = rest / (8 * a.ntn);
     const int gm = min(8, mt - 8 * grp);
     rest -= grp * 8 * a.ntn;
@@ -512,6 +386,36 @@ __device__ __forceinline__ Tile list_tile(const ExpertArgs &a, int id)
     t.rows = min(bm, static_cast<int>(lo + g - t.r0));
     return t;
 }
+
+// The tiles of this workgroup, in order.  Workgroup j runs on XCD j % 8; every
+// XCD takes a run of consecutive tiles, so that its L2 holds what they share,
+// dealt over its workgroups in rounds.  A group's tiles may differ in height
+// and follow each other in a short rhythm, so the dealing shifts from round to
+// round.
+template <int BM>
+struct TileList {
+    int first, count, slot, slots, round;
+    uint32_t pre, off;
+    __device__ __forceinline__ TileList(const ExpertArgs &a, uint32_t pre_, uint32_t off_) : pre(pre_), off(off_)
+    {
+        const int total = uniform(*lds_at<lds_int>(pre + a.EL * 4));
+        const int chunk = (total + kXcds - 1) / kXcds;
+        first = blockIdx.x % kXcds * chunk;
+        count = min(chunk, total - first);
+        slot = blockIdx.x / kXcds;
+        slots = gridDim.x / kXcds;
+        round = 0;
+    }
+    __device__ __forceinline__ Tile next(const ExpertArgs &a)
+    {
+        const int pos = round * slots + (slot + 5 * round) % slots;
+        ++round;
+        Tile t = {-1, 0, 0, 0};
+        if (pos < count)
+            t = list_tile<BM>(a, first + pos, pre, off);
+        return t;
+    }
+};
 
 // What a wave keeps from tile to tile.
 struct TileWave {
@@ -827,34 +731,13 @@ __global__ void __launch_bounds__(kTileWaves * kWave) k_expert_tile(ExpertArgs a
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = uniform(threadIdx.x / kWave);
     if (wave == 0)
-        tile_tables(a);
+        tile_tables<kTileRows>(a, L::kPre, L::kOff);
     // the compiler sees LDS reads and writes but not the loads to LDS, nor
     // what the assembly above does: the array's address escapes here
     asm volatile("" : : "v"(tile_lds) : "memory");
     __syncthreads();
-    // Workgroup j runs on XCD j % 8; every XCD takes a run of consecutive
-    // tiles, so that its L2 holds what they share, dealt over its workgroups
-    // in rounds.  A group's tiles may differ in height and follow each other
-    // in a short rhythm, so the dealing shifts from round to round.
-    const int total = uniform(*lds_at<lds_int>(L::kPre + a.EL * 4));
-    const int xcd = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
-    const int slots = gridDim.x / kXcds;
-    const int chunk = (total + kXcds - 1) / kXcds;
-    const int first = xcd * chunk, count = min(chunk, total - first);
-    const auto tile = [&](int round) {
-        const int pos = round * slots + (slot + 5 * round) % slots;
-        Tile t = {-1, 0, 0, 0};
-        if (pos < count)
-            t = list_tile(a, first + pos);
-        return t;
-    };
-    const auto next_tile = [&](int &round) {
-        // a round's last places may be beyond the list
-        Tile t = tile(++round);
-        return t;
-    };
-    int round = 0;
-    Tile t = tile(0);
+    TileList<kTileRows> list(a, L::kPre, L::kOff);
+    Tile t = list.next(a);
     if (t.e < 0)
         return;
     TileWave w;
@@ -878,7 +761,7 @@ __global__ void __launch_bounds__(kTileWaves * kWave) k_expert_tile(ExpertArgs a
         send_load(w, i, 1, L::kStage);
     int keep = 0;
     while (t.e >= 0) {
-        const Tile next = next_tile(round);
+        const Tile next = list.next(a);
         switch ((t.rows + 63) >> 6) {
         case 1: keep = tile_run<1, GATED, FP8>(a, t, next, w, keep); break;
         case 2: keep = tile_run<2, GATED, FP8>(a, t, next, w, keep); break;
@@ -892,6 +775,181 @@ __global__ void __launch_bounds__(kTileWaves * kWave) k_expert_tile(ExpertArgs a
 }
 
 // ---------------------------------------------------------------------------
+// Products with up to a few dozen rows per expert: the weights, read once, are
+// all that counts.  Workgroups of 8 waves walk a list of tiles of 32 rows by
+// 256 weight rows (gated: 128 gate and 128 up rows) as above, but their steps
+// go through a ring of four stages in LDS: three steps, across tiles, are on
+// their way at any time.  A wave has 32 weight rows (gated: 16 gate and the 16
+// up rows of the same columns).
+// ---------------------------------------------------------------------------
+struct RingLds {
+    static constexpr int kRows = 32;
+    static constexpr int kStages = 4, kSets = 4;
+    static constexpr uint32_t kX = kTileCols * 128;              // in a stage
+    static constexpr uint32_t kStage = kX + kRows * 128;
+    static constexpr uint32_t kS = kStages * kStage;             // sets of scales of four steps: [row][4],
+    static constexpr uint32_t kSW = kRows * 16;                  // then [weight block][4]
+    static constexpr uint32_t kSet = kSW + 256;
+    static constexpr uint32_t kAmax = kS + kSets * kSet;         // gated: [wave][row]
+    static constexpr uint32_t kPre = kAmax + kTileWaves * kRows * 4;
+    static constexpr uint32_t kOff = kPre + (kMaxLocal + 1) * 4;
+    static constexpr uint32_t kBytes = kOff + (kMaxLocal + 1) * 4;
+    static_assert(kBytes <= 160 * 1024, "LDS of a CU");
+};
+constexpr int kRingLoads = 5; // loads of a wave per step, scales aside
+
+template <bool GATED, bool FP8>
+__global__ void __launch_bounds__(kTileWaves * kWave) k_expert_ring(ExpertArgs a)
+{
+    typedef RingLds L;
+    constexpr int kCols = GATED ? 128 : kTileCols; // output columns
+    extern __shared__ uint8_t tile_lds[];
+    flag_mismatch(a);
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = uniform(threadIdx.x / kWave);
+    const int l32 = lane & 31, upper = lane >> 5;
+    if (wave == 0)
+        tile_tables<L::kRows>(a, L::kPre, L::kOff);
+    asm volatile("" : : "v"(tile_lds) : "memory"); // (as in the tile kernel)
+    __syncthreads();
+    const int KB = a.K >> 7;
+    const uint32_t K = a.K;
+
+    // ---- loads: the tile and step to send for, and where it goes
+    TileList<L::kRows> ahead(a, L::kPre, L::kOff);
+    Tile to = {0, 0, 0, 0};
+    int to_b = KB, to_stage = 0, to_set = L::kSets - 1;
+    uint32_t woff[4], xoff = 0;
+    const uint8_t *wbase = nullptr, *xbase = nullptr;
+    const auto send = [&]() {
+        if (to.e < 0)
+            return;
+        if (to_b == KB) {
+            to = ahead.next(a);
+            if (to.e < 0)
+                return;
+            to_b = 0;
+            const uint32_t chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = wave * 32 + i * 8 + (lane >> 3);
+                woff[i] = (GATED ? r & 127 : min(r, a.N - 1 - to.ni * kTileCols)) * K + chunk;
+            }
+            xoff = min((wave & 3) * 8 + (lane >> 3), to.rows - 1) * K + chunk;
+            xbase = a.a + to.r0 * a.K;
+            wbase = a.w + (static_cast<int64_t>(to.e) * (GATED ? 2 * a.N : a.N) +
+                           static_cast<int64_t>(to.ni) * kCols) * a.K;
+            if (GATED && wave >= kTileWaves / 2) // up rows
+                wbase += static_cast<int64_t>(a.N) * a.K;
+        }
+        const uint32_t at = uniform(to_stage) * L::kStage;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            lds_load16(at + (wave * 4 + i) * 1024, wbase + to_b * 128 + woff[i]);
+        // two waves bring each 8 rows, so that all count the same loads
+        lds_load16(at + L::kX + (wave & 3) * 1024, xbase + to_b * 128 + xoff);
+        if ((to_b & 3) == 0) { // with a set's first step its scales: waves 0, 1 the rows', 2 the weights'
+            to_set = (to_set + 1) & (L::kSets - 1);
+            const uint32_t set = L::kS + uniform(to_set) * L::kSet;
+            const int col = min(to_b + (lane & 3), KB - 1);
+            if (wave < 2) {
+                const uint32_t row = min(wave * 16 + (lane >> 2), to.rows - 1);
+                lds_load4(set + wave * 256, a.sa + to.r0 * KB + row * KB + col);
+            } else if (wave == 2) {
+                const int nb = GATED ? to.ni : to.ni * 2;
+                const uint32_t other = GATED ? a.N >> 7 : min(nb + 1, a.NB - 1) - nb;
+                lds_load4(set + L::kSW, a.sw + (static_cast<int64_t>(to.e) * a.NB + nb) * KB +
+                                            ((lane >> 2) ? other * KB + col : col));
+            }
+        }
+        ++to_b;
+        to_stage = (to_stage + 1) & (L::kStages - 1);
+    };
+#pragma unroll
+    for (int i = 0; i < L::kStages - 1; ++i)
+        send();
+
+    // ---- products
+    TileList<L::kRows> list(a, L::kPre, L::kOff);
+    const int wrow = GATED ? (l32 < 16 ? wave * 16 + l32 : 128 + wave * 16 + l32 - 16) : wave * 32 + l32;
+    int stage = 0, set = L::kSets - 1;
+    for (Tile t = list.next(a); t.e >= 0; t = list.next(a)) {
+        f32x16 acc = f32x16{};
+        for (int b = 0; b < KB; ++b) {
+            // this step's loads are there: at least the next two steps' are newer
+            if (to.e >= 0)
+                step_barrier<(L::kStages - 2) * kRingLoads>();
+            else
+                step_barrier<0>();
+            send(); // over the stage before, which every wave is done with
+            if ((b & 3) == 0)
+                set = (set + 1) & (L::kSets - 1);
+            const uint32_t at = stage * L::kStage, sat = L::kS + set * L::kSet + (b & 3) * 4;
+            uint32_t xad[4], wad[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t c = (i >> 1) * 4 + upper * 2 + (i & 1);
+                xad[i] = at + L::kX + l32 * 128 + (c ^ (l32 & 7)) * 16;
+                wad[i] = at + wrow * 128 + (c ^ (wrow & 7)) * 16;
+            }
+            f32x16 q = mfma64(read_half(wad, 0, 0), read_half(xad, 0, 0), f32x16{});
+            q = mfma64(read_half(wad, 1, 0), read_half(xad, 1, 0), q);
+            const uint32_t swat = sat + L::kSW + (GATED ? 0 : (wave >> 2) * 16);
+            const float s = *lds_at<lds_float>(sat + l32 * 16);
+            const float f0 = s * *lds_at<lds_float>(swat);
+            const float f1 = GATED ? s * *lds_at<lds_float>(swat + 16) : f0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                acc[i] = fmaf(q[i], i < 8 ? f0 : f1, acc[i]);
+            stage = (stage + 1) & (L::kStages - 1);
+        }
+        const int64_t r = t.r0 + l32;
+        const bool in = l32 < t.rows;
+        if (!GATED) {
+#pragma unroll
+            for (int g = 0; g < 4; g += 2) {
+                const int n = t.ni * kTileCols + wave * 32 + g * 8 + upper * 8;
+                const u32x4 v = pack_eights(acc, g);
+                if (in && n < a.N)
+                    *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.out) + r * a.N + n) = v;
+            }
+            continue;
+        }
+        // h in place of the gate: the first 8 elements
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            acc[i] = gated(acc[i], acc[8 + i]);
+        const int n = t.ni * 128 + wave * 16 + upper * 8;
+        if (FP8) {
+            float v = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v = fmaxf(v, fabsf(acc[i]));
+            v = fmaxf(v, __shfl_xor(v, 32));
+            if (upper == 0)
+                *lds_at<lds_float>(L::kAmax + (wave * L::kRows + l32) * 4) = v;
+            lds_barrier();
+            v = kAmaxFloor;
+#pragma unroll
+            for (int i = 0; i < kTileWaves; ++i)
+                v = fmaxf(v, *lds_at<lds_float>(L::kAmax + (i * L::kRows + l32) * 4));
+            const float inv = __fdiv_rn(kE4M3Max, v);
+            uint32_t c0 = pack_e4m3(f32x4{acc[0], acc[1], acc[2], acc[3]}, inv);
+            uint32_t c1 = pack_e4m3(f32x4{acc[4], acc[5], acc[6], acc[7]}, inv);
+            whole_eights(c0, c1);
+            if (in)
+                *reinterpret_cast<u32x2 *>(static_cast<uint8_t *>(a.out) + r * a.N + n) = u32x2{c0, c1};
+            if (in && wave == 0 && upper == 0)
+                a.out_scale[r * (a.N >> 7) + t.ni] = __fdiv_rn(v, kE4M3Max);
+        } else {
+            const u32x4 v = pack_eights(acc, 0);
+            if (in)
+                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.out) + r * a.N + n) = v;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
 // launch
 // ---------------------------------------------------------------------------
 // The most tiles that `rows` rows in EL groups can make.
@@ -902,30 +960,13 @@ static int64_t tiles_max(const ExpertArgs &a, int bm)
     return (n + kXcds - 1) / kXcds * kXcds;
 }
 
-template <int MT>
-static hipError_t launch_gemm(ExpertArgs &a, hipStream_t s)
+static hipError_t launch_rows(ExpertArgs &a, hipStream_t s)
 {
-    a.ntn = (a.N + 16 * kProdWaves - 1) / (16 * kProdWaves);
-    const int64_t nb = tiles_max(a, 16 * MT);
-    if (nb > 0xFFFFFFFFll / (kProdWaves * kWave))
+    a.ntn = (a.N + kRowsCols - 1) / kRowsCols;
+    const int64_t nb = (a.rows_max < a.EL ? a.rows_max : a.EL) * a.ntn;
+    if (nb > 0xFFFFFFFFll / (kSplit * kWave))
         return hipErrorInvalidConfiguration;
-    const dim3 g(static_cast<unsigned>(nb)), blk(kProdWaves * kWave);
-    launch(k_expert_gemm<MT>, g, blk, 0, s, a);
-    return hipGetLastError();
-}
-
-template <int MT>
-static hipError_t launch_swiglu(ExpertArgs &a, hipStream_t s)
-{
-    a.ntn = a.N >> 7;
-    const int64_t nb = tiles_max(a, 16 * MT);
-    if (nb > 0xFFFFFFFFll / (kGatedWaves * kWave))
-        return hipErrorInvalidConfiguration;
-    const dim3 g(static_cast<unsigned>(nb)), blk(kGatedWaves * kWave);
-    if (a.out_scale)
-        launch(k_expert_swiglu<MT, true>, g, blk, 0, s, a);
-    else
-        launch(k_expert_swiglu<MT, false>, g, blk, 0, s, a);
+    launch(k_expert_rows, dim3(static_cast<unsigned>(nb)), dim3(kSplit * kWave), 0, s, a);
     return hipGetLastError();
 }
 
@@ -946,15 +987,51 @@ static hipError_t launch_tile(ExpertArgs &a, hipStream_t s)
     return hipGetLastError();
 }
 
+static hipError_t launch_ring(ExpertArgs &a, hipStream_t s)
+{
+    const int cols = a.gated ? 128 : kTileCols;
+    a.ntn = (a.N + cols - 1) / cols;
+    const int64_t nb = tiles_max(a, RingLds::kRows);
+    if (nb > 0x7FFFFFFF)
+        return hipErrorInvalidConfiguration;
+    const dim3 g(static_cast<unsigned>(nb < kCus ? nb : kCus)), blk(kTileWaves * kWave);
+    if (!a.gated)
+        launch(k_expert_ring<false, false>, g, blk, RingLds::kBytes, s, a);
+    else if (a.out_scale)
+        launch(k_expert_ring<true, true>, g, blk, RingLds::kBytes, s, a);
+    else
+        launch(k_expert_ring<true, false>, g, blk, RingLds::kBytes, s, a);
+    return hipGetLastError();
+}
+
+// Which kernel, from what is known before the launch.  `tiles`: column tiles of
+// the experts that can have rows; times are medians in us, E experts with r
+// rows each.
 hipError_t launch_expert_product(const ExpertArgs &a0, hipStream_t s)
 {
     ExpertArgs a = a0;
-    if (a.rows_mean > 32 && a.K >= 256) // (the tile kernel sends for two steps ahead)
-        return launch_tile(a, s);
-    const bool many = a.rows_mean > 16;
-    if (a.gated)
-        return many ? launch_swiglu<4>(a, s) : launch_swiglu<1>(a, s);
-    return many ? launch_gemm<4>(a, s) : launch_gemm<1>(a, s);
+    const int cols = a.gated ? 128 : kTileCols;
+    const int64_t tiles =
+        (a.rows_max < a.EL ? a.rows_max : a.EL) * static_cast<int64_t>((a.N + cols - 1) / cols);
+    // Products that are over before the others have listed their tiles: no
+    // group can be more than two passes of 16 rows, and the work is small.
+    // K = 2048, N = 4096 (rows / ring): E = 1: r = 1 5.4 / 13.7, r = 32 9.8 / 14.2,
+    // r = 64 20.0 / 14.6; E = 4, r = 16: 9.8 / 14.9; E = 16: r = 1 25.9 / 26.2,
+    // r = 16 33.9 / 26.6.  N = 512, E = 64: r = 8 14.6 / 15.6, r = 16 16.3 / 15.6.
+    // (Gated, K = 2048, N = 768: E = 1, r = 1 21.0 / 14.6, E = 64 46 / 40: the
+    // ring always.)
+    if (!a.gated && a.group_max <= 32 && tiles * a.rows_mean <= 4 * kCus)
+        return launch_rows(a, s);
+    // Tiles of 32 rows while the weights' bytes bound the product, or while
+    // taller ones would leave CUs without work.  K = 2048, N = 4096 (ring / tile):
+    // E = 64: r = 64 127 / 131, r = 128 207 / 147; E = 1, r = 512 17.1 / 31.6;
+    // E = 4: r = 256 28.2 / 32.2, r = 512 50.3 / 35.1.  N = 512: E = 16, r = 512 29.2 / 32.7; E = 64:
+    // r = 128 29.4 / 32.6, r = 256 54.4 / 44.6.  (The tile kernel sends two steps
+    // ahead: K >= 256.)
+    const int64_t ring_tiles = tiles * ((a.rows_mean + RingLds::kRows - 1) / RingLds::kRows);
+    if (a.K < 256 || a.rows_mean <= 64 || ring_tiles <= 2 * kCus)
+        return launch_ring(a, s);
+    return launch_tile(a, s);
 }
 
 }  // namespace moe

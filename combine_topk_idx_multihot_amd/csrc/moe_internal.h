@@ -175,6 +175,7 @@ struct ExpertArgs {
     int32_t *status;
     int64_t R;
     int64_t rows_max;       // most rows the groups can hold: min(R, the worst case)
+    int64_t group_max;      // most rows that one group can hold
     int64_t rows_mean;      // expected rows of one expert under uniform routing, rounded up
     int32_t K, N, EL;
     int32_t NB;             // scale rows of one expert

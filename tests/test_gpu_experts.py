@@ -115,12 +115,18 @@ LAYERS = {
     "one_group": dict(counts=[1000]),
     "one_token": dict(T=1, E=128, k=8, sync_free=True, extra=5),
     "two_tokens": dict(T=2, E=4, k=4),
+    "few_tokens": dict(counts=[0, 20, 1, 11]),
+    "few_tokens_padded": dict(counts=[17, 0, 3, 7], P=8, sync_free=True, extra=9),
+    "few_of_many": dict(T=3, E=200, k=5),
+    "two_large": dict(counts=[1000, 900, 40]),
     "decode": dict(T=77, E=32, k=4, sync_free=True, P=8, empty=0.2),
     "share": dict(T=700, E=32, k=8, lb=5, EL=7, sync_free=True, extra=100),
     "single_local": dict(T=90, E=16, k=3, lb=15, EL=1),
     "many_experts": dict(T=300, E=1024, k=6, lb=1, EL=1000, P=2),
 }
-SHAPES = [(128, 8), (256, 136), (384, 512), (768, 200), (2048, 264)]
+# many column tiles: tall tiles of rows (fewer would leave most of the chip idle)
+SHAPES = [(128, 8), (256, 136), (384, 512), (768, 200), (2048, 264),
+          (256, 2312), (384, 2312), (1024, 2560)]
 
 
 @pytest.mark.parametrize("K,N", SHAPES)
@@ -134,7 +140,7 @@ def test_gemm(name, K, N):
     check_gemm(L, *w, f"{name} {K} {N}")
 
 
-@pytest.mark.parametrize("K,I", [(128, 128), (640, 256), (2048, 384)])
+@pytest.mark.parametrize("K,I", [(128, 128), (640, 256), (2048, 384), (256, 1280), (640, 1280)])
 @pytest.mark.parametrize("name", LAYERS)
 def test_swiglu(name, K, I):
     if name == "many_experts":
@@ -156,10 +162,10 @@ def test_swiglu_saturated_gates():
     check_swiglu(L, w_q, w_s, False, "saturated bf16")
 
 
-@pytest.mark.parametrize("counts", [[5, 9, 0], [200, 300, 0], [1200, 600]])
-def test_nan_row_stays_alone(counts):
+@pytest.mark.parametrize("counts,N", [([5, 9, 0], 256), ([200, 300, 0], 256), ([1200, 600], 5120)])
+def test_nan_row_stays_alone(counts, N):
     L = Layer(256, counts=counts)
-    w = ref.make_weights(L.EL, 256, 256, L.g)
+    w = ref.make_weights(L.EL, N, 256, L.g)
     clean = B.expert_gemm_fp8(L.d, L.h, L.rows_q, L.row_scale, *w)
     h_clean, _ = B.expert_swiglu_fp8(L.d, L.h, L.rows_q, L.row_scale, *w, torch.bfloat16)
     bad = L.rows_q.clone()
@@ -339,4 +345,24 @@ def test_rows_past_four_gib():
     out = B.expert_gemm_fp8(d, h, rows.view(torch.float8_e4m3fn), scale, *w)
     ref.check_bf16(out[pick], *ref.product(q, s, *w, [0, 4, 4, 6]), "far rows")
     out[pick] = 0
+    assert not out.any()
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_weights_past_four_gib(T):
+    """Weight offsets past 2^32 bytes inside one expert, for a single token and for a few dozen."""
+    K, N = 16512, 1 << 18
+    d = B.make_desc(T, 1, 1)
+    h, _ = B.route(d, torch.zeros((T, 1), dtype=torch.int32, device="cuda"))
+    g = torch.Generator(device="cuda").manual_seed(T)
+    q, s = ref.quant_rows(torch.randn((T, K), generator=g, device="cuda"))
+    pick = torch.tensor([0, 1, N // 2 + 3, N - 300, N - 17, N - 1], device="cuda")
+    w_q = torch.zeros((1, N, K), dtype=torch.uint8, device="cuda")
+    w_s = torch.ones((1, N // 128, K // 128), device="cuda")
+    few, few_s = ref.make_weights(1, 6, K, g)
+    w_q[0, pick] = few.view(torch.uint8)[0]
+    w_s[0] = few_s[0]
+    out = B.expert_gemm_fp8(d, h, q, s, w_q.view(torch.float8_e4m3fn), w_s)
+    ref.check_bf16(out[:, pick], *ref.product(q, s, few, few_s, [0, T]), "far weights")
+    out[:, pick] = 0
     assert not out.any()
