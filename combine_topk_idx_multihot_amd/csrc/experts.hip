@@ -308,6 +308,30 @@ __device__ __forceinline__ u32x4 pack_eights(const f32x16 &v, int g)
     return u32x4{x0, x1, y0, y1};
 }
 
+// The value of lane l ^ X, X = 1 or 2.
+template <int X>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t v)
+{
+    constexpr int kPerm = X == 1 ? 0xB1 : 0x4E; // quad_perm 1 0 3 2, 2 3 0 1
+    return static_cast<uint32_t>(
+        __builtin_amdgcn_update_dpp(0, static_cast<int>(v), kPerm, 0xF, 0xF, true));
+}
+
+// Lanes l and l ^ X each hold x and y: afterwards the lower one has both x, the
+// upper one both y, each first the lower lane's.
+template <int X>
+__device__ __forceinline__ void trade(u32x4 &x, u32x4 &y)
+{
+    const bool up = threadIdx.x & X;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // (both moves before the choice: they need every lane)
+        const uint32_t other_x = lane_xor<X>(x[i]), other_y = lane_xor<X>(y[i]);
+        x[i] = up ? other_y : x[i];
+        y[i] = up ? y[i] : other_x;
+    }
+}
+
 __device__ __forceinline__ f32x16 mfma64(const i32x8 &a, const i32x8 &b, const f32x16 &c)
 {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
@@ -651,17 +675,24 @@ __device__ __forceinline__ int tile_run(const ExpertArgs &a, const Tile &t, cons
     if (!GATED) {
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            const int row = 64 * m + xrow;
-            uint16_t *o = static_cast<uint16_t *>(a.out) + (t.r0 + row) * a.N;
+            // v[c]: columns 16 c + 8 upper .. + 7 of this lane's row; traded in
+            // groups of four lanes, v[i] is of row i of the four and columns 16
+            // (lane % 4) + 8 upper, so that a store writes whole cache lines
+            u32x4 v[4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int c = 0; c < 4; ++c)
+                v[c] = pack_eights(acc[m][c >> 1], (c & 1) * 2);
+            trade<1>(v[0], v[1]);
+            trade<1>(v[2], v[3]);
+            trade<2>(v[0], v[2]);
+            trade<2>(v[1], v[3]);
+            const int row = 64 * m + (xrow & ~3);
+            const int n = t.ni * kTileCols + wn * 64 + (lane & 3) * 16 + upper * 8;
+            uint16_t *o = static_cast<uint16_t *>(a.out) + (t.r0 + row) * a.N + n;
 #pragma unroll
-                for (int g = 0; g < 4; g += 2) {
-                    const int n = t.ni * kTileCols + wn * 64 + j * 32 + g * 8 + upper * 8;
-                    const u32x4 v = pack_eights(acc[m][j], g);
-                    if (row < t.rows && n < a.N)
-                        *reinterpret_cast<u32x4 *>(o + n) = v;
-                }
+            for (int i = 0; i < 4; ++i)
+                if (row + i < t.rows && n < a.N)
+                    *reinterpret_cast<u32x4 *>(o + static_cast<int64_t>(i) * a.N) = v[i];
         }
         return whole ? 4 * M : 0;
     }
