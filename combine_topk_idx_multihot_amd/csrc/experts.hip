@@ -551,6 +551,8 @@ __device__ __forceinline__ int tile_run(const ExpertArgs &a, const Tile &t, cons
         asm volatile("s_waitcnt vmcnt(24) lgkmcnt(0)\n\ts_barrier" : : : "memory");
     else if (keep >= 8)
         asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)\n\ts_barrier" : : : "memory");
+    else if (keep >= 4)
+        asm volatile("s_waitcnt vmcnt(12) lgkmcnt(0)\n\ts_barrier" : : : "memory");
     else
         asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" : : : "memory");
     // Step b; with `send`, the loads (n of rows) of step `sb` of the tile aimed
@@ -642,6 +644,8 @@ __device__ __forceinline__ int tile_run(const ExpertArgs &a, const Tile &t, cons
         step_barrier<16>();
     else if (keep >= 8)
         step_barrier<8>();
+    else if (keep >= 4)
+        step_barrier<4>();
     else
         step_barrier<0>();
     scales(0);
@@ -718,10 +722,9 @@ __device__ __forceinline__ int tile_run(const ExpertArgs &a, const Tile &t, cons
     }
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-        const int row = 64 * m + xrow;
-        const int64_t r = t.r0 + row;
-        const int n = t.ni * 128 + wn * 32 + upper * 8;
         if (FP8) {
+            const int row = 64 * m + xrow;
+            const int64_t r = t.r0 + row;
             float v = kAmaxFloor;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -732,25 +735,30 @@ __device__ __forceinline__ int tile_run(const ExpertArgs &a, const Tile &t, cons
             for (int g = 0; g < 4; ++g)
                 c[g] = pack_e4m3(f32x4{acc[m][0][4 * g], acc[m][0][4 * g + 1], acc[m][0][4 * g + 2],
                                        acc[m][0][4 * g + 3]}, inv);
-#pragma unroll
-            for (int g = 0; g < 4; g += 2) {
-                whole_eights(c[g], c[g + 1]);
-                if (row < t.rows)
-                    *reinterpret_cast<u32x2 *>(static_cast<uint8_t *>(a.out) + r * a.N + n + g * 8) =
-                        u32x2{c[g], c[g + 1]};
-            }
+            // columns 16 upper .. + 15: eights of columns, then pairs of those
+            whole_eights(c[0], c[1]);
+            whole_eights(c[2], c[3]);
+            whole_eights(c[0], c[2]);
+            whole_eights(c[1], c[3]);
+            if (row < t.rows)
+                *reinterpret_cast<u32x4 *>(static_cast<uint8_t *>(a.out) + r * a.N + t.ni * 128 + wn * 32 +
+                                           upper * 16) = u32x4{c[0], c[1], c[2], c[3]};
             if (wn == 0 && upper == 0 && row < t.rows)
                 a.out_scale[r * (a.N >> 7) + t.ni] = __fdiv_rn(v, kE4M3Max);
         } else {
+            // (as above, in groups of two lanes: a wave has 64 bytes of a row)
+            u32x4 v[2] = {pack_eights(acc[m][0], 0), pack_eights(acc[m][0], 2)};
+            trade<1>(v[0], v[1]);
+            const int row = 64 * m + (xrow & ~1);
+            uint16_t *o = static_cast<uint16_t *>(a.out) + (t.r0 + row) * a.N + t.ni * 128 + wn * 32 +
+                          (lane & 1) * 16 + upper * 8;
 #pragma unroll
-            for (int g = 0; g < 4; g += 2) {
-                const u32x4 v = pack_eights(acc[m][0], g);
-                if (row < t.rows)
-                    *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.out) + r * a.N + n + g * 8) = v;
-            }
+            for (int i = 0; i < 2; ++i)
+                if (row + i < t.rows)
+                    *reinterpret_cast<u32x4 *>(o + static_cast<int64_t>(i) * a.N) = v[i];
         }
     }
-    return whole ? 2 * M : 0;
+    return whole ? (FP8 ? M : 2 * M) : 0;
 }
 
 template <bool GATED, bool FP8>
