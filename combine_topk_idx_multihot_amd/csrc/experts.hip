@@ -253,9 +253,15 @@ __device__ __forceinline__ void lds_barrier()
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
 }
 
-// LDS of the tile kernel, from address 0.  A row of a stage is 128 bytes, eight
-// 16-byte chunks, chunk c kept at place c ^ (row % 8): the rows that a matrix
-// operand reads at one chunk then lie in different banks.
+// A row of a stage in LDS is 128 bytes, eight 16-byte chunks.  Where row r keeps
+// its chunk c, and which chunk is at place c: rows of one parity share their
+// banks (64 of 4 bytes make two rows), and 16 consecutive rows read at one chunk
+// then lie in different ones.  With r % 8 in place of (r / 2) % 8 conflicts were
+// 53 % of the LDS cycles (16384 tokens, K = 2048, N = 4096; now 18 %) and the
+// products 1 - 3 % slower.
+__device__ __forceinline__ int place_of(int r, int c) { return c ^ ((r >> 1) & 7); }
+
+// LDS of the tile kernel, from address 0.
 struct TileLds {
     static constexpr uint32_t kX = kTileCols * 128;  // in a stage: weight rows, then rows
     static constexpr uint32_t kStage = 65536;        // two stages
@@ -460,10 +466,11 @@ __device__ __forceinline__ void aim_rows(const ExpertArgs &a, const Tile &t, Til
 {
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = uniform(threadIdx.x / kWave);
-    const uint32_t chunk = ((lane & 7) ^ (lane >> 3)) * 16;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w.off[4 + i] = min((wave * n + i) * 8 + (lane >> 3), t.rows - 1) * static_cast<uint32_t>(a.K) + chunk;
+    for (int i = 0; i < 4; ++i) {
+        const int r = (wave * n + i) * 8 + (lane >> 3);
+        w.off[4 + i] = min(r, t.rows - 1) * static_cast<uint32_t>(a.K) + place_of(r, lane & 7) * 16;
+    }
 }
 
 template <bool GATED>
@@ -473,11 +480,10 @@ __device__ __forceinline__ void aim(const ExpertArgs &a, const Tile &t, TileWave
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = uniform(threadIdx.x / kWave);
     const uint32_t K = a.K;
-    const uint32_t chunk = ((lane & 7) ^ (lane >> 3)) * 16;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = wave * 32 + i * 8 + (lane >> 3);
-        w.off[i] = (GATED ? r & 127 : min(r, a.N - 1 - t.ni * kTileCols)) * K + chunk;
+        w.off[i] = (GATED ? r & 127 : min(r, a.N - 1 - t.ni * kTileCols)) * K + place_of(r, lane & 7) * 16;
     }
     aim_rows(a, t, w, 4);
     w.xbase = a.a + t.r0 * a.K;
@@ -785,7 +791,7 @@ __global__ void __launch_bounds__(kTileWaves * kWave) k_expert_tile(ExpertArgs a
     const int l32 = lane & 31, upper = lane >> 5;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t place = (((i >> 1) * 4 + upper * 2 + (i & 1)) ^ (lane & 7)) * 16;
+        const uint32_t place = place_of(l32, (i >> 1) * 4 + upper * 2 + (i & 1)) * 16;
         w.xad[i] = L::kX + ((wave >> 2) * 32 + l32) * 128 + place;
     }
     aim<GATED>(a, t, w);
@@ -868,13 +874,14 @@ __global__ void __launch_bounds__(kTileWaves * kWave) k_expert_ring(ExpertArgs a
             if (to.e < 0)
                 return;
             to_b = 0;
-            const uint32_t chunk = ((lane & 7) ^ (lane >> 3)) * 16;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = wave * 32 + i * 8 + (lane >> 3);
-                woff[i] = (GATED ? r & 127 : min(r, a.N - 1 - to.ni * kTileCols)) * K + chunk;
+                woff[i] = (GATED ? r & 127 : min(r, a.N - 1 - to.ni * kTileCols)) * K +
+                          place_of(r, lane & 7) * 16;
             }
-            xoff = min((wave & 3) * 8 + (lane >> 3), to.rows - 1) * K + chunk;
+            const int r = (wave & 3) * 8 + (lane >> 3);
+            xoff = min(r, to.rows - 1) * K + place_of(r, lane & 7) * 16;
             xbase = a.a + to.r0 * a.K;
             wbase = a.w + (static_cast<int64_t>(to.e) * (GATED ? 2 * a.N : a.N) +
                            static_cast<int64_t>(to.ni) * kCols) * a.K;
@@ -928,8 +935,8 @@ __global__ void __launch_bounds__(kTileWaves * kWave) k_expert_ring(ExpertArgs a
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t c = (i >> 1) * 4 + upper * 2 + (i & 1);
-                xad[i] = at + L::kX + l32 * 128 + (c ^ (l32 & 7)) * 16;
-                wad[i] = at + wrow * 128 + (c ^ (wrow & 7)) * 16;
+                xad[i] = at + L::kX + l32 * 128 + place_of(l32, c) * 16;
+                wad[i] = at + wrow * 128 + place_of(wrow, c) * 16;
             }
             f32x16 q = mfma64(read_half(wad, 0, 0), read_half(xad, 0, 0), f32x16{});
             q = mfma64(read_half(wad, 1, 0), read_half(xad, 1, 0), q);
