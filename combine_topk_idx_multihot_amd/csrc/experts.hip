@@ -5,10 +5,10 @@
 // block.  Row r of local expert e's group:
 //   y[r,n] = sum over blocks b of 128 columns of
 //            sa[r,b] * sw[e, n / 128, b] * (sum over k in b of a[r,k] * w[e,n,k])
-// The inner sum is one matrix instruction of depth 128 (gfx950's f8f6f4 form,
-// whose 8-bit rate is twice that of the older 8-bit instructions); the two
-// scales are multiplied in fp32 and the block's sum enters the fp32
-// accumulator by one fma.
+// The inner sum is one matrix instruction of depth 128 or two of depth 64
+// (gfx950's f8f6f4 forms, whose 8-bit rate is twice that of the older 8-bit
+// instructions); the two scales are multiplied in fp32 and the block's sum
+// enters the fp32 accumulator by one fma.
 // What the 8-bit matrix instructions sum, measured on MI355X with chosen
 // operands: products are exact, groups of 8 consecutive columns are aligned to
 // the group's largest exponent sum E and cut off below 2^(E-13), and the
@@ -17,9 +17,12 @@
 // older 8-bit instructions do the same, and bf16 instructions on widened
 // codes, which are exact to fp32, run at half the rate.  Outputs are therefore
 // bf16 (or E4M3), not fp32.
-// Products are taken as w * a^T: the accumulator of a 16 x 16 tile then holds,
-// per lane, one token row and four consecutive output columns, so that a
-// lane's row scale is a single register and its outputs are stored together.
+// Products are taken as w * a^T: a lane of an accumulator then holds one token
+// row and runs of four consecutive output columns, so that its row scale is a
+// single register and its outputs are stored together.
+//
+// Three kernels, chosen by launch_expert_product: k_expert_rows (a few tokens),
+// k_expert_ring (up to dozens of rows per expert) and k_expert_tile.
 #include "moe_internal.h"
 
 namespace moe {
@@ -209,6 +212,22 @@ __global__ void __launch_bounds__(kSplit * kWave) k_expert_rows(ExpertArgs a)
 // up columns) one after the other.  Rows and weights come through LDS 128
 // columns (a step) at a time, in two stages: while a step is worked on, the
 // next one's data, or the first step's of the next tile, is on its way.
+//
+// What bounds it: per step and CU 128 32x32x64 instructions (16.8 Mflop), 64 KB
+// into LDS and 192 KB out of it, and 1024 wave fmas that bring the blocks' sums
+// under their scales.  At 16384 tokens, top-8 of 128, K = 2048, N = 4096 the
+// matrix units are busy for 51 % of the cycles, and the clock settles at 1.6 -
+// 1.7 GHz instead of 2.4: the card's power limit, which also makes zeros 15 - 20 %
+// faster than random codes.  There 1216 us, 1.80 PFLOP/s (a library's FP8 product
+// without block scales: 2.62 at 8192^3).  4096 tokens, K = 768, N = 2048 (256 rows per
+// expert, 6 steps a tile): 113 us, 3.2 TB/s.  Gated: 4096 tokens, K = 2048, N = 768
+// 190 us, 1.09 PFLOP/s; 16 of 128 experts, 16384 tokens, K = 4096, N = 1024 189 us,
+// 1.45 PFLOP/s.
+// Measured against it and dropped: 16x16x128 instructions (4 % slower), two
+// barriers per step with the waves in two groups, 128 x 128 tiles (1.3 - 1.9 times the
+// time), scales loaded with every step (0.2 - 0.3 us more per step), tiles dealt by
+// height for equal shares (the 16-expert case 5 % faster, the 16384-token one 6 %
+// slower, as tiles of the same weights drift apart).
 // ---------------------------------------------------------------------------
 constexpr int kTileWaves = 8;
 constexpr int kTileCols = 256;
@@ -826,6 +845,13 @@ __global__ void __launch_bounds__(kTileWaves * kWave) k_expert_tile(ExpertArgs a
 // go through a ring of four stages in LDS: three steps, across tiles, are on
 // their way at any time.  A wave has 32 weight rows (gated: 16 gate and the 16
 // up rows of the same columns).
+// With tiles for every CU the rate is HBM's: 256 tokens, top-8 of 128, K = 768,
+// N = 2048 44 us, 4.9 TB/s; gated, 333 tokens on 32 experts, K = 2048, N = 768 20 -
+// 23 us, 4.4 - 5.2 TB/s.  With fewer, a CU's own: 0.6 us per step of 36 KB, whatever
+// the order of its loads and LDS reads, and also where idle CUs had read the
+// weights into the L2 before it.  One token, gated, 48 tiles of 16 steps: 16 us
+// (from HBM to registers, 16 waves per 128 columns: 20 - 22 us); a group of 128
+// columns shares one scale, so fewer columns per tile are no choice there.
 // ---------------------------------------------------------------------------
 struct RingLds {
     static constexpr int kRows = 32;
