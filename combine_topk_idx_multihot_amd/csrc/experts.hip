@@ -223,11 +223,11 @@ __global__ void __launch_bounds__(kSplit * kWave) k_expert_rows(ExpertArgs a)
 // expert, 6 steps a tile): 113 us, 3.2 TB/s.  Gated: 4096 tokens, K = 2048, N = 768
 // 190 us, 1.09 PFLOP/s; 16 of 128 experts, 16384 tokens, K = 4096, N = 1024 189 us,
 // 1.45 PFLOP/s.
-// Measured against it and dropped: 16x16x128 instructions (4 % slower), two
-// barriers per step with the waves in two groups, 128 x 128 tiles (1.3 - 1.9 times the
-// time), scales loaded with every step (0.2 - 0.3 us more per step), tiles dealt by
-// height for equal shares (the 16-expert case 5 % faster, the 16384-token one 6 %
-// slower, as tiles of the same weights drift apart).
+// Measured against it and dropped: 16x16x128 instructions (from registers alone
+// 4.3 PFLOP/s, 32x32x64 5.0), two barriers per step with the waves in two groups
+// (6 - 12 % slower), scales loaded with every step (0.2 - 0.3 us more per step of
+// 2.0), tiles dealt by height for equal shares (the 16-expert case 5 % faster, the
+// 16384-token one 6 % slower, as tiles of the same weights drift apart).
 // ---------------------------------------------------------------------------
 constexpr int kTileWaves = 8;
 constexpr int kTileCols = 256;
