@@ -538,6 +538,20 @@ def _handle_here(handle: Handle, desc: Desc):
           handle.workspace)
 
 
+# Their workgroups write outputs while others still read inputs.
+def _apart(outs, ins):
+    def span(t):
+        return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+    outs = [t for t in outs if t is not None and t.numel()]
+    for i, t in enumerate(outs):
+        a, b = span(t)
+        for o in (*ins, *outs[:i]):
+            if o is not None and o.numel():
+                c, e = span(o)
+                if a < e and c < b:
+                    raise MoeError(MOE_ERR_ARG, "an output overlaps an input or another output")
+
+
 def _int32(name: str, v) -> int:
     if not 0 <= v < 1 << 31:
         raise MoeError(MOE_ERR_ARG, f"{name} must be in [0, 2^31) (got {v})")
@@ -555,6 +569,7 @@ def _weighted_ptrs(desc, handle, Y, H, cap, topk_w, out):
     p_y = _dev(Y, "Y", _BF16, cap * H) if cap else None
     p_w = _dev(topk_w, "topk_w", _F32, desc.T * desc.k) if desc.T else None
     p_o = _dev(out, "out", _BF16_F32, desc.T * H) if desc.T else None
+    _apart((out,), (Y, topk_w))
     return p_y, p_w, p_o
 
 
@@ -575,6 +590,7 @@ def _weighted_bwd_ptrs(desc, handle, grad_out, Y, H, cap, topk_w, grad_rows, dw)
     p_w = _dev(topk_w, "topk_w", _F32, n) if desc.T else None
     p_gr = _dev(grad_rows, "grad_rows", _BF16, cap * H) if cap else None
     p_dw = _dev(dw, "dw", _F32, n) if desc.T else None
+    _apart((grad_rows, dw), (grad_out, Y, topk_w))
     return p_g, p_y, p_w, p_gr, p_dw
 
 
@@ -607,6 +623,7 @@ def moe_expert_gemm_fp8(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_sc
     p = _product_ptrs(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, _int32("N", N))
     _here(out)
     p_o = _dev(out, "out", _BF16, R * N) if R else None
+    _apart((out,), (rows_q, row_scale, w_q, w_scale))
     return _check(lib().moe_expert_gemm_fp8(ctypes.byref(desc), handle.cref(), p[0], p[1], K, R,
                                             p[2], p[3], N, p_o, _stream(stream)))
 
@@ -630,6 +647,7 @@ def moe_expert_swiglu_fp8(desc: Desc, handle: Handle, rows_q: torch.Tensor,
     or, with out_scale [R,I/128], out [R,I] E4M3 codes."""
     p = _product_ptrs(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, 2 * _int32("I", I))
     p_o, p_s = _swiglu_out(out, out_scale, R, I)
+    _apart((out, out_scale), (rows_q, row_scale, w_q, w_scale))
     return _check(lib().moe_expert_swiglu_fp8(ctypes.byref(desc), handle.cref(), p[0], p[1], K, R,
                                               p[2], p[3], I, p_o, p_s, _stream(stream)))
 
@@ -692,6 +710,7 @@ class PreparedExpertGemmFp8(_Prepared):
         p = _product_ptrs(desc, handle, rows_q, row_scale, K, cap, w_q, w_scale, N)
         _here(out)
         p_o = _dev(out, "out", _BF16, cap * N) if cap else None
+        _apart((out,), (rows_q, row_scale, w_q, w_scale))
         self._bind(lib().moe_expert_gemm_fp8, desc, handle, (p[0], p[1], K),
                    (p[2], p[3], N, p_o, _stream(stream)), cap,
                    (rows_q, row_scale, w_q, w_scale, out))
@@ -706,6 +725,7 @@ class PreparedExpertSwigluFp8(_Prepared):
         cap = min(rows_q.numel() // _positive("K", K), out.numel() // _positive("I", I))
         p = _product_ptrs(desc, handle, rows_q, row_scale, K, cap, w_q, w_scale, 2 * I)
         p_o, p_s = _swiglu_out(out, out_scale, cap, I)
+        _apart((out, out_scale), (rows_q, row_scale, w_q, w_scale))
         self._bind(lib().moe_expert_swiglu_fp8, desc, handle, (p[0], p[1], K),
                    (p[2], p[3], I, p_o, p_s, _stream(stream)), cap,
                    (rows_q, row_scale, w_q, w_scale, out, out_scale))
@@ -906,7 +926,7 @@ def expert_gemm_fp8(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scale:
                     w_q: torch.Tensor, w_scale: torch.Tensor, stream=None):
     """moe_expert_gemm_fp8 with a fresh output [R,N] bf16 (its rows past the total are not written)."""
     (R, K), N = rows_q.shape, w_q.shape[1]
-    _same_k(rows_q, w_q)
+    _shapes_fit(desc, rows_q, row_scale, w_q, w_scale)
     out = torch.empty((R, N), dtype=torch.bfloat16, device=rows_q.device)
     moe_expert_gemm_fp8(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, N, out, stream=stream)
     return out
@@ -918,7 +938,7 @@ def expert_swiglu_fp8(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scal
     """moe_expert_swiglu_fp8 with fresh outputs (rows past the total are not written): (h [R,I]
     float8_e4m3fn, h_scale [R,I/128]), or with out_dtype=torch.bfloat16 (h, None)."""
     (R, K), I = rows_q.shape, w_q.shape[1] // 2
-    _same_k(rows_q, w_q)
+    _shapes_fit(desc, rows_q, row_scale, w_q, w_scale)
     if w_q.shape[1] % 2:
         raise MoeError(MOE_ERR_ARG, f"w_q needs 2I rows per expert (got {w_q.shape[1]})")
     out = torch.empty((R, I), dtype=out_dtype, device=rows_q.device)
@@ -929,7 +949,14 @@ def expert_swiglu_fp8(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scal
     return out, out_scale
 
 
-def _same_k(rows_q, w_q):
-    if w_q.dim() != 3 or w_q.shape[2] != rows_q.shape[1]:
-        raise MoeError(MOE_ERR_ARG, f"w_q must be [EL,N,K] with K={rows_q.shape[1]} "
+def _shapes_fit(desc, rows_q, row_scale, w_q, w_scale):
+    R, K = rows_q.shape
+    if w_q.dim() != 3 or w_q.shape[0] != desc.num_local or w_q.shape[2] != K:
+        raise MoeError(MOE_ERR_ARG, f"w_q must be [EL,N,K] with EL={desc.num_local} and K={K} "
                                     f"(got {tuple(w_q.shape)})")
+    blocks = (desc.num_local, -(-w_q.shape[1] // 128), K // 128)
+    if tuple(w_scale.shape) != blocks:
+        raise MoeError(MOE_ERR_ARG, f"w_scale must be {list(blocks)} (got {tuple(w_scale.shape)})")
+    if tuple(row_scale.shape) != (R, K // 128):
+        raise MoeError(MOE_ERR_ARG, f"row_scale must be {[R, K // 128]} "
+                                    f"(got {tuple(row_scale.shape)})")

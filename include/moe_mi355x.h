@@ -329,6 +329,9 @@ int moe_dispatch_bwd(const moe_desc *desc, const moe_handle *handle, const uint1
                      int32_t grad_x_is_f32, float *grad_topk_w, void *stream);
 
 /*
+ * (The four calls that follow read inputs to their end: outputs must not
+ * overlap inputs or each other.)
+ *
  * Weighted combine: out[t] = sum of w * Y[row] over t's distinct local slots,
  * in ascending slot order, for experts that leave their rows unweighted (the
  * plain moe_combine expects rows that already carry the weight).

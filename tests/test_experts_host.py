@@ -128,3 +128,26 @@ def test_binding_rejects_cpu_tensors_and_bad_types():
         B.moe_expert_gemm_fp8(B.make_desc(5, 2, 4), h, q, s, 128, 8, w, ws, 128, out)
     with pytest.raises(B.MoeError, match="positive"):
         B.PreparedExpertGemmFp8(d, h, q, s, 0, w, ws, 128, out)
+
+
+def test_convenience_shapes():
+    """Weights of other experts than the local ones, or scales of another layout, are refused."""
+    d = B.make_desc(4, 2, 8, 2, 4)
+    q, s = torch.zeros((8, 256), dtype=torch.uint8), torch.zeros((8, 2))
+    w, ws = torch.zeros((4, 256, 256), dtype=torch.uint8), torch.zeros((4, 2, 2))
+    for call in (B.expert_gemm_fp8, B.expert_swiglu_fp8):
+        for bad in ((q, s, torch.zeros((8, 256, 256), dtype=torch.uint8), torch.zeros((8, 2, 2))),
+                    (q, s, w, torch.zeros((4, 2, 1))), (q, s, w, torch.zeros((4, 4))),
+                    (q, s.T, w, ws), (q, s[:7], w, ws)):
+            with pytest.raises(B.MoeError, match="must be"):
+                call(d, None, *bad)
+
+
+def test_outputs_apart():
+    buf = torch.zeros(64, dtype=torch.uint8)
+    a, b, c = buf[:32], buf[16:48], buf[32:]
+    B._apart((a, c), (None, torch.zeros(4)))
+    B._apart((a[:0],), (a,))
+    for outs, ins in (((a,), (b,)), ((a, b), ()), ((c,), (a, b)), ((a,), (a,)), ((a, None), (buf,))):
+        with pytest.raises(B.MoeError, match="overlaps"):
+            B._apart(outs, ins)
