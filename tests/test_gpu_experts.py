@@ -366,3 +366,50 @@ def test_weights_past_four_gib(T):
     ref.check_bf16(out[:, pick], *ref.product(q, s, few, few_s, [0, T]), "far weights")
     out[:, pick] = 0
     assert not out.any()
+
+
+def test_fp8_layer_compiled():
+    T, H, I, E, k, C = 48, 256, 128, 8, 2, 48 * 2 + 8
+    x, idx, w, *weights = fp8_layer_inputs(T, H, I, E, E, k, 9)
+    fn = lambda *a: ops.moe_layer_fp8(*a, E, 0, 2, C)  # noqa: E731
+    want = fn(x, idx, w, *weights)
+    got = torch.compile(fn, backend="aot_eager", fullgraph=True)(x, idx, w, *weights)
+    assert torch.equal(got, want)
+
+
+def test_two_graphs_at_once():
+    """Two captured layers over the same weights, replayed on two streams at the same time."""
+    T, H, I, E, k, C = 200, 512, 256, 16, 4, 200 * 4
+    both = []
+    for seed in (1, 2):
+        x, idx, w, *weights = fp8_layer_inputs(T, H, I, E, E, k, seed)
+        weights = both[0][3] if both else weights
+        run = lambda x=x, idx=idx, w=w, ws=weights: ops.moe_layer_fp8(x, idx, w, *ws, E, 0, 1, C)  # noqa: E731
+        want, s = run(), torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            out = run()
+        both.append((graph, s, want, weights, out, (x, idx, w)))  # what a graph reads stays alive
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for graph, s, _, _, out, _ in both:
+            with torch.cuda.stream(s):
+                out.zero_()
+                for _ in range(4):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for _, _, want, _, out, _ in both:
+            assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("T,K,N", [(20, 512, 264), (512, 512, 1032), (2048, 384, 5128)])
+def test_every_token_to_one_expert(T, K, N):
+    """Group sizes far from the mean that uniform routing would give."""
+    counts = [0] * 16
+    counts[5] = T
+    L = Layer(K, counts=counts, P=8)
+    w = ref.make_weights(16, N, K, L.g)
+    check_gemm(L, *w, f"one of 16, {T}")
+    w = ref.make_weights(16, 256, K, L.g)
+    check_swiglu(L, *w, True, f"one of 16, {T} fp8")
