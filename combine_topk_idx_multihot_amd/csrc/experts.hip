@@ -696,6 +696,10 @@ __device__ __forceinline__ int tile_run(const ExpertArgs &a, const Tile &t, cons
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
         send_load(w, i, n1, w.stage ^ L::kStage);
+    // The next tile's waits count this one's stores as newer than these loads,
+    // which name no memory themselves: here no store may be moved ahead of them
+    // (and, by the clobber of the waits, none behind the next tile's start).
+    asm volatile("" : : : "memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i)
         acc[M - 1][1][i] = fmaf(q[1][i], f1, acc[M - 1][1][i]);
