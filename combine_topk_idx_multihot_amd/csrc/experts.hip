@@ -280,7 +280,11 @@ __device__ __forceinline__ void lds_barrier()
 // products 1 - 3 % slower.
 __device__ __forceinline__ int place_of(int r, int c) { return c ^ ((r >> 1) & 7); }
 
-// LDS of the tile kernel, from address 0.
+// LDS of the tile kernel, from address 0: the loads to LDS take plain addresses
+// and the two stages are told apart by one address bit.  Dynamic LDS starts
+// there only in a kernel without static LDS, so neither this kernel nor the ring
+// kernel may have a __shared__ of its own (the tests read that from the built
+// code).
 struct TileLds {
     static constexpr uint32_t kX = kTileCols * 128;  // in a stage: weight rows, then rows
     static constexpr uint32_t kStage = 65536;        // two stages
@@ -878,7 +882,7 @@ __global__ void __launch_bounds__(kTileWaves * kWave) k_expert_ring(ExpertArgs a
 {
     typedef RingLds L;
     constexpr int kCols = GATED ? 128 : kTileCols; // output columns
-    extern __shared__ uint8_t tile_lds[];
+    extern __shared__ uint8_t tile_lds[]; // from 0, and the kernel's only LDS
     flag_mismatch(a);
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = uniform(threadIdx.x / kWave);

@@ -11,6 +11,7 @@ from combine_topk_idx_multihot_amd import binding as B
 
 LLVM = "/opt/rocm/llvm/bin"
 TILE = "13k_expert_tile"
+RING = "13k_expert_ring"
 
 
 def tool(name, *args, cwd=None):
@@ -77,3 +78,18 @@ def test_tile_stores_come_after_the_next_tiles_loads(code):
         assert sum(line.startswith("global_load_lds_dwordx4") for line in lines) >= 4 * 8, name
         assert sum(line.startswith("global_store") for line in lines) >= 4, name
         assert stores_ahead_of_loads(lines) == 0, name
+
+
+def test_lds_by_address_has_no_static_neighbour(code):
+    """Both kernels address their dynamic LDS from 0, so they may have no static LDS before it."""
+    notes = tool("llvm-readelf", "--notes", code)
+    sizes = re.findall(r"\.group_segment_fixed_size: (\d+).*?\.name: +(\S+)", notes, re.S)
+    mine = {name: int(size) for size, name in sizes if TILE in name or RING in name}
+    assert len(mine) == 6 and not any(mine.values()), mine
+
+
+def test_notes_of_a_kernel_with_static_lds_are_seen(code):
+    """The reading above finds static LDS where there is some: the kernel for a few tokens has 6 KiB."""
+    notes = tool("llvm-readelf", "--notes", code)
+    sizes = re.findall(r"\.group_segment_fixed_size: (\d+).*?\.name: +(\S+)", notes, re.S)
+    assert [int(size) for size, name in sizes if "13k_expert_rows" in name] == [6144]
