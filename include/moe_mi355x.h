@@ -377,7 +377,10 @@ int moe_combine_weighted_bwd(const moe_desc *desc, const moe_handle *handle,
  *   w_scale     device [EL,ceil(N/128),K/128] fp32: one scale per block of 128
  *               x 128 weights (the last block of rows may be smaller).
  *   out         device [R,N] bf16, rounded to nearest-even.
- *   R           rows, as for moe_dispatch.
+ *   R           rows, as for moe_dispatch; a device total != R sets
+ *               MOE_FLAG_ROWS_MISMATCH, except where R = 0 (eager mode): then
+ *               nothing is launched and this call flags nothing.  The calls that
+ *               move rows do, the combine of the outputs among them.
  * Each block of 128 columns is summed by the GPU's 8-bit matrix instructions
  * (exact products; of every 8 consecutive ones, bits below 2^-13 of the
  * largest one's power of two are cut off; fp32 sums), then added to an fp32

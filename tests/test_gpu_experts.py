@@ -209,6 +209,22 @@ def test_eager_fewer_rows_than_routed():
     assert int(L.h.status[1]) & B.MOE_FLAG_ROWS_MISMATCH
 
 
+def test_eager_no_rows_of_a_routed_batch():
+    """R = 0 where rows were routed: the products launch nothing and flag nothing (the one exception to
+    the rule above); the combine that follows writes zeros and flags it."""
+    L = Layer(128, counts=[30, 0, 20])
+    w = ref.make_weights(3, 256, 128, L.g)
+    out, h, hs = fill((4, 256), torch.bfloat16), fill((4, 128), torch.float8_e4m3fn), fill((4, 1), torch.float32)
+    B.moe_expert_gemm_fp8(L.d, L.h, L.rows_q, L.row_scale, 128, 0, *w, 256, out)
+    B.moe_expert_swiglu_fp8(L.d, L.h, L.rows_q, L.row_scale, 128, 0, *w, 128, h, hs)
+    assert B.expert_gemm_fp8(L.d, L.h, L.rows_q[:0], L.row_scale[:0], *w).shape == (0, 256)
+    assert untouched(out, 0) and untouched(h, 0) and untouched(hs, 0)
+    assert not int(L.h.status[1]) & B.MOE_FLAG_ROWS_MISMATCH
+    topk_w = torch.ones((50, 1), device="cuda")
+    assert (B.combine_weighted(L.d, L.h, out[:0], topk_w) == 0).all()
+    assert int(L.h.status[1]) & B.MOE_FLAG_ROWS_MISMATCH
+
+
 def test_no_tokens_and_no_rows():
     d = B.make_desc(0, 2, 4)
     h, _ = B.route(d, torch.empty((0, 2), dtype=torch.int32, device="cuda"))
