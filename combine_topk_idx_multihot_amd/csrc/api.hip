@@ -280,8 +280,7 @@ int check_product(const moe_desc *desc, const moe_handle *handle, const uint8_t 
     return MOE_OK;
 }
 
-// The arguments that both products share.  The groups hold at most R rows and
-// at most the worst case of the description, whatever capacity the caller chose.
+// The arguments that both products share.
 moe::ExpertArgs product_args(const moe_desc *desc, const moe_handle *handle, const uint8_t *rows_q,
                              const float *row_scale, int32_t K, int64_t R, const uint8_t *w_q,
                              const float *w_scale)
@@ -294,11 +293,8 @@ moe::ExpertArgs product_args(const moe_desc *desc, const moe_handle *handle, con
     a.off = handle->padded_offsets;
     a.status = handle->status;
     a.R = R;
-    const int64_t worst = cap_min(desc);
-    a.rows_max = R < worst ? R : worst;
-    const int64_t P = desc->pad_multiple, group = (desc->T + P - 1) / P * P; // a row per token at most
-    a.group_max = group < a.rows_max ? group : a.rows_max;
-    a.rows_mean = (desc->T * desc->k + desc->E - 1) / desc->E;
+    a.load = moe::expert_load(desc->T, desc->k, desc->E, desc->num_local, desc->pad_multiple, cap_min(desc), R,
+                              desc->mode == MOE_EAGER);
     a.K = K;
     a.EL = desc->num_local;
     a.eager = desc->mode == MOE_EAGER;
@@ -931,7 +927,7 @@ int moe_expert_gemm_fp8(const moe_desc *desc, const moe_handle *handle, const ui
     a.N = N;
     a.NB = (N + 127) / 128;
     a.gated = 0;
-    if (a.rows_max == 0)
+    if (a.load.rows_max == 0)
         return ok();
     hipError_t e = moe::launch_expert_product(a, static_cast<hipStream_t>(stream));
     if (e != hipSuccess)
@@ -960,7 +956,7 @@ int moe_expert_swiglu_fp8(const moe_desc *desc, const moe_handle *handle, const 
     a.N = I;
     a.NB = I / 64;
     a.gated = 1;
-    if (a.rows_max == 0)
+    if (a.load.rows_max == 0)
         return ok();
     hipError_t e = moe::launch_expert_product(a, static_cast<hipStream_t>(stream));
     if (e != hipSuccess)

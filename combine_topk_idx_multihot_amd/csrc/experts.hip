@@ -21,7 +21,7 @@
 // row and runs of four consecutive output columns, so that its row scale is a
 // single register and its outputs are stored together.
 //
-// Three kernels, chosen by launch_expert_product: k_expert_rows (a few tokens),
+// Three kernels, chosen by choose_expert_kernel: k_expert_rows (a few tokens),
 // k_expert_ring (up to dozens of rows per expert) and k_expert_tile.
 #include "moe_internal.h"
 
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kSplit * kWave) k_expert_rows(ExpertArgs a)
     flag_mismatch(a);
     const int slot = blockIdx.x / a.ntn, ni = blockIdx.x - slot * a.ntn;
     // as many slots as experts, or as rows where those are fewer
-    const int e = __builtin_amdgcn_readfirstlane(a.rows_max < a.EL ? nonempty_expert(a, slot) : slot);
+    const int e = __builtin_amdgcn_readfirstlane(a.load.rows_max < a.EL ? nonempty_expert(a, slot) : slot);
     if (e < 0)
         return;
     const int64_t r0 = group_begin(a, e), r1 = group_begin(a, e + 1);
@@ -230,10 +230,8 @@ __global__ void __launch_bounds__(kSplit * kWave) k_expert_rows(ExpertArgs a)
 // 16384-token one 6 % slower, as tiles of the same weights drift apart).
 // ---------------------------------------------------------------------------
 constexpr int kTileWaves = 8;
-constexpr int kTileCols = 256;
 constexpr int kTileRows = 256;
 constexpr int kTileBlocks = kTileRows / 64; // blocks of 64 rows, 32 per half of the waves
-constexpr int kCus = 256;                   // MI355X
 constexpr int kLoads = 8;                   // loads of a wave per step
 
 // 16 or 4 bytes per lane from each lane's address to LDS, lane l's at `lds` +
@@ -862,7 +860,7 @@ __global__ void __launch_bounds__(kTileWaves * kWave) k_expert_tile(ExpertArgs a
 // columns shares one scale, so fewer columns per tile are no choice there.
 // ---------------------------------------------------------------------------
 struct RingLds {
-    static constexpr int kRows = 32;
+    static constexpr int kRows = kRingRows;
     static constexpr int kStages = 4, kSets = 4;
     static constexpr uint32_t kX = kTileCols * 128;              // in a stage
     static constexpr uint32_t kStage = kX + kRows * 128;
@@ -1035,15 +1033,15 @@ __global__ void __launch_bounds__(kTileWaves * kWave) k_expert_ring(ExpertArgs a
 // The most tiles that `rows` rows in EL groups can make.
 static int64_t tiles_max(const ExpertArgs &a, int bm)
 {
-    const int64_t groups = a.rows_max < a.EL ? a.rows_max : a.EL;
-    const int64_t n = (a.rows_max / bm + groups) * a.ntn;
+    const int64_t groups = a.load.rows_max < a.EL ? a.load.rows_max : a.EL;
+    const int64_t n = (a.load.rows_max / bm + groups) * a.ntn;
     return (n + kXcds - 1) / kXcds * kXcds;
 }
 
 static hipError_t launch_rows(ExpertArgs &a, hipStream_t s)
 {
     a.ntn = (a.N + kRowsCols - 1) / kRowsCols;
-    const int64_t nb = (a.rows_max < a.EL ? a.rows_max : a.EL) * a.ntn;
+    const int64_t nb = (a.load.rows_max < a.EL ? a.load.rows_max : a.EL) * a.ntn;
     if (nb > 0xFFFFFFFFll / (kSplit * kWave))
         return hipErrorInvalidConfiguration;
     launch(k_expert_rows, dim3(static_cast<unsigned>(nb)), dim3(kSplit * kWave), 0, s, a);
@@ -1084,34 +1082,14 @@ static hipError_t launch_ring(ExpertArgs &a, hipStream_t s)
     return hipGetLastError();
 }
 
-// Which kernel, from what is known before the launch.  `tiles`: column tiles of
-// the experts that can have rows; times are medians in us, E experts with r
-// rows each.
 hipError_t launch_expert_product(const ExpertArgs &a0, hipStream_t s)
 {
     ExpertArgs a = a0;
-    const int cols = a.gated ? 128 : kTileCols;
-    const int64_t tiles =
-        (a.rows_max < a.EL ? a.rows_max : a.EL) * static_cast<int64_t>((a.N + cols - 1) / cols);
-    // Products that are over before the others have listed their tiles: no
-    // group can be more than two passes of 16 rows, and the work is small.
-    // K = 2048, N = 4096 (rows / ring): E = 1: r = 1 5.4 / 13.7, r = 32 9.8 / 14.2,
-    // r = 64 20.0 / 14.6; E = 4, r = 16: 9.8 / 14.9; E = 16: r = 1 25.9 / 26.2,
-    // r = 16 33.9 / 26.6.  N = 512, E = 64: r = 8 14.6 / 15.6, r = 16 16.3 / 15.6.
-    // (Gated, K = 2048, N = 768: E = 1, r = 1 21.0 / 14.6, E = 64 46 / 40: the
-    // ring always.)
-    if (!a.gated && a.group_max <= 32 && tiles * a.rows_mean <= 4 * kCus)
-        return launch_rows(a, s);
-    // Tiles of 32 rows while the weights' bytes bound the product, or while
-    // taller ones would leave CUs without work.  K = 2048, N = 4096 (ring / tile):
-    // E = 64: r = 64 127 / 131, r = 128 207 / 147; E = 1, r = 512 17.1 / 31.6;
-    // E = 4: r = 256 28.2 / 32.2, r = 512 50.3 / 35.1.  N = 512: E = 16, r = 512 29.2 / 32.7; E = 64:
-    // r = 128 29.4 / 32.6, r = 256 54.4 / 44.6.  (The tile kernel sends two steps
-    // ahead: K >= 256.)
-    const int64_t ring_tiles = tiles * ((a.rows_mean + RingLds::kRows - 1) / RingLds::kRows);
-    if (a.K < 256 || a.rows_mean <= 64 || ring_tiles <= 2 * kCus)
-        return launch_ring(a, s);
-    return launch_tile(a, s);
+    switch (choose_expert_kernel(a.load, a.K, a.N, a.gated != 0)) {
+    case ExpertKernel::rows: return launch_rows(a, s);
+    case ExpertKernel::ring: return launch_ring(a, s);
+    default: return launch_tile(a, s);
+    }
 }
 
 }  // namespace moe

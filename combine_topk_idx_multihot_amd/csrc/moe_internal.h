@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "expert_choice.h"
+
 namespace moe {
 
 constexpr int kWave = 64;
@@ -174,9 +176,7 @@ struct ExpertArgs {
     const int32_t *off;     // [EL+1]
     int32_t *status;
     int64_t R;
-    int64_t rows_max;       // most rows the groups can hold: min(R, the worst case)
-    int64_t group_max;      // most rows that one group can hold
-    int64_t rows_mean;      // expected rows of one expert under uniform routing, rounded up
+    ExpertLoad load;        // what the host knows of the groups
     int32_t K, N, EL;
     int32_t NB;             // scale rows of one expert
     int32_t ntn;            // column tiles (set by the launcher)

@@ -151,6 +151,17 @@ def test_swiglu(name, K, I):
     check_swiglu(L, *w, False, f"{name} {K} {I} bf16")
 
 
+@pytest.mark.parametrize("sync_free", [False, True])
+@pytest.mark.parametrize("T,P", [(3, 128), (40, 128), (300, 32)])
+def test_mostly_pad_rows(T, P, sync_free):
+    """Groups of a few tokens padded to many rows."""
+    L = Layer(384, T=T, E=16, k=4, P=P, sync_free=sync_free, seed=T)
+    w = ref.make_weights(16, 2560, 384, L.g)
+    check_gemm(L, *w, f"{T} padded to {P}")
+    check_swiglu(L, *w, True, f"{T} padded to {P} fp8")
+    check_swiglu(L, *w, False, f"{T} padded to {P} bf16")
+
+
 def test_swiglu_saturated_gates():
     """Gates far on both sides: silu(g) -> g and -> 0; a row whose h is 0 takes the floor scale."""
     L = Layer(256, counts=[40, 3])
