@@ -89,3 +89,15 @@ def test_bounds(rule):
     (16384, 8, 128, 16, 1, None, 4096, 1024, True, "tile")])
 def test_choice(rule, T, k, E, EL, P, R, K, N, gated, kernel):
     assert rule(T, k, E, P, K, N, R=R, EL=EL, gated=gated)[1] == kernel
+
+
+def test_deep_gpu_cases_take_the_tall_tiles(rule):
+    """The cases of test_gpu_experts.test_deep_products reach the kernel that they are for."""
+    import test_gpu_experts as gpu
+
+    for name in ("edges", "edges_padded", "large_groups"):
+        counts, P = gpu.LAYERS[name]["counts"], gpu.LAYERS[name].get("P", 1)
+        R = sum(-(-n // P) * P for n in counts)
+        for K in gpu.DEEP:
+            for N, gated in ((2560, False), (1280, True)):
+                assert rule(sum(counts), 1, len(counts), P, K, N, R=R, gated=gated)[1] == "tile", (name, K)

@@ -162,6 +162,30 @@ def test_mostly_pad_rows(T, P, sync_free):
     check_swiglu(L, *w, False, f"{T} padded to {P} bf16")
 
 
+# deep products in tall tiles: 9, 10, 11 and 16 steps of 128 columns, so that a tile's scales are sent
+# for two and three times over and the next tile starts with either set
+DEEP = (1152, 1280, 1408, 2048)
+
+
+@pytest.mark.parametrize("K", DEEP)
+@pytest.mark.parametrize("name", ["edges", "edges_padded", "large_groups"])
+def test_deep_products(name, K):
+    L = Layer(K, seed=K, **LAYERS[name])
+    w = ref.make_weights(L.EL, 2560, K, L.g)
+    check_gemm(L, *w, f"{name} {K}")
+    check_swiglu(L, *w, True, f"{name} {K} fp8")
+    check_swiglu(L, *w, False, f"{name} {K} bf16")
+
+
+@pytest.mark.parametrize("I", [768, 2048])
+def test_deep_gated_products_of_a_share(I):
+    """16 of 128 experts, 32 steps: the ring (I = 768) and the tall tiles (I = 2048)."""
+    L = Layer(4096, T=1500, E=128, k=8, lb=16, EL=16, sync_free=True, seed=I)
+    w = ref.make_weights(16, 2 * I, 4096, L.g)
+    check_swiglu(L, *w, True, f"share {I} fp8")
+    check_swiglu(L, *w, False, f"share {I} bf16")
+
+
 def test_swiglu_saturated_gates():
     """Gates far on both sides: silu(g) -> g and -> 0; a row whose h is 0 takes the floor scale."""
     L = Layer(256, counts=[40, 3])
