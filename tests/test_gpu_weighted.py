@@ -211,6 +211,57 @@ def test_gradients_against_differences():
     assert abs(float(got - (gr.double() * step).sum())) <= slack
 
 
+@pytest.mark.parametrize("sync_free", [False, True])
+def test_row_gradients_against_differences_token_by_token(sync_free):
+    """As above for the rows, along a step whose sign is the gradient's, so that no two terms of a token
+    cancel: D = |Y| / 2 * sign(W g).  Per token, with S = sum |W g step| (the difference itself), the
+    grad rows' rounding to bf16 is within 2^-8 S, and the forward's, at most k roundings of every output
+    at either end, within k u sum |W g| (|Y + D| + |Y - D|) / 2.  The forward and the gradient use the same
+    fp32 W.  A gradient that is zero, negated, without its weight or zero in one row of each token is outside."""
+    c = Case(120, 10, 3, 256, dup=True, sync_free=sync_free)
+    Y, w, g = c.gpu()
+    G = g.double()
+    gr = B.combine_weighted_bwd(c.d, c.h, g, Y, w)[0].double()
+    # every data row's token and merged weight
+    t, j = (i.cuda() for i in c.first.nonzero(as_tuple=True))
+    r, W = c.ros.cuda()[t, j], c.W.cuda()[t, j].double()[:, None]
+    grad = W * G[t]
+    D = Y[r].double().abs() / 2 * torch.sign(grad)
+    ends = []
+    for side in (1, -1):
+        Ys = Y.clone()
+        Ys[r] = (Y[r].double() + side * D).to(torch.bfloat16)
+        out = torch.empty((c.d.T, c.H), device="cuda")
+        B.moe_combine_weighted(c.d, c.h, Ys, c.H, c.R, w, out)
+        ends.append((Ys[r].double(), (out.double() * G).sum(1)))
+    (yp, lp), (ym, lm) = ends
+    step, got = (yp - ym) / 2, (lp - lm) / 2
+
+    def per_token(rows):
+        return torch.zeros(c.d.T, dtype=torch.float64, device="cuda").index_add_(0, t, rows.sum(1))
+
+    slack = per_token(2.0 ** -8 * (grad * step).abs()
+                      + c.d.k * ref.U * grad.abs() * (yp.abs() + ym.abs()) / 2 * (1 + 1e-6))
+
+    def off(rows):
+        return (got - per_token(rows * step)).abs() > slack
+
+    assert not off(gr[r]).any()
+    some = per_token(grad.abs()) > 0
+    assert int(some.sum()) > 100
+    for wrong in (torch.zeros_like(grad), -gr[r]):
+        assert off(wrong)[some].all()
+    one = gr[r].clone()
+    first = c.first.cumsum(1)[c.first].cuda() == 1  # the first row of every token
+    one[first] = 0
+    # leaving that row out takes at least (1 - 2^-8) of its share away: outside the slack where that is
+    # more than twice the slack (a row whose weight is next to nothing is not)
+    share = per_token(first[:, None] * (grad * step).abs()) * (1 - 2.0 ** -8) > 2 * slack
+    assert int(share.sum()) > 100 and off(one)[share].all()
+    far = per_token(((W - 1).abs() > 0.1) * grad.abs()) == per_token(grad.abs())  # no weight near 1
+    assert int((far & some).sum()) > 80 and off(G[t])[far & some].all()
+
+
 def test_prepared_and_streams():
     c = Case(400, 16, 4, 512, P=4)
     Y, w, g = c.gpu()
