@@ -4,8 +4,11 @@ import ctypes
 
 import pytest
 import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+from torch.fx.experimental.proxy_tensor import make_fx
 
 from combine_topk_idx_multihot_amd import binding as B
+from combine_topk_idx_multihot_amd import ops
 
 FAKE = 0x100000  # 16-byte aligned, never dereferenced by validation
 
@@ -151,3 +154,57 @@ def test_outputs_apart():
     for outs, ins in (((a,), (b,)), ((a, b), ()), ((c,), (a, b)), ((a,), (a,)), ((a, None), (buf,))):
         with pytest.raises(B.MoeError, match="overlaps"):
             B._apart(outs, ins)
+
+
+# ---------------------------------------------------------------------------
+# the torch ops, traced with fake tensors
+# ---------------------------------------------------------------------------
+def test_ops_are_registered():
+    for name in ("combine_weighted", "combine_weighted_bwd", "expert_gemm_fp8", "expert_swiglu_fp8"):
+        schema = str(getattr(torch.ops.moe_mi355x, name).default._schema)
+        assert schema.startswith(f"moe_mi355x::{name}(") and "!" not in schema
+
+
+def test_fake_shapes():
+    T, k, E, EL, H, I, P = 70, 4, 64, 24, 512, 384, 4
+    C = T * k + EL * (P - 1)
+    e8 = torch.float8_e4m3fn
+    with FakeTensorMode():
+        x = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+        w = torch.empty((T, k), device="cuda")
+        meta = ops.route(torch.empty((T, k), dtype=torch.int32, device="cuda"), E, 8, EL, P, C)[:6]
+        where = (*meta, E, 8, P, C)
+        q, sc, *_ = ops.dispatch_fp8(x, w, *where, C)
+        w1, s1 = torch.empty((EL, 2 * I, H), dtype=e8, device="cuda"), torch.empty((EL, 6, 4), device="cuda")
+        h, hs = ops.expert_swiglu_fp8(q, sc, w1, s1, *where)
+        assert h.shape == (C, I) and h.dtype == e8 and h.device.type == "cuda"
+        assert hs.shape == (C, I // 128) and hs.dtype == torch.float32
+        w2, s2 = torch.empty((EL, H, I), dtype=e8, device="cuda"), torch.empty((EL, 4, 3), device="cuda")
+        Y = ops.expert_gemm_fp8(h, hs, w2, s2, *where)
+        assert Y.shape == (C, H) and Y.dtype == torch.bfloat16
+        out = ops.combine_weighted(Y, w, *where)
+        assert out.shape == (T, H) and out.dtype == torch.bfloat16
+        gr, dw = ops.combine_weighted_bwd(out, Y, w, *where)
+        assert gr.shape == (C, H) and gr.dtype == torch.bfloat16
+        assert dw.shape == (T, k) and dw.dtype == torch.float32
+        out = ops.moe_layer_fp8(x, torch.empty((T, k), dtype=torch.int64, device="cuda"), w, w1, s1, w2, s2,
+                                E, 8, P, C)
+        assert out.shape == (T, H) and out.dtype == torch.bfloat16
+
+
+def test_weighted_backward_traces_to_its_op():
+    T, k, E, H, P = 32, 2, 8, 256, 1
+    C = T * k
+
+    def step(Y, w, idx, G):
+        Y, w = Y.detach().requires_grad_(True), w.detach().requires_grad_(True)
+        meta = ops.route(idx, E, 0, E, P, C)[:6]
+        out = ops.combine_weighted(Y, w, *meta, E, 0, P, C)
+        return torch.autograd.grad((out.float() * G).sum(), (Y, w))
+
+    g = make_fx(step, tracing_mode="fake")(torch.zeros((C, H), dtype=torch.bfloat16), torch.zeros((T, k)),
+                                           torch.zeros((T, k), dtype=torch.int32), torch.zeros((T, H)))
+    names = [str(n.target) for n in g.graph.nodes if "moe_mi355x" in str(n.target)]
+    assert names == [f"moe_mi355x.{n}.default" for n in ("route", "combine_weighted", "combine_weighted_bwd")]
+    outs = [n for n in g.graph.nodes if n.op == "output"][0].args[0]
+    assert [tuple(o.meta["val"].shape) for o in outs] == [(C, H), (T, k)]
