@@ -16,7 +16,10 @@
 // norm (6e-5 on heavy tails), a hundredth of the bf16 output's rounding; the
 // older 8-bit instructions do the same, and bf16 instructions on widened
 // codes, which are exact to fp32, run at half the rate.  Outputs are therefore
-// bf16 (or E4M3), not fp32.
+// bf16 (or E4M3), not fp32.  Where it shows: a few outputs round the other way.
+// bf16 outputs differ from those of fp32 sums by 2.5e-4 in norm (0.0017 from 64
+// bits on either side), values of requantized E4M3 outputs by 6e-4 to 1.6e-3
+// (0.0022 - 0.0028 from 64 bits; with fp32 sums 0.0021 - 0.0024).
 // Products are taken as w * a^T: a lane of an accumulator then holds one token
 // row and runs of four consecutive output columns, so that its row scale is a
 // single register and its outputs are stored together.
@@ -216,13 +219,19 @@ __global__ void __launch_bounds__(kSplit * kWave) k_expert_rows(ExpertArgs a)
 // What bounds it: per step and CU 128 32x32x64 instructions (16.8 Mflop), 64 KB
 // into LDS and 192 KB out of it, and 1024 wave fmas that bring the blocks' sums
 // under their scales.  At 16384 tokens, top-8 of 128, K = 2048, N = 4096 the
-// matrix units are busy for 51 % of the cycles, and the clock settles at 1.6 -
+// matrix units are busy for 50 % of the cycles, and the clock settles at 1.6 -
 // 1.7 GHz instead of 2.4: the card's power limit, which also makes zeros 15 - 20 %
-// faster than random codes.  There 1216 us, 1.80 PFLOP/s (a library's FP8 product
-// without block scales: 2.62 at 8192^3).  4096 tokens, K = 768, N = 2048 (256 rows per
-// expert, 6 steps a tile): 113 us, 3.2 TB/s.  Gated: 4096 tokens, K = 2048, N = 768
-// 190 us, 1.09 PFLOP/s; 16 of 128 experts, 16384 tokens, K = 4096, N = 1024 189 us,
-// 1.45 PFLOP/s.
+// faster than random codes.  There 1194 - 1271 us over runs and cards, 1.73 - 1.84
+// PFLOP/s (a library's FP8 product without block scales: 2.62 at 8192^3, 3.19 at
+// 16384^3), and 1.4 times the bytes that it needs.  4096 tokens, K = 768, N = 2048
+// (256 rows per expert, 6 steps a tile): 110 - 115 us, 3.1 - 3.3 TB/s: what a step
+// needs is sent in the step before and awaited at its end.  Gated: 4096 tokens, K =
+// 2048, N = 768 184 - 191 us, 1.08 - 1.12 PFLOP/s; 16 of 128 experts, 16384 tokens, K
+// = 4096, N = 1024 182 - 200 us, 1.38 - 1.51 PFLOP/s.
+// At its 256 registers it spills 3 addresses (gated E4M3 12, gated bf16 15).  Before
+// a reload is used the compiler waits for every load in flight: at the first
+// scales of a tile, before the next tile's scales (gated), before the stores of
+// codes (gated E4M3).
 // Measured against it and dropped: 16x16x128 instructions (from registers alone
 // 4.3 PFLOP/s, 32x32x64 5.0), two barriers per step with the waves in two groups
 // (6 - 12 % slower), scales loaded with every step (0.2 - 0.3 us more per step of
@@ -852,11 +861,11 @@ __global__ void __launch_bounds__(kTileWaves * kWave) k_expert_tile(ExpertArgs a
 // their way at any time.  A wave has 32 weight rows (gated: 16 gate and the 16
 // up rows of the same columns).
 // With tiles for every CU the rate is HBM's: 256 tokens, top-8 of 128, K = 768,
-// N = 2048 44 us, 4.9 TB/s; gated, 333 tokens on 32 experts, K = 2048, N = 768 20 -
-// 23 us, 4.4 - 5.2 TB/s.  With fewer, a CU's own: 0.6 us per step of 36 KB, whatever
+// N = 2048 42 - 45 us, 4.7 - 5.1 TB/s; gated, 333 tokens on 32 experts, K = 2048, N = 768
+// 19.7 - 23 us, 4.5 - 5.2 TB/s.  With fewer, a CU's own: 0.6 us per step of 36 KB, whatever
 // the order of its loads and LDS reads, and also where idle CUs had read the
-// weights into the L2 before it.  One token, gated, 48 tiles of 16 steps: 16 us
-// (from HBM to registers, 16 waves per 128 columns: 20 - 22 us); a group of 128
+// weights into the L2 before it.  One token, gated, 48 tiles of 16 steps: 16 - 18 us
+// (from HBM to registers, 16 waves per 128 columns: 20 - 22 us); for E4M3 outputs a group of 128
 // columns shares one scale, so fewer columns per tile are no choice there.
 // ---------------------------------------------------------------------------
 struct RingLds {

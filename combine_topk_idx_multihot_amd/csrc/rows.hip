@@ -768,8 +768,9 @@ __device__ __forceinline__ void list_bwd_upto(int n, const u32x4 *__restrict__ s
 // the token that names the row.  WT: the row's weight is formed from the slot
 // numbers that the wave has loaded for dw, so the list serves the weighted form
 // as it is; scaling costs two products and a conversion per two elements under
-// the memory's time: 16384 tokens, top-8, H = 4096 398 us for 2.28 GB (5.7 TB/s; 407
-// us without weights), 8191 tokens with skewed routing, H = 2048 91 us (5.7 TB/s).
+// the memory's time: 16384 tokens, top-8, H = 4096 394 - 409 us for 2.28 GB (5.6 - 5.8
+// TB/s; 407 us without weights), 8191 tokens with skewed routing, H = 2048 90 - 95 us
+// (5.4 - 5.7 TB/s).
 template <bool WT>
 __device__ __forceinline__ void list_bwd(const RowArgs &a, int64_t pb)
 {
@@ -1471,8 +1472,8 @@ __global__ void __launch_bounds__(kRowThreads) k_dispatch_fp8(RowArgs a)
 // GW: the dispatch backward (also gathers the weight gradients of the slots).
 // WT: every row enters with its weight, by one fma per element, the weights
 // read once per token beside its rows' numbers.  Bound by HBM like the plain
-// form, and as fast: 16384 tokens, top-8, H = 4096 211 - 222 us for 1.21 GB (5.5 -
-// 5.7 TB/s, the plain sum of the same rows 210 us), one token 3.7 us.
+// form, and as fast: 16384 tokens, top-8, H = 4096 212 - 226 us for 1.21 GB (5.3 -
+// 5.7 TB/s, the plain sum of the same rows 210 us), one token 3.7 - 4.1 us.
 template <int SEG, bool OUT_F32, bool GW, bool WT = false>
 __global__ void __launch_bounds__(kRowThreads) k_combine(CombineArgs a)
 {
