@@ -54,6 +54,9 @@ inline ExpertKernel choose_expert_kernel(const ExpertLoad &l, int K, int N, bool
     // r = 16 33.9 / 26.6.  N = 512, E = 64: r = 8 14.6 / 15.6, r = 16 16.3 / 15.6.
     // (Gated, K = 2048, N = 768: E = 1, r = 1 21.0 / 14.6, E = 64 46 / 40: the
     // ring always.)
+    // Groups padded to P, top-8 of 128, K = 768, N = 2048: T = 1: P = 16 6.3 / 9.0, P = 32
+    // 14 / 9.5; T = 3: P = 4 10.0 / 10.2, P = 8 12.4 / 10.8; T = 5: P = 4 15.2 / 16.7 (the ring
+    // by this rule); T = 8, P = 16 22.7 / 19.
     if (!gated && l.group_max <= 32 && tiles * l.rows_mean <= 4 * kCus)
         return ExpertKernel::rows;
     // Tiles of 32 rows while the weights' bytes bound the product, or while
@@ -70,7 +73,8 @@ inline ExpertKernel choose_expert_kernel(const ExpertLoad &l, int K, int N, bool
     // 64.0, 768 86.5 / 68.8; N = 2048: 384 123 / 127, 512 149 / 126, 768 191 / 147; N =
     // 256: 384 19.9 / 22.8, 1024 42.7 / 29.2, 2048 65.2 / 39.4.  N = 768, E = 1: r = 1024 16.0 /
     // 33.5; E = 4: r = 256 16.1 / 33.4, r = 512 27.4 / 34.4; E = 16: r = 64 16.3 / 23.4, r = 128
-    // 27.8 / 28.0, r = 256 50.6 / 36.2 (E4M3 and bf16 outputs within 5 %).
+    // 27.8 / 28.0, r = 256 50.6 / 36.2 (E4M3 outputs; bf16 within 7 %, at N = 256 up to
+    // 16 % less).
     // Groups padded to 128 of 128 experts, K = 768, N = 2048: T = 16 78.9 / 52.1, 64 106 /
     // 69.7, 256 108 / 68.0, 1024 110 / 70.1; K = 2048, N = 4096, T = 1024 423 / 277; gated K =
     // 2048, N = 768: T = 256 167 / 105.  Padded to 16, T = 256: 48.4 / 56.5, gated 74.1 / 93.2.

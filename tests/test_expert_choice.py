@@ -1,5 +1,6 @@
 """CPU: which kernel an experts' product takes (csrc/expert_choice.h), compiled with the host compiler."""
 import os
+import random
 import subprocess
 
 import pytest
@@ -75,6 +76,29 @@ def test_bounds(rule):
             assert load["rows_max"] == (worst if R is None else min(R, worst))
             assert load["group_max"] <= load["rows_max"] and 1 <= load["groups"] <= EL
             assert load["rows_mean"] * load["groups"] >= load["rows_max"] or R is None
+
+
+def test_no_routing_makes_more_groups(rule):
+    """The kernel for few rows launches one slot per group: `groups` is a bound for every routing, also
+    where R cuts the rows off."""
+    rng = random.Random(5)
+    for _ in range(400):
+        E, P, T = rng.choice((1, 3, 8, 40)), rng.choice((1, 2, 5, 16)), rng.randrange(0, 12)
+        k, lb = rng.randint(1, 9), rng.randrange(E)
+        EL = rng.randint(1, E - lb)
+        rows = [0] * EL
+        for _ in range(T):
+            for e in {rng.randrange(-1, E) for _ in range(k)}:
+                if lb <= e < lb + EL:
+                    rows[e - lb] += 1
+        off = [0]
+        for n in rows:
+            off.append(off[-1] + -(-n // P) * P)
+        for R in {None, off[-1], rng.randrange(off[-1] + 1), off[-1] + 7}:
+            cut = [min(o, off[-1] if R is None else R) for o in off]
+            load, _ = rule(T, k, E, P, 512, 256, R=R, EL=EL)
+            assert sum(b > a for a, b in zip(cut, cut[1:])) <= load["groups"] <= EL
+            assert max((b - a for a, b in zip(cut, cut[1:]))) <= load["group_max"]
 
 
 @pytest.mark.parametrize("T,k,E,EL,P,R,K,N,gated,kernel", [
