@@ -10,7 +10,9 @@ namespace moe {
 struct ExpertLoad {
     int64_t rows_max;  // most rows that all of them can hold
     int64_t group_max; // most rows that one can hold
-    int64_t groups;    // most groups there can be
+    int64_t slots;     // most groups there can be, whatever they were padded to: a launch that
+                       // takes one slot per group must have as many
+    int64_t groups;    // the same, groups padded to multiples of P
     int64_t rows_mean; // rows of one of that many, pad rows (computed like any other) among them
 };
 
@@ -25,9 +27,10 @@ inline ExpertLoad expert_load(int64_t T, int64_t k, int64_t E, int64_t EL, int64
     ExpertLoad l;
     l.rows_max = least(R, worst); // whatever capacity the caller chose
     l.group_max = least(up(T, P) * P, l.rows_max);
-    l.groups = least(EL, T * least(k, EL));
-    if (eager)
-        l.groups = least(l.groups, up(l.rows_max, P));
+    l.slots = least(least(EL, T * least(k, EL)), l.rows_max);
+    if (l.slots < 1)
+        l.slots = 1;
+    l.groups = eager ? least(l.slots, up(l.rows_max, P)) : l.slots;
     if (l.groups < 1)
         l.groups = 1;
     // sync-free: uniform routing

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kSplit * kWave) k_expert_rows(ExpertArgs a)
     flag_mismatch(a);
     const int slot = blockIdx.x / a.ntn, ni = blockIdx.x - slot * a.ntn;
     // as many slots as experts, or as groups where those are fewer
-    const int e = __builtin_amdgcn_readfirstlane(a.load.groups < a.EL ? nonempty_expert(a, slot) : slot);
+    const int e = __builtin_amdgcn_readfirstlane(a.load.slots < a.EL ? nonempty_expert(a, slot) : slot);
     if (e < 0)
         return;
     const int64_t r0 = group_begin(a, e), r1 = group_begin(a, e + 1);
@@ -1053,7 +1053,7 @@ static int64_t tiles_max(const ExpertArgs &a, int bm)
 static hipError_t launch_rows(ExpertArgs &a, hipStream_t s)
 {
     a.ntn = (a.N + kRowsCols - 1) / kRowsCols;
-    const int64_t nb = a.load.groups * a.ntn;
+    const int64_t nb = a.load.slots * a.ntn;
     if (nb > 0xFFFFFFFFll / (kSplit * kWave))
         return hipErrorInvalidConfiguration;
     launch(k_expert_rows, dim3(static_cast<unsigned>(nb)), dim3(kSplit * kWave), 0, s, a);

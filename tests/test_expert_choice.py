@@ -17,8 +17,8 @@ int main()
     while (std::scanf("%lld %lld %lld %lld %lld %lld %lld %d %d %d %d", &T, &k, &E, &EL, &P, &worst, &R, &eager,
                       &K, &N, &gated) == 11) {
         const moe::ExpertLoad l = moe::expert_load(T, k, E, EL, P, worst, R, eager != 0);
-        std::printf("%lld %lld %lld %lld %d\n", (long long)l.rows_max, (long long)l.group_max, (long long)l.groups,
-                    (long long)l.rows_mean, static_cast<int>(moe::choose_expert_kernel(l, K, N, gated != 0)));
+        std::printf("%lld %lld %lld %lld %lld %d\n", (long long)l.rows_max, (long long)l.group_max,
+                    (long long)l.slots, (long long)l.groups, (long long)l.rows_mean, static_cast<int>(moe::choose_expert_kernel(l, K, N, gated != 0)));
     }
 }
 """
@@ -40,7 +40,7 @@ def rule(tmp_path_factory):
                                   int(gated))))
         out = subprocess.run([os.path.join(at, "main")], input=line, check=True, text=True,
                              capture_output=True).stdout.split()
-        return dict(zip(("rows_max", "group_max", "groups", "rows_mean"), map(int, out))), KERNELS[int(out[4])]
+        return dict(zip(("rows_max", "group_max", "slots", "groups", "rows_mean"), map(int, out))), KERNELS[int(out[5])]
 
     return ask
 
@@ -79,8 +79,9 @@ def test_bounds(rule):
 
 
 def test_no_routing_makes_more_groups(rule):
-    """The kernel for few rows launches one slot per group: `groups` is a bound for every routing, also
-    where R cuts the rows off."""
+    """The kernel for few rows launches one slot per group: `slots` is a bound for every routing, also
+    where R cuts the rows off or the description of the product names another padding than the route's;
+    `groups` is one for the route's padding."""
     rng = random.Random(5)
     for _ in range(400):
         E, P, T = rng.choice((1, 3, 8, 40)), rng.choice((1, 2, 5, 16)), rng.randrange(0, 12)
@@ -97,7 +98,10 @@ def test_no_routing_makes_more_groups(rule):
         for R in {None, off[-1], rng.randrange(off[-1] + 1), off[-1] + 7}:
             cut = [min(o, off[-1] if R is None else R) for o in off]
             load, _ = rule(T, k, E, P, 512, 256, R=R, EL=EL)
-            assert sum(b > a for a, b in zip(cut, cut[1:])) <= load["groups"] <= EL
+            n = sum(b > a for a, b in zip(cut, cut[1:]))
+            assert n <= load["groups"] <= load["slots"] <= EL
+            if R is not None:
+                assert n <= rule(T, k, E, P + 3, 512, 256, R=R, EL=EL)[0]["slots"]
             assert max((b - a for a, b in zip(cut, cut[1:]))) <= load["group_max"]
 
 
