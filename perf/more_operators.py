@@ -143,21 +143,31 @@ def work(case):
 # ---------------------------------------------------------------------------
 # MXFP4 from elementary operations
 # ---------------------------------------------------------------------------
+def _pow2(e):
+    """2^e as fp32, e in [-126, 127], from its bits (exp2 and ldexp round on some devices)."""
+    return ((e.to(torch.int32) + 127) << 23).view(torch.float32)
+
+
+def _shift(v, e):
+    """v * 2^e, e in [-252, 254], exact while the result is a normal number."""
+    half = torch.div(e, 2, rounding_mode="floor")
+    return v * _pow2(half) * _pow2(e - half)
+
+
 def _mx_quant(v):
     """fp32 [..., K] -> E2M1 code values [..., K / 32, 32] and the blocks' exponents: the largest
     magnitude's power of two over 4, at least 2^-127; nearest codes, ties to even, up to 6."""
     b = v.reshape(*v.shape[:-1], -1, 32)
     e = (torch.frexp(b.abs().amax(-1)).exponent - 3).clamp_min(-127)
     e = torch.where(b.abs().amax(-1) > 0, e, torch.full_like(e, -127))
-    s = torch.ldexp(torch.ones((), device=v.device), -e)[..., None]
-    a = (b * s).abs().clamp_max(6.0)
+    a = _shift(b, -e[..., None]).abs().clamp_max(6.0)
     unit = torch.where(a < 2, 0.5, torch.where(a < 4, 1.0, 2.0))
     return torch.copysign(torch.round(a / unit) * unit, b), e
 
 
 def _mx_values(q, e, shape):
     """bf16 values of codes and exponents (exact: two significant bits)."""
-    return torch.ldexp(q, e[..., None]).reshape(shape).to(torch.bfloat16)
+    return _shift(q, e[..., None]).reshape(shape).to(torch.bfloat16)
 
 
 def _mx_pack(q, e, shape):
@@ -172,8 +182,8 @@ def _mx_unpack(codes, scales):
     """Packed codes [..., K / 2] and E8M0 bytes [..., K / 32] -> fp32 [..., K]."""
     table = torch.tensor([*E2M1, *(-x for x in E2M1)], device=codes.device)
     q = torch.stack((codes & 15, codes >> 4), -1).reshape(*codes.shape[:-1], -1, 32)
-    s = torch.ldexp(torch.ones((), device=codes.device), scales.to(torch.int32) - 127)
-    return (table[q.int()] * s[..., None]).reshape(*codes.shape[:-1], -1)
+    e = scales.to(torch.int32)[..., None] - 127
+    return _shift(table[q.int()], e).reshape(*codes.shape[:-1], -1)
 
 
 def _mx_make(v):
@@ -414,6 +424,11 @@ def run(state):
 # ---------------------------------------------------------------------------
 # the definition in 64 bits
 # ---------------------------------------------------------------------------
+def _exact_pow2(e):
+    """2^e in fp64, e whole, from its bits."""
+    return ((e.to(torch.int64) + 1023) << 52).view(torch.float64)
+
+
 def _exact_mx(v):
     """Values that the MXFP4 codes of v [..., K] stand for: the nearest of the code values, the even
     one of two as near."""
@@ -425,8 +440,8 @@ def _exact_mx(v):
         top = b.abs().amax(-1, keepdim=True)
         power = torch.floor(torch.log2(torch.where(top > 0, top, torch.ones_like(top))))
         # log2 may round up to a whole number just below a power of two
-        power = torch.where(torch.exp2(power) > top, power - 1, power)
-        s = torch.exp2((power - 2).clamp_min(-127.0))
+        power = torch.where(_exact_pow2(power) > top, power - 1, power)
+        s = _exact_pow2((power - 2).clamp_min(-127.0))
         a = (b.abs() / s).clamp_max(6.0)
         above = torch.searchsorted(grid, a.contiguous()).clamp(1, 7)
         under = above - 1
@@ -452,10 +467,10 @@ def _exact_unpack(codes, scales):
     b = torch.empty((codes.shape[0], codes.shape[1] * 2), dtype=torch.long, device=codes.device)
     b[:, 0::2], b[:, 1::2] = codes.long() % 16, codes.long() // 16
     mag = b % 8
-    v = torch.where(mag < 2, mag / 2.0, (1 + 0.5 * (mag % 2)) * torch.exp2((mag // 2 - 1).double()))
+    v = torch.where(mag < 2, mag / 2.0, (1 + 0.5 * (mag % 2)) * _exact_pow2(mag // 2 - 1))
     v = torch.where(b >= 8, -v.double(), v.double())
     kb = torch.arange(v.shape[1], device=codes.device) // 32
-    return v * torch.exp2(scales.double() - 127.0)[:, kb]
+    return v * _exact_pow2(scales.long() - 127)[:, kb]
 
 
 def exact(case, seed):
