@@ -40,7 +40,8 @@ EXPORTS = ("moe_capacity_min", "moe_route_workspace_size", "moe_route_build",
            "moe_route_build_noalloc", "moe_route_dispatch", "moe_dispatch",
            "moe_dispatch_fp8", "moe_combine", "moe_combine_bwd", "moe_dispatch_bwd",
            "moe_combine_weighted", "moe_combine_weighted_bwd", "moe_expert_gemm_fp8",
-           "moe_expert_swiglu_fp8",
+           "moe_expert_swiglu_fp8", "moe_quantize_mxfp4", "moe_dequantize_mxfp4",
+           "moe_dispatch_mxfp4", "moe_expert_gemm_mxfp4", "moe_expert_swiglu_mxfp4",
            "moe_last_error", "moe_device_check", "moe_time_next_call")
 
 
@@ -104,6 +105,16 @@ def lib() -> ctypes.CDLL:
         L.moe_expert_gemm_fp8.restype = ctypes.c_int
         L.moe_expert_swiglu_fp8.argtypes = [pd, ph, vp, vp, i32, i64, vp, vp, i32, vp, vp, vp]
         L.moe_expert_swiglu_fp8.restype = ctypes.c_int
+        L.moe_quantize_mxfp4.argtypes = [vp, i32, i64, i32, vp, vp, vp]
+        L.moe_quantize_mxfp4.restype = ctypes.c_int
+        L.moe_dequantize_mxfp4.argtypes = [vp, vp, i64, i32, vp, i32, vp]
+        L.moe_dequantize_mxfp4.restype = ctypes.c_int
+        L.moe_dispatch_mxfp4.argtypes = [pd, ph, vp, i32, vp, i64, vp, vp, vp, vp, vp, vp]
+        L.moe_dispatch_mxfp4.restype = ctypes.c_int
+        L.moe_expert_gemm_mxfp4.argtypes = [pd, ph, vp, vp, i32, i64, vp, vp, i32, vp, vp]
+        L.moe_expert_gemm_mxfp4.restype = ctypes.c_int
+        L.moe_expert_swiglu_mxfp4.argtypes = [pd, ph, vp, vp, i32, i64, vp, vp, i32, vp, vp, vp]
+        L.moe_expert_swiglu_mxfp4.restype = ctypes.c_int
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = ctypes.c_char_p
         L.moe_device_check.argtypes = [ctypes.c_int]
@@ -603,13 +614,23 @@ def moe_combine_weighted_bwd(desc: Desc, handle: Handle, grad_out: torch.Tensor,
                                                  p_w, R, p_gr, p_dw, _stream(stream)))
 
 
-def _product_ptrs(desc, handle, rows_q, row_scale, K, cap, w_q, w_scale, n):
+# MXFP4: two E2M1 codes a byte, E8M0 scale bytes
+_FP4 = (torch.uint8,) + ((torch.float4_e2m1fn_x2,) if hasattr(torch, "float4_e2m1fn_x2") else ())
+_E8M0 = (torch.uint8,) + ((torch.float8_e8m0fnu,) if hasattr(torch, "float8_e8m0fnu") else ())
+
+
+def _product_ptrs(desc, handle, rows_q, row_scale, K, cap, w_q, w_scale, n, mx=False):
     """Checked pointers of a product with n weight rows per expert."""
     _handle_here(handle, desc)
     _here(rows_q, row_scale, w_q, w_scale)
     K, EL = _int32("K", K), desc.num_local
     if not cap:
         return None, None, None, None
+    if mx:
+        return (_dev(rows_q, "rows_q", _FP4, cap * (K // 2)),
+                _dev(row_scale, "row_scale", _E8M0, cap * (K // 32)),
+                _dev(w_q, "w_q", _FP4, EL * n * (K // 2)),
+                _dev(w_scale, "w_scale", _E8M0, EL * n * (K // 32)))
     return (_dev(rows_q, "rows_q", _FP8, cap * K),
             _dev(row_scale, "row_scale", _F32, cap * (K // 128)),
             _dev(w_q, "w_q", _FP8, EL * n * K),
@@ -628,13 +649,18 @@ def moe_expert_gemm_fp8(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_sc
                                             p[2], p[3], N, p_o, _stream(stream)))
 
 
-def _swiglu_out(out, out_scale, cap, I):
+def _swiglu_out(out, out_scale, cap, I, mx=False):
     _here(out, out_scale)
     if (out.dtype == torch.bfloat16) != (out_scale is None):
-        raise MoeError(MOE_ERR_ARG, "out is bfloat16 without out_scale, or E4M3 codes "
-                                    "(float8_e4m3fn or uint8) with it")
+        raise MoeError(MOE_ERR_ARG, "out is bfloat16 without out_scale, or " +
+                       ("MXFP4 codes (uint8)" if mx else "E4M3 codes (float8_e4m3fn or uint8)") +
+                       " with it")
     if not cap:  # nothing to write
         return None, None
+    if mx:
+        p_o = _dev(out, "out", _BF16 if out_scale is None else _FP4,
+                   cap * (I if out_scale is None else I // 2))
+        return p_o, _dev(out_scale, "out_scale", _E8M0, cap * (I // 32), optional=True)
     p_o = _dev(out, "out", _BF16 if out_scale is None else _FP8, cap * I)
     return p_o, _dev(out_scale, "out_scale", _F32, cap * (I // 128), optional=True)
 
@@ -650,6 +676,86 @@ def moe_expert_swiglu_fp8(desc: Desc, handle: Handle, rows_q: torch.Tensor,
     _apart((out, out_scale), (rows_q, row_scale, w_q, w_scale))
     return _check(lib().moe_expert_swiglu_fp8(ctypes.byref(desc), handle.cref(), p[0], p[1], K, R,
                                               p[2], p[3], I, p_o, p_s, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# microscaled 4-bit floats (MXFP4)
+# ---------------------------------------------------------------------------
+
+def _mx_ptrs(values, name, n, K, q, scale):
+    _here(values, q, scale)
+    n, K = _int32("n", n), _int32("K", K)
+    if not n:
+        return None, None, None
+    return (_dev(values, name, _BF16_F32, n * K), _dev(q, "q", _FP4, n * (K // 2)),
+            _dev(scale, "scale", _E8M0, n * (K // 32)))
+
+
+def moe_quantize_mxfp4(x: torch.Tensor, n: int, K: int, q: torch.Tensor, scale: torch.Tensor,
+                       stream=None) -> int:
+    """q [n,K/2] and scale [n,K/32] uint8 = x [n,K] bf16 or fp32 in MXFP4."""
+    p_x, p_q, p_s = _mx_ptrs(x, "x", n, K, q, scale)
+    _apart((q, scale), (x,))
+    return _check(lib().moe_quantize_mxfp4(p_x, int(x.dtype == torch.float32), n, K, p_q, p_s,
+                                           _stream(stream)))
+
+
+def moe_dequantize_mxfp4(q: torch.Tensor, scale: torch.Tensor, n: int, K: int, out: torch.Tensor,
+                         stream=None) -> int:
+    """out [n,K] bf16 or fp32 = the values of MXFP4 codes q [n,K/2] and scale [n,K/32]."""
+    p_o, p_q, p_s = _mx_ptrs(out, "out", n, K, q, scale)
+    _apart((out,), (q, scale))
+    return _check(lib().moe_dequantize_mxfp4(p_q, p_s, n, K, p_o, int(out.dtype == torch.float32),
+                                             _stream(stream)))
+
+
+def moe_dispatch_mxfp4(desc: Desc, handle: Handle, x: torch.Tensor, H: int, R: int,
+                       rows_q: torch.Tensor, row_scale: torch.Tensor,
+                       topk_w: torch.Tensor | None = None, row_w: torch.Tensor | None = None,
+                       row_token: torch.Tensor | None = None,
+                       row_expert: torch.Tensor | None = None, stream=None) -> int:
+    _handle_here(handle, desc)
+    _here(x, rows_q, row_scale, topk_w, row_w, row_token, row_expert)
+    H = _int32("H", H)
+    p_x = _dev(x, "x", _BF16, desc.T * H) if desc.T else None
+    p_q = _dev(rows_q, "rows_q", _FP4, R * (H // 2)) if R else None
+    p_s = _dev(row_scale, "row_scale", _E8M0, R * (H // 32)) if R else None
+    p_w = _dev(topk_w, "topk_w", _F32, desc.T * desc.k, optional=True)
+    p_rw = _dev(row_w, "row_w", _F32, R, optional=True)
+    if desc.T == 0:
+        p_w = None
+    if R == 0:  # no row to weight; the C ABI pairs the two pointers
+        p_rw = p_w = None
+    p_rt = _dev(row_token, "row_token", _I32, R, optional=True)
+    p_re = _dev(row_expert, "row_expert", _I32, R, optional=True)
+    _apart((rows_q, row_scale, row_w, row_token, row_expert), (x, topk_w))
+    return _check(lib().moe_dispatch_mxfp4(ctypes.byref(desc), handle.cref(), p_x, H, p_w, R, p_q,
+                                           p_s, p_rw, p_rt, p_re, _stream(stream)))
+
+
+def moe_expert_gemm_mxfp4(desc: Desc, handle: Handle, rows_q: torch.Tensor,
+                          row_scale: torch.Tensor, K: int, R: int, w_q: torch.Tensor,
+                          w_scale: torch.Tensor, N: int, out: torch.Tensor, stream=None) -> int:
+    """out [R,N] bf16 = every expert's MXFP4 rows times its MXFP4 weights [EL,N,K/2]."""
+    p = _product_ptrs(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, _int32("N", N), True)
+    _here(out)
+    p_o = _dev(out, "out", _BF16, R * N) if R else None
+    _apart((out,), (rows_q, row_scale, w_q, w_scale))
+    return _check(lib().moe_expert_gemm_mxfp4(ctypes.byref(desc), handle.cref(), p[0], p[1], K, R,
+                                              p[2], p[3], N, p_o, _stream(stream)))
+
+
+def moe_expert_swiglu_mxfp4(desc: Desc, handle: Handle, rows_q: torch.Tensor,
+                            row_scale: torch.Tensor, K: int, R: int, w_q: torch.Tensor,
+                            w_scale: torch.Tensor, I: int, out: torch.Tensor,
+                            out_scale: torch.Tensor | None = None, stream=None) -> int:
+    """h = silu(gate) * up of the product with w_q [EL,2I,K/2] (gate rows first): out [R,I] bf16,
+    or, with out_scale [R,I/32], out [R,I/2] MXFP4 codes."""
+    p = _product_ptrs(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, 2 * _int32("I", I), True)
+    p_o, p_s = _swiglu_out(out, out_scale, R, I, True)
+    _apart((out, out_scale), (rows_q, row_scale, w_q, w_scale))
+    return _check(lib().moe_expert_swiglu_mxfp4(ctypes.byref(desc), handle.cref(), p[0], p[1], K, R,
+                                                p[2], p[3], I, p_o, p_s, _stream(stream)))
 
 
 class _Prepared:
@@ -727,6 +833,38 @@ class PreparedExpertSwigluFp8(_Prepared):
         p_o, p_s = _swiglu_out(out, out_scale, cap, I)
         _apart((out, out_scale), (rows_q, row_scale, w_q, w_scale))
         self._bind(lib().moe_expert_swiglu_fp8, desc, handle, (p[0], p[1], K),
+                   (p[2], p[3], I, p_o, p_s, _stream(stream)), cap,
+                   (rows_q, row_scale, w_q, w_scale, out, out_scale))
+
+
+class PreparedExpertGemmMxfp4(_Prepared):
+    """moe_expert_gemm_mxfp4 over up to min(rows_q, out) rows, checked once."""
+
+    def __init__(self, desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scale: torch.Tensor,
+                 K: int, w_q: torch.Tensor, w_scale: torch.Tensor, N: int, out: torch.Tensor,
+                 stream=None):
+        cap = min(2 * rows_q.numel() // _positive("K", K), out.numel() // _positive("N", N))
+        p = _product_ptrs(desc, handle, rows_q, row_scale, K, cap, w_q, w_scale, N, True)
+        _here(out)
+        p_o = _dev(out, "out", _BF16, cap * N) if cap else None
+        _apart((out,), (rows_q, row_scale, w_q, w_scale))
+        self._bind(lib().moe_expert_gemm_mxfp4, desc, handle, (p[0], p[1], K),
+                   (p[2], p[3], N, p_o, _stream(stream)), cap,
+                   (rows_q, row_scale, w_q, w_scale, out))
+
+
+class PreparedExpertSwigluMxfp4(_Prepared):
+    """moe_expert_swiglu_mxfp4 over up to min(rows_q, out) rows, checked once."""
+
+    def __init__(self, desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scale: torch.Tensor,
+                 K: int, w_q: torch.Tensor, w_scale: torch.Tensor, I: int, out: torch.Tensor,
+                 out_scale: torch.Tensor | None = None, stream=None):
+        per_row = _positive("I", I) if out_scale is None else max(1, I // 2)
+        cap = min(2 * rows_q.numel() // _positive("K", K), out.numel() // per_row)
+        p = _product_ptrs(desc, handle, rows_q, row_scale, K, cap, w_q, w_scale, 2 * I, True)
+        p_o, p_s = _swiglu_out(out, out_scale, cap, I, True)
+        _apart((out, out_scale), (rows_q, row_scale, w_q, w_scale))
+        self._bind(lib().moe_expert_swiglu_mxfp4, desc, handle, (p[0], p[1], K),
                    (p[2], p[3], I, p_o, p_s, _stream(stream)), cap,
                    (rows_q, row_scale, w_q, w_scale, out, out_scale))
 
@@ -947,6 +1085,86 @@ def expert_swiglu_fp8(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scal
     moe_expert_swiglu_fp8(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, I, out, out_scale,
                           stream=stream)
     return out, out_scale
+
+
+def quantize_mxfp4(x: torch.Tensor, stream=None):
+    """moe_quantize_mxfp4 of x [...,K] bf16 or fp32 with fresh outputs: (q [...,K/2], scale
+    [...,K/32]), uint8."""
+    K = x.shape[-1]
+    if K % 32:
+        raise MoeError(MOE_ERR_ARG, f"K must be a positive multiple of 32 (got {K})")
+    q = torch.empty((*x.shape[:-1], K // 2), dtype=torch.uint8, device=x.device)
+    scale = torch.empty((*x.shape[:-1], K // 32), dtype=torch.uint8, device=x.device)
+    moe_quantize_mxfp4(x, x.numel() // max(K, 1), K, q, scale, stream=stream)
+    return q, scale
+
+
+def dequantize_mxfp4(q: torch.Tensor, scale: torch.Tensor, out_dtype=torch.bfloat16, stream=None):
+    """moe_dequantize_mxfp4 with a fresh output [...,K]."""
+    K = 2 * q.shape[-1]
+    if tuple(scale.shape) != (*q.shape[:-1], K // 32):
+        raise MoeError(MOE_ERR_ARG, f"scale must be {[*q.shape[:-1], K // 32]} "
+                                    f"(got {tuple(scale.shape)})")
+    out = torch.empty((*q.shape[:-1], K), dtype=out_dtype, device=q.device)
+    moe_dequantize_mxfp4(q, scale, out.numel() // max(K, 1), K, out, stream=stream)
+    return out
+
+
+def dispatch_mxfp4(desc: Desc, handle: Handle, x: torch.Tensor, topk_w: torch.Tensor | None = None,
+                   meta: bool = True, stream=None):
+    """moe_dispatch_mxfp4 with fresh outputs: (rows_q [R,H/2], row_scale [R,H/32], row_w, row_token,
+    row_expert)."""
+    R, H, dev = rows_for(desc, handle), x.shape[1], x.device
+    rows_q = torch.empty((R, H // 2), dtype=torch.uint8, device=dev)
+    row_scale = torch.empty((R, H // 32), dtype=torch.uint8, device=dev)
+    row_w = torch.empty(R, dtype=torch.float32, device=dev) if topk_w is not None else None
+    rt = torch.empty(R, dtype=torch.int32, device=dev) if meta else None
+    re = torch.empty(R, dtype=torch.int32, device=dev) if meta else None
+    moe_dispatch_mxfp4(desc, handle, x, H, R, rows_q, row_scale, topk_w, row_w, rt, re,
+                       stream=stream)
+    return rows_q, row_scale, row_w, rt, re
+
+
+def expert_gemm_mxfp4(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scale: torch.Tensor,
+                      w_q: torch.Tensor, w_scale: torch.Tensor, stream=None):
+    """moe_expert_gemm_mxfp4 with a fresh output [R,N] bf16 (its rows past the total are not written)."""
+    R, K, N = rows_q.shape[0], 2 * rows_q.shape[1], w_q.shape[1]
+    _mx_shapes_fit(desc, rows_q, row_scale, w_q, w_scale)
+    out = torch.empty((R, N), dtype=torch.bfloat16, device=rows_q.device)
+    moe_expert_gemm_mxfp4(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, N, out, stream=stream)
+    return out
+
+
+def expert_swiglu_mxfp4(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scale: torch.Tensor,
+                        w_q: torch.Tensor, w_scale: torch.Tensor, out_dtype=torch.uint8,
+                        stream=None):
+    """moe_expert_swiglu_mxfp4 with fresh outputs (rows past the total are not written): (h [R,I/2]
+    codes, h_scale [R,I/32]), uint8, or with out_dtype=torch.bfloat16 (h [R,I], None)."""
+    R, K, I = rows_q.shape[0], 2 * rows_q.shape[1], w_q.shape[1] // 2
+    _mx_shapes_fit(desc, rows_q, row_scale, w_q, w_scale)
+    if w_q.shape[1] % 2:
+        raise MoeError(MOE_ERR_ARG, f"w_q needs 2I rows per expert (got {w_q.shape[1]})")
+    if out_dtype == torch.bfloat16:
+        out, out_scale = torch.empty((R, I), dtype=out_dtype, device=rows_q.device), None
+    else:
+        out = torch.empty((R, I // 2), dtype=out_dtype, device=rows_q.device)
+        out_scale = torch.empty((R, I // 32), dtype=torch.uint8, device=rows_q.device)
+    moe_expert_swiglu_mxfp4(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, I, out, out_scale,
+                            stream=stream)
+    return out, out_scale
+
+
+def _mx_shapes_fit(desc, rows_q, row_scale, w_q, w_scale):
+    R, half = rows_q.shape
+    if w_q.dim() != 3 or w_q.shape[0] != desc.num_local or w_q.shape[2] != half:
+        raise MoeError(MOE_ERR_ARG, f"w_q must be [EL,N,K/2] with EL={desc.num_local} and K/2={half} "
+                                    f"(got {tuple(w_q.shape)})")
+    blocks = (desc.num_local, w_q.shape[1], half // 16)
+    if tuple(w_scale.shape) != blocks:
+        raise MoeError(MOE_ERR_ARG, f"w_scale must be {list(blocks)} (got {tuple(w_scale.shape)})")
+    if tuple(row_scale.shape) != (R, half // 16):
+        raise MoeError(MOE_ERR_ARG, f"row_scale must be {[R, half // 16]} "
+                                    f"(got {tuple(row_scale.shape)})")
 
 
 def _shapes_fit(desc, rows_q, row_scale, w_q, w_scale):

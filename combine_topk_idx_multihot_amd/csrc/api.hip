@@ -219,14 +219,15 @@ int check_dispatch(const moe_desc *desc, const moe_handle *handle, const uint16_
 
 // One launch of the dispatch: bf16 rows, or (rows_q set) E4M3 rows and scales.
 // The arguments and launch shape of one dispatch: bf16 rows, or (rows_q set)
-// E4M3 rows and scales.
+// E4M3 rows and scales, with mx MXFP4 rows and scales.
 moe::RowArgs dispatch_args(const moe_desc *desc, const moe_handle *handle, const uint16_t *x,
                            int32_t H, const float *topk_w, int64_t R, uint16_t *rows,
                            uint8_t *rows_q, float *row_scale, float *row_w, int32_t *row_token,
-                           int32_t *row_expert, bool keep_tail)
+                           int32_t *row_expert, bool keep_tail, bool mx = false)
 {
     moe::RowArgs a;
     a.keep_tail = keep_tail;
+    a.mx = mx;
     a.src = x;
     a.topk_w = topk_w;
     a.F = nullptr;
@@ -254,10 +255,9 @@ moe::RowArgs dispatch_args(const moe_desc *desc, const moe_handle *handle, const
     return a;
 }
 
-// Argument rules shared by the experts' products.
-int check_product(const moe_desc *desc, const moe_handle *handle, const uint8_t *rows_q,
-                  const float *row_scale, int32_t K, int64_t R, const uint8_t *w_q,
-                  const float *w_scale)
+// Argument rules shared by the experts' products on E4M3 and on MXFP4 rows.
+int check_product(const moe_desc *desc, const moe_handle *handle, const void *rows_q,
+                  const void *row_scale, int32_t K, int64_t R, const void *w_q, const void *w_scale)
 {
     int rc;
     if ((rc = check_desc(desc)) != MOE_OK)
@@ -269,49 +269,125 @@ int check_product(const moe_desc *desc, const moe_handle *handle, const uint8_t 
     if (K <= 0 || K % 128 != 0 || K > (1 << 23))
         return fail(MOE_ERR_ARG, "K must be a positive multiple of 128 up to 2^23 (got %d)", K);
     if (R > 0 && (!rows_q || !aligned16(rows_q)))
-        return fail(MOE_ERR_ARG, "rows_q must be a non-NULL, 16-byte aligned [R,K] byte tensor");
+        return fail(MOE_ERR_ARG, "rows_q must be a non-NULL, 16-byte aligned byte tensor of R rows");
     if (R > 0 && (!row_scale || !aligned16(row_scale)))
-        return fail(MOE_ERR_ARG, "row_scale must be a non-NULL, 16-byte aligned [R,K/128] fp32 "
-                                 "tensor");
+        return fail(MOE_ERR_ARG, "row_scale must be a non-NULL, 16-byte aligned tensor of R rows");
     if (R > 0 && (!w_q || !aligned16(w_q)))
-        return fail(MOE_ERR_ARG, "w_q must be a non-NULL, 16-byte aligned [EL,N,K] byte tensor");
+        return fail(MOE_ERR_ARG, "w_q must be a non-NULL, 16-byte aligned byte tensor of EL experts");
     if (R > 0 && (!w_scale || !aligned16(w_scale)))
-        return fail(MOE_ERR_ARG, "w_scale must be a non-NULL, 16-byte aligned fp32 tensor");
+        return fail(MOE_ERR_ARG, "w_scale must be a non-NULL, 16-byte aligned tensor of EL experts");
     return MOE_OK;
 }
 
-// The arguments that both products share.
-moe::ExpertArgs product_args(const moe_desc *desc, const moe_handle *handle, const uint8_t *rows_q,
-                             const float *row_scale, int32_t K, int64_t R, const uint8_t *w_q,
-                             const float *w_scale)
+int check_gemm_out(int32_t N, int64_t R, const void *out)
 {
-    moe::ExpertArgs a;
-    a.a = rows_q;
-    a.sa = row_scale;
-    a.w = w_q;
-    a.sw = w_scale;
+    if (N <= 0 || N % 8 != 0 || N > (1 << 30))
+        return fail(MOE_ERR_ARG, "N must be a positive multiple of 8 up to 2^30 (got %d)", N);
+    if (R > 0 && (!out || !aligned16(out)))
+        return fail(MOE_ERR_ARG, "out must be a non-NULL, 16-byte aligned [R,N] bf16 tensor");
+    return MOE_OK;
+}
+
+int check_swiglu_out(int32_t I, int64_t R, const void *out, const void *out_scale)
+{
+    if (I <= 0 || I % 128 != 0 || I > (1 << 29))
+        return fail(MOE_ERR_ARG, "I must be a positive multiple of 128 up to 2^29 (got %d)", I);
+    if (R > 0 && (!out || !aligned16(out)))
+        return fail(MOE_ERR_ARG, "out must be a non-NULL, 16-byte aligned [R,I] tensor");
+    if (out_scale && !aligned16(out_scale))
+        return fail(MOE_ERR_ARG, "out_scale must be 16-byte aligned");
+    return MOE_OK;
+}
+
+// The arguments that the products share.
+void product_args(moe::ProductArgs &a, const moe_desc *desc, const moe_handle *handle, int32_t K, int64_t R,
+                  int32_t N, bool gated, void *out)
+{
+    a.out = out;
     a.off = handle->padded_offsets;
     a.status = handle->status;
     a.R = R;
     a.load = moe::expert_load(desc->T, desc->k, desc->E, desc->num_local, desc->pad_multiple, cap_min(desc), R,
                               desc->mode == MOE_EAGER);
     a.K = K;
+    a.N = N;
     a.EL = desc->num_local;
+    a.gated = gated;
     a.eager = desc->mode == MOE_EAGER;
-    return a;
+}
+
+// One launch of a product on E4M3 rows.
+int launch_product(const moe_desc *desc, const moe_handle *handle, const uint8_t *rows_q,
+                   const float *row_scale, int32_t K, int64_t R, const uint8_t *w_q, const float *w_scale,
+                   int32_t N, bool gated, void *out, float *out_scale, void *stream)
+{
+    moe::ExpertArgs a;
+    product_args(a, desc, handle, K, R, N, gated, out);
+    a.a = rows_q;
+    a.sa = row_scale;
+    a.w = w_q;
+    a.sw = w_scale;
+    a.out_scale = out_scale;
+    a.NB = gated ? N / 64 : (N + 127) / 128;
+    if (a.load.rows_max == 0)
+        return ok();
+    hipError_t e = moe::launch_expert_product(a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess)
+        return hip_fail(e, gated ? "expert_swiglu_fp8 launch" : "expert_gemm_fp8 launch");
+    return ok();
+}
+
+// One launch of a product on MXFP4 rows.
+int launch_product_mx(const moe_desc *desc, const moe_handle *handle, const uint8_t *rows_q,
+                      const uint8_t *row_scale, int32_t K, int64_t R, const uint8_t *w_q, const uint8_t *w_scale,
+                      int32_t N, bool gated, void *out, uint8_t *out_scale, void *stream)
+{
+    moe::MxExpertArgs a;
+    product_args(a, desc, handle, K, R, N, gated, out);
+    a.a = rows_q;
+    a.sa = row_scale;
+    a.w = w_q;
+    a.sw = w_scale;
+    a.out_scale = out_scale;
+    if (a.load.rows_max == 0)
+        return ok();
+    hipError_t e = moe::launch_expert_product_mx(a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess)
+        return hip_fail(e, gated ? "expert_swiglu_mxfp4 launch" : "expert_gemm_mxfp4 launch");
+    return ok();
+}
+
+// Argument rules shared by the quantization to MXFP4 and the way back, and its
+// arguments.
+int check_mx(int64_t n, int32_t K, const void *codes, const void *scales, const void *values, int32_t is_f32,
+             const char *name)
+{
+    if (n < 0 || n > kI32Max)
+        return fail(MOE_ERR_ARG, "n must be in [0, 2^31) (got %lld)", (long long)n);
+    if (K <= 0 || K % 32 != 0)
+        return fail(MOE_ERR_ARG, "K must be a positive multiple of 32 (got %d)", K);
+    if (is_f32 != 0 && is_f32 != 1)
+        return fail(MOE_ERR_ARG, "%s_is_f32 must be 0 or 1 (got %d)", name, is_f32);
+    if (n > 0 && (!values || !aligned16(values)))
+        return fail(MOE_ERR_ARG, "%s must be a non-NULL, 16-byte aligned [n,K] tensor", name);
+    if (n > 0 && (!codes || !aligned16(codes)))
+        return fail(MOE_ERR_ARG, "q must be a non-NULL, 16-byte aligned [n,K/2] byte tensor");
+    if (n > 0 && (!scales || !aligned16(scales)))
+        return fail(MOE_ERR_ARG, "scale must be a non-NULL, 16-byte aligned [n,K/32] byte tensor");
+    return MOE_OK;
 }
 
 // One launch of the dispatch.
 int launch_dispatch(const moe_desc *desc, const moe_handle *handle, const uint16_t *x, int32_t H,
                     const float *topk_w, int64_t R, uint16_t *rows, uint8_t *rows_q,
                     float *row_scale, float *row_w, int32_t *row_token, int32_t *row_expert,
-                    void *stream)
+                    void *stream, bool mx = false)
 {
     const moe::RowArgs a = dispatch_args(desc, handle, x, H, topk_w, R, rows, rows_q, row_scale,
-                                         row_w, row_token, row_expert, false);
+                                         row_w, row_token, row_expert, false, mx);
     hipError_t e = moe::launch_move_rows(a, static_cast<hipStream_t>(stream));
     if (e != hipSuccess)
-        return hip_fail(e, rows_q ? "fp8 dispatch launch" : "dispatch launch");
+        return hip_fail(e, mx ? "mxfp4 dispatch launch" : rows_q ? "fp8 dispatch launch" : "dispatch launch");
     return ok();
 }
 
@@ -917,22 +993,9 @@ int moe_expert_gemm_fp8(const moe_desc *desc, const moe_handle *handle, const ui
     int rc;
     if ((rc = check_product(desc, handle, rows_q, row_scale, K, R, w_q, w_scale)) != MOE_OK)
         return rc;
-    if (N <= 0 || N % 8 != 0 || N > (1 << 30))
-        return fail(MOE_ERR_ARG, "N must be a positive multiple of 8 up to 2^30 (got %d)", N);
-    if (R > 0 && (!out || !aligned16(out)))
-        return fail(MOE_ERR_ARG, "out must be a non-NULL, 16-byte aligned [R,N] bf16 tensor");
-    moe::ExpertArgs a = product_args(desc, handle, rows_q, row_scale, K, R, w_q, w_scale);
-    a.out = out;
-    a.out_scale = nullptr;
-    a.N = N;
-    a.NB = (N + 127) / 128;
-    a.gated = 0;
-    if (a.load.rows_max == 0)
-        return ok();
-    hipError_t e = moe::launch_expert_product(a, static_cast<hipStream_t>(stream));
-    if (e != hipSuccess)
-        return hip_fail(e, "expert_gemm_fp8 launch");
-    return ok();
+    if ((rc = check_gemm_out(N, R, out)) != MOE_OK)
+        return rc;
+    return launch_product(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, N, false, out, nullptr, stream);
 }
 
 int moe_expert_swiglu_fp8(const moe_desc *desc, const moe_handle *handle, const uint8_t *rows_q,
@@ -944,24 +1007,94 @@ int moe_expert_swiglu_fp8(const moe_desc *desc, const moe_handle *handle, const 
     int rc;
     if ((rc = check_product(desc, handle, rows_q, row_scale, K, R, w_q, w_scale)) != MOE_OK)
         return rc;
-    if (I <= 0 || I % 128 != 0 || I > (1 << 29))
-        return fail(MOE_ERR_ARG, "I must be a positive multiple of 128 up to 2^29 (got %d)", I);
-    if (R > 0 && (!out || !aligned16(out)))
-        return fail(MOE_ERR_ARG, "out must be a non-NULL, 16-byte aligned [R,I] tensor");
-    if (out_scale && !aligned16(out_scale))
-        return fail(MOE_ERR_ARG, "out_scale must be 16-byte aligned");
-    moe::ExpertArgs a = product_args(desc, handle, rows_q, row_scale, K, R, w_q, w_scale);
-    a.out = out;
-    a.out_scale = out_scale;
-    a.N = I;
-    a.NB = I / 64;
-    a.gated = 1;
-    if (a.load.rows_max == 0)
+    if ((rc = check_swiglu_out(I, R, out, out_scale)) != MOE_OK)
+        return rc;
+    return launch_product(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, I, true, out, out_scale, stream);
+}
+
+int moe_quantize_mxfp4(const void *x, int32_t x_is_f32, int64_t n, int32_t K, uint8_t *q, uint8_t *scale,
+                       void *stream)
+{
+    TimingScope timing_scope;
+    int rc;
+    if ((rc = check_mx(n, K, q, scale, x, x_is_f32, "x")) != MOE_OK)
+        return rc;
+    if (n == 0)
         return ok();
-    hipError_t e = moe::launch_expert_product(a, static_cast<hipStream_t>(stream));
+    moe::MxArgs a;
+    a.values = x;
+    a.out = nullptr;
+    a.codes = q;
+    a.scales = scale;
+    a.chunks = n * (K / 8);
+    hipError_t e = moe::launch_quantize_mx(a, x_is_f32, static_cast<hipStream_t>(stream));
     if (e != hipSuccess)
-        return hip_fail(e, "expert_swiglu_fp8 launch");
+        return hip_fail(e, "quantize_mxfp4 launch");
     return ok();
+}
+
+int moe_dequantize_mxfp4(const uint8_t *q, const uint8_t *scale, int64_t n, int32_t K, void *out,
+                         int32_t out_is_f32, void *stream)
+{
+    TimingScope timing_scope;
+    int rc;
+    if ((rc = check_mx(n, K, q, scale, out, out_is_f32, "out")) != MOE_OK)
+        return rc;
+    if (n == 0)
+        return ok();
+    moe::MxArgs a;
+    a.values = nullptr;
+    a.out = out;
+    a.codes = const_cast<uint8_t *>(q);
+    a.scales = const_cast<uint8_t *>(scale);
+    a.chunks = n * (K / 8);
+    hipError_t e = moe::launch_dequantize_mx(a, out_is_f32, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess)
+        return hip_fail(e, "dequantize_mxfp4 launch");
+    return ok();
+}
+
+int moe_dispatch_mxfp4(const moe_desc *desc, const moe_handle *handle, const uint16_t *x, int32_t H,
+                       const float *topk_w, int64_t R, uint8_t *rows_q, uint8_t *row_scale, float *row_w,
+                       int32_t *row_token, int32_t *row_expert, void *stream)
+{
+    TimingScope timing_scope;
+    int rc;
+    if ((rc = check_dispatch(desc, handle, x, H, topk_w, R, row_w)) != MOE_OK)
+        return rc;
+    if (R > 0 && (!rows_q || !aligned16(rows_q)))
+        return fail(MOE_ERR_ARG, "rows_q must be a non-NULL, 16-byte aligned [R,H/2] byte tensor");
+    if (R > 0 && (!row_scale || !aligned16(row_scale)))
+        return fail(MOE_ERR_ARG, "row_scale must be a non-NULL, 16-byte aligned [R,H/32] byte tensor");
+    // (the scale array is written in words: four bytes of a row's H / 32, a multiple of 8)
+    return launch_dispatch(desc, handle, x, H, topk_w, R, nullptr, rows_q, reinterpret_cast<float *>(row_scale),
+                           row_w, row_token, row_expert, stream, true);
+}
+
+int moe_expert_gemm_mxfp4(const moe_desc *desc, const moe_handle *handle, const uint8_t *rows_q,
+                          const uint8_t *row_scale, int32_t K, int64_t R, const uint8_t *w_q,
+                          const uint8_t *w_scale, int32_t N, uint16_t *out, void *stream)
+{
+    TimingScope timing_scope;
+    int rc;
+    if ((rc = check_product(desc, handle, rows_q, row_scale, K, R, w_q, w_scale)) != MOE_OK)
+        return rc;
+    if ((rc = check_gemm_out(N, R, out)) != MOE_OK)
+        return rc;
+    return launch_product_mx(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, N, false, out, nullptr, stream);
+}
+
+int moe_expert_swiglu_mxfp4(const moe_desc *desc, const moe_handle *handle, const uint8_t *rows_q,
+                            const uint8_t *row_scale, int32_t K, int64_t R, const uint8_t *w_q,
+                            const uint8_t *w_scale, int32_t I, void *out, uint8_t *out_scale, void *stream)
+{
+    TimingScope timing_scope;
+    int rc;
+    if ((rc = check_product(desc, handle, rows_q, row_scale, K, R, w_q, w_scale)) != MOE_OK)
+        return rc;
+    if ((rc = check_swiglu_out(I, R, out, out_scale)) != MOE_OK)
+        return rc;
+    return launch_product_mx(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, I, true, out, out_scale, stream);
 }
 
 const char *moe_last_error(void) { return g_err; }

@@ -87,4 +87,15 @@ inline ExpertKernel choose_expert_kernel(const ExpertLoad &l, int K, int N, bool
     return ExpertKernel::tile;
 }
 
+// The same for MXFP4 rows and weights.
+inline ExpertKernel choose_mx_kernel(const ExpertLoad &l, int K, int N, bool gated)
+{
+    (void)K;
+    const int cols = gated ? kTileCols / 2 : kTileCols;
+    const int64_t tiles = l.groups * ((static_cast<int64_t>(N) + cols - 1) / cols);
+    if (l.group_max <= 32 && tiles * l.rows_mean <= 4 * kCus)
+        return ExpertKernel::rows;
+    return ExpertKernel::ring;
+}
+
 }  // namespace moe

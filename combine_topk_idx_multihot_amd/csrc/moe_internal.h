@@ -93,7 +93,8 @@ struct RowArgs {
     const uint16_t *F;         // [R,H] expert outputs for dw, or null
     uint16_t *rows;            // [R,H] bf16, or null with rows_q set
     uint8_t *rows_q;           // [R,H] E4M3 codes (FP8 dispatch) or null
-    float *row_scale;          // [R,H/128] scales of rows_q (FP8 dispatch)
+    float *row_scale;          // [R,H/128] scales of rows_q (FP8 dispatch); with mx [R,H/32] bytes
+    int32_t mx = 0;            // rows_q holds MXFP4 codes, [R,H/2]
     float *row_w;              // [R] or null
     int32_t *row_token;        // [R] or null
     int32_t *row_expert;       // [R] or null
@@ -165,25 +166,50 @@ struct CombineArgs {
 // gradients of the slots are gathered from their rows).
 hipError_t launch_combine(const CombineArgs &a, hipStream_t s);
 
-// The experts' products on E4M3 rows (experts.hip).
-struct ExpertArgs {
-    const uint8_t *a;       // [R,K] E4M3 rows
-    const float *sa;        // [R,K/128] their scales
-    const uint8_t *w;       // [EL,N,K] E4M3 weights (gated: [EL,2N,K], gate rows first)
-    const float *sw;        // [EL,NB,K/128] their scales
-    void *out;              // [R,N] bf16, or E4M3 with out_scale
-    float *out_scale;       // [R,N/128] or null
+// What the experts' products share, whatever their rows and weights are held in.
+struct ProductArgs {
+    void *out;              // [R,N] bf16, or codes (gated)
     const int32_t *off;     // [EL+1]
     int32_t *status;
     int64_t R;
     ExpertLoad load;        // what the host knows of the groups
     int32_t K, N, EL;
-    int32_t NB;             // scale rows of one expert
     int32_t ntn;            // column tiles (set by the launcher)
     int32_t gated;          // silu(gate) * up of a [2N] product
     int32_t eager;
 };
+
+// The experts' products on E4M3 rows (experts.hip).
+struct ExpertArgs : ProductArgs {
+    const uint8_t *a;       // [R,K] E4M3 rows
+    const float *sa;        // [R,K/128] their scales
+    const uint8_t *w;       // [EL,N,K] E4M3 weights (gated: [EL,2N,K], gate rows first)
+    const float *sw;        // [EL,NB,K/128] their scales
+    float *out_scale;       // [R,N/128] of E4M3 outputs, or null
+    int32_t NB;             // scale rows of one expert
+};
 hipError_t launch_expert_product(const ExpertArgs &a, hipStream_t s);
+
+// The same on MXFP4 rows and weights (experts_mx.hip).
+struct MxExpertArgs : ProductArgs {
+    const uint8_t *a;       // [R,K/2] codes of the rows
+    const uint8_t *sa;      // [R,K/32] their E8M0 scales
+    const uint8_t *w;       // [EL,N,K/2] codes of the weights (gated: [EL,2N,K/2], gate rows first)
+    const uint8_t *sw;      // [EL,N,K/32] (gated: [EL,2N,K/32]) their scales
+    uint8_t *out_scale;     // [R,N/32] of MXFP4 outputs, or null
+};
+hipError_t launch_expert_product_mx(const MxExpertArgs &a, hipStream_t s);
+
+// Quantization to MXFP4 and back (mx.hip): `chunks` runs of 8 values.
+struct MxArgs {
+    const void *values;     // bf16 or fp32 (quantization)
+    void *out;              // bf16 or fp32 (the way back)
+    uint8_t *codes;
+    uint8_t *scales;
+    int64_t chunks;
+};
+hipError_t launch_quantize_mx(const MxArgs &a, bool f32, hipStream_t s);
+hipError_t launch_dequantize_mx(const MxArgs &a, bool f32, hipStream_t s);
 
 // Kernel timing request of the calling host thread (moe_time_next_call).
 // The events ride on the kernels' own dispatch packets: the first kernel of

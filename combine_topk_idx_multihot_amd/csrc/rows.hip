@@ -51,6 +51,7 @@
 //     loads: measured on MI355X, this keeps the write-back of one kernel from
 //     landing in the next one and shortens the whole step.
 #include "moe_internal.h"
+#include "mx.h"
 
 // Compile-time launch parameters.  The defaults are the fastest settings
 // measured on MI355X; the others exist for measurement and give the same
@@ -282,14 +283,18 @@ __device__ __forceinline__ void zero_words(uint32_t *__restrict__ base, int64_t 
     zero_chunks(reinterpret_cast<u32x4 *>(base), a0 >> 2, a1 >> 2, w, nw, lane);
 }
 
-// Zero rows [r0, r1) of the dispatch output: bf16 rows, or E4M3 rows and
+// 16-byte chunks of a row of codes.  (Its scales take H / 128 words in either
+// format: fp32 per 128 elements, or a byte per 32.)
+__host__ __device__ __forceinline__ int code_chunks(const RowArgs &a) { return a.mx ? a.H >> 5 : a.H >> 4; }
+
+// Zero rows [r0, r1) of the dispatch output: bf16 rows, or rows of codes and
 // their scales; `w` of `nw` waves.
 __device__ __forceinline__ void zero_rows(const RowArgs &a, int64_t r0, int64_t r1, int64_t w,
                                           int64_t nw, int lane)
 {
     if (a.rows_q) {
-        zero_chunks(reinterpret_cast<u32x4 *>(a.rows_q), r0 * (a.H >> 4), r1 * (a.H >> 4), w, nw,
-                    lane);
+        const int nch = code_chunks(a);
+        zero_chunks(reinterpret_cast<u32x4 *>(a.rows_q), r0 * nch, r1 * nch, w, nw, lane);
         zero_words(reinterpret_cast<uint32_t *>(a.row_scale), r0 * (a.H >> 7), r1 * (a.H >> 7), w,
                    nw, lane);
     } else {
@@ -498,7 +503,7 @@ __device__ __forceinline__ void fill_sentinel_oneshot(const RowArgs &a, int64_t 
     const int64_t total = a.status[0];
     const int64_t r0 = max<int64_t>(0, min<int64_t>(total, a.R));
     const u32x4 z = {0u, 0u, 0u, 0u};
-    const int64_t nch = a.rows_q ? (a.H >> 4) : (a.H >> 3); // chunks per row
+    const int64_t nch = a.rows_q ? code_chunks(a) : (a.H >> 3); // chunks per row
     const int64_t nrow_pieces = (a.R * nch + PC - 1) / PC;
     if (gw < nrow_pieces) {
         const int64_t p0 = gw * PC;
@@ -1371,7 +1376,9 @@ __device__ __forceinline__ u32x2 e4m3_pack8(const float (&y)[8])
     return r;
 }
 
-template <int SEG>
+// MX: MXFP4 rows instead, blocks of 32 with a byte each: a lane's 8 elements make
+// one word of codes, a block is four lanes (mx.h).
+template <int SEG, bool MX>
 __device__ __forceinline__ void quant_token(const RowArgs &a, int64_t bid)
 {
     const int lane = threadIdx.x & (kWave - 1);
@@ -1396,6 +1403,7 @@ __device__ __forceinline__ void quant_token(const RowArgs &a, int64_t bid)
         u32x4 v[SEG];
         load_seg<SEG>(v, a.src, t, a.H, c0, nch, lane);
         u32x2 q[SEG];
+        uint32_t qx[SEG], scx[SEG]; // MX: codes, and the scales of four blocks
         float sc[SEG];
 #pragma unroll
         for (int i = 0; i < SEG; ++i) {
@@ -1405,6 +1413,16 @@ __device__ __forceinline__ void quant_token(const RowArgs &a, int64_t bid)
             for (int j = 0; j < 4; ++j) {
                 x[2 * j] = in ? bf16_lo(v[i][j]) : 0.f;
                 x[2 * j + 1] = in ? bf16_hi(v[i][j]) : 0.f;
+            }
+            if constexpr (MX) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    top = max(top, mag_bits(x[j]));
+                const uint32_t b = mx_scale(max_of_quad(top));
+                qx[i] = mx_pack8(x, b);
+                scx[i] = gather_bytes(b);
+                continue;
             }
             float m = 0.f;
 #pragma unroll
@@ -1427,7 +1445,23 @@ __device__ __forceinline__ void quant_token(const RowArgs &a, int64_t bid)
             const Batch<kCopyBatch> bt = take_batch<kCopyBatch>(mrest, sl.row);
 #pragma unroll
             for (int b = 0; b < kCopyBatch; ++b) {
-                if (b < bt.n) {
+                if (MX && b < bt.n) {
+                    uint32_t *__restrict__ dst =
+                        reinterpret_cast<uint32_t *>(a.rows_q + bt.row[b] * (a.H >> 1));
+                    uint32_t *__restrict__ ds = reinterpret_cast<uint32_t *>(a.row_scale) + bt.row[b] * nb;
+#pragma unroll
+                    for (int i = 0; i < SEG; ++i) {
+                        const int c = c0 + i * kWave + lane;
+                        if (c < nch) {
+                            if (MOE_NT_COPY_ROWS)
+                                __builtin_nontemporal_store(qx[i], dst + c);
+                            else
+                                dst[c] = qx[i];
+                            if ((lane & 15) == 0)
+                                ds[c >> 4] = scx[i];
+                        }
+                    }
+                } else if (b < bt.n) {
                     u32x2 *__restrict__ dst = reinterpret_cast<u32x2 *>(a.rows_q + bt.row[b] * a.H);
                     float *__restrict__ ds = a.row_scale + bt.row[b] * nb;
 #pragma unroll
@@ -1449,8 +1483,8 @@ __device__ __forceinline__ void quant_token(const RowArgs &a, int64_t bid)
 }
 
 // Grid as k_move_rows: [sentinel blocks][token blocks][expert blocks].
-template <int SEG>
-__global__ void __launch_bounds__(kRowThreads) k_dispatch_fp8(RowArgs a)
+template <int SEG, bool MX>
+__device__ __forceinline__ void quant_rows(const RowArgs &a)
 {
     int64_t bid = blockIdx.x;
     if (bid < a.nsent_blocks) {
@@ -1459,9 +1493,21 @@ __global__ void __launch_bounds__(kRowThreads) k_dispatch_fp8(RowArgs a)
     }
     bid -= a.nsent_blocks;
     if (bid < a.ntok_blocks)
-        quant_token<SEG>(a, bid);
+        quant_token<SEG, MX>(a, bid);
     else
         fill_expert(a, static_cast<int>(bid - a.ntok_blocks));
+}
+
+template <int SEG>
+__global__ void __launch_bounds__(kRowThreads) k_dispatch_fp8(RowArgs a)
+{
+    quant_rows<SEG, false>(a);
+}
+
+template <int SEG>
+__global__ void __launch_bounds__(kRowThreads) k_dispatch_mxfp4(RowArgs a)
+{
+    quant_rows<SEG, true>(a);
 }
 
 // ---------------------------------------------------------------------------
@@ -1579,9 +1625,14 @@ static int chunks_per_lane(int H)
 // whose address-ordered writes are the faster way to zero hundreds of MB.
 constexpr int64_t kInlineTailBytes = int64_t(32) << 20;
 
+static int64_t row_bytes(const RowArgs &a)
+{
+    return a.rows_q ? code_chunks(a) * 16 + (a.H >> 7) * 4 : static_cast<int64_t>(a.H) * 2;
+}
+
 static int64_t row_array_bytes(const RowArgs &a)
 {
-    return a.rows_q ? a.R * (a.H + (a.H >> 7) * 4) : a.R * 2 * a.H;
+    return a.R * row_bytes(a);
 }
 
 static bool tail_in_rows_launch(const RowArgs &a)
@@ -1611,7 +1662,7 @@ static int64_t sentinel_blocks(const RowArgs &a)
     // array (the host does not know where the tail starts), and over the
     // scale array of E4M3 rows
     const int64_t pc = static_cast<int64_t>(MOE_TAIL_PIECE_KIB) * kWave;
-    const int64_t nch = a.rows_q ? (a.H >> 4) : (a.H >> 3);
+    const int64_t nch = a.rows_q ? code_chunks(a) : (a.H >> 3);
     int64_t pieces = (a.R * nch + pc - 1) / pc;
     if (a.rows_q)
         pieces += (a.R * (a.H >> 7) + pc * 4 - 1) / (pc * 4);
@@ -1658,8 +1709,7 @@ void row_shape(RowArgs &a)
     // them so that none zeroes more than about 64 KiB (1 to 16 per expert).
     // One workgroup zeroing 127 rows of 4 KiB (P = 128) ran alone at the end
     // of the grid.
-    const int64_t row_bytes = a.rows_q ? a.H + (a.H >> 7) * 4 : static_cast<int64_t>(a.H) * 2;
-    const int64_t pad_bytes = static_cast<int64_t>(a.P > 1 ? a.P - 1 : 0) * row_bytes;
+    const int64_t pad_bytes = static_cast<int64_t>(a.P > 1 ? a.P - 1 : 0) * row_bytes(a);
     const int64_t sl = (pad_bytes + MOE_PAD_SLICE_BYTES - 1) / MOE_PAD_SLICE_BYTES;
     a.exp_slices = static_cast<int32_t>(sl < 1 ? 1 : (sl > 16 ? 16 : sl));
     a.nexp_blocks = a.R > 0 ? static_cast<int64_t>(a.EL) * a.exp_slices : 0;
@@ -1764,7 +1814,13 @@ hipError_t launch_move_rows(const RowArgs &a0, hipStream_t s)
         return hipSuccess;
     const dim3 g(static_cast<unsigned>(nb));
     const dim3 blk(kRowThreads);
-    if (a.rows_q) {
+    if (a.rows_q && a.mx) {
+        switch (a.seg) {
+        case 1: launch(k_dispatch_mxfp4<1>, g, blk, 0, s, a); break;
+        case 2: launch(k_dispatch_mxfp4<2>, g, blk, 0, s, a); break;
+        default: launch(k_dispatch_mxfp4<4>, g, blk, 0, s, a); break;
+        }
+    } else if (a.rows_q) {
         switch (a.seg) {
         case 1: launch(k_dispatch_fp8<1>, g, blk, 0, s, a); break;
         case 2: launch(k_dispatch_fp8<2>, g, blk, 0, s, a); break;

@@ -37,6 +37,12 @@ step runs in the HIP library:
       -> (h_q [R,I] float8_e4m3fn, h_scale [R,I/128]): silu(gate) * up,
       requantized for a following expert_gemm_fp8; neither has autograd (the
       rows are codes).  Their rows past the routed total are not written.
+  quantize_mxfp4(x [...,K]) -> (q [...,K/2], scale [...,K/32]) uint8 and
+      dequantize_mxfp4(q, scale, f32) -> [...,K]: microscaled 4-bit floats
+  dispatch_mxfp4(same arguments as dispatch)
+      -> (rows_q [R,H/2], row_scale [R,H/32], row_w, row_token, row_expert)
+  expert_gemm_mxfp4, expert_swiglu_mxfp4: the experts' products on MXFP4 rows
+      and weights, arguments as for the FP8 ones
 
 <handle tensors> = routing_map, tokens_per_expert, padded_offsets, row_of_slot,
 status, workspace, in that order.  The workspace carries the route's row list
@@ -45,7 +51,8 @@ of the tokens.  The handle fields the ops need but do not carry (T, k, the
 number of local experts) are read off the tensors' shapes.
 
 ``moe_layer`` strings the ops together around a caller-supplied expert;
-``moe_layer_fp8`` is the FP8 layer for serving, dispatch to combine.
+``moe_layer_fp8`` and ``moe_layer_mxfp4`` are the FP8 and MXFP4 layers for serving,
+dispatch to combine.
 """
 from __future__ import annotations
 
@@ -386,6 +393,102 @@ def _(rows_q, row_scale, w_q, w_scale, routing_map, tokens_per_expert, padded_of
 
 
 # ---------------------------------------------------------------------------
+# MXFP4: quantization, dispatch and the experts' products
+# ---------------------------------------------------------------------------
+@torch.library.custom_op(f"{_NS}::quantize_mxfp4", mutates_args=())
+def quantize_mxfp4(x: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    return B.quantize_mxfp4(x.contiguous())
+
+
+@quantize_mxfp4.register_fake
+def _(x):
+    *n, K = x.shape
+    return (x.new_empty((*n, K // 2), dtype=torch.uint8), x.new_empty((*n, K // 32), dtype=torch.uint8))
+
+
+@torch.library.custom_op(f"{_NS}::dequantize_mxfp4", mutates_args=())
+def dequantize_mxfp4(q: torch.Tensor, scale: torch.Tensor, f32: bool) -> torch.Tensor:
+    return B.dequantize_mxfp4(q.contiguous(), scale.contiguous(),
+                              torch.float32 if f32 else torch.bfloat16)
+
+
+@dequantize_mxfp4.register_fake
+def _(q, scale, f32):
+    return q.new_empty((*q.shape[:-1], 2 * q.shape[-1]),
+                       dtype=torch.float32 if f32 else torch.bfloat16)
+
+
+@torch.library.custom_op(f"{_NS}::dispatch_mxfp4", mutates_args=())
+def dispatch_mxfp4(x: torch.Tensor, topk_w: torch.Tensor, routing_map: torch.Tensor,
+                   tokens_per_expert: torch.Tensor, padded_offsets: torch.Tensor,
+                   row_of_slot: torch.Tensor, status: torch.Tensor, workspace: torch.Tensor,
+                   num_experts: int, local_begin: int, pad_multiple: int, capacity: int, R: int
+                   ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """MXFP4 dispatch: (rows_q [R,H/2], row_scale [R,H/32] uint8, row_w, row_token, row_expert).
+    Not differentiable (the codes are a quantization)."""
+    desc, h = _rebuild(routing_map, tokens_per_expert, padded_offsets, row_of_slot, status,
+                       workspace, num_experts, local_begin, pad_multiple, capacity)
+    H = x.shape[1]
+    rows_q = x.new_empty((R, H // 2), dtype=torch.uint8)
+    row_scale = x.new_empty((R, H // 32), dtype=torch.uint8)
+    row_w = x.new_empty(R, dtype=torch.float32)
+    row_token = x.new_empty(R, dtype=torch.int32)
+    row_expert = x.new_empty(R, dtype=torch.int32)
+    B.moe_dispatch_mxfp4(desc, h, x.contiguous(), H, R, rows_q, row_scale, topk_w.contiguous(),
+                         row_w, row_token, row_expert)
+    return rows_q, row_scale, row_w, row_token, row_expert
+
+
+@dispatch_mxfp4.register_fake
+def _(x, topk_w, routing_map, tokens_per_expert, padded_offsets, row_of_slot, status,
+      workspace, num_experts, local_begin, pad_multiple, capacity, R):
+    H = x.shape[1]
+    return (x.new_empty((R, H // 2), dtype=torch.uint8),
+            x.new_empty((R, H // 32), dtype=torch.uint8), x.new_empty(R, dtype=torch.float32),
+            x.new_empty(R, dtype=torch.int32), x.new_empty(R, dtype=torch.int32))
+
+
+@torch.library.custom_op(f"{_NS}::expert_gemm_mxfp4", mutates_args=())
+def expert_gemm_mxfp4(rows_q: torch.Tensor, row_scale: torch.Tensor, w_q: torch.Tensor,
+                      w_scale: torch.Tensor, routing_map: torch.Tensor,
+                      tokens_per_expert: torch.Tensor, padded_offsets: torch.Tensor,
+                      row_of_slot: torch.Tensor, status: torch.Tensor, workspace: torch.Tensor,
+                      num_experts: int, local_begin: int, pad_multiple: int, capacity: int
+                      ) -> torch.Tensor:
+    desc, h = _rebuild(routing_map, tokens_per_expert, padded_offsets, row_of_slot, status,
+                       workspace, num_experts, local_begin, pad_multiple, capacity)
+    return B.expert_gemm_mxfp4(desc, h, rows_q.contiguous(), row_scale.contiguous(),
+                               w_q.contiguous(), w_scale.contiguous())
+
+
+@expert_gemm_mxfp4.register_fake
+def _(rows_q, row_scale, w_q, w_scale, routing_map, tokens_per_expert, padded_offsets,
+      row_of_slot, status, workspace, num_experts, local_begin, pad_multiple, capacity):
+    return rows_q.new_empty((rows_q.shape[0], w_q.shape[1]), dtype=torch.bfloat16)
+
+
+@torch.library.custom_op(f"{_NS}::expert_swiglu_mxfp4", mutates_args=())
+def expert_swiglu_mxfp4(rows_q: torch.Tensor, row_scale: torch.Tensor, w_q: torch.Tensor,
+                        w_scale: torch.Tensor, routing_map: torch.Tensor,
+                        tokens_per_expert: torch.Tensor, padded_offsets: torch.Tensor,
+                        row_of_slot: torch.Tensor, status: torch.Tensor, workspace: torch.Tensor,
+                        num_experts: int, local_begin: int, pad_multiple: int, capacity: int
+                        ) -> tuple[torch.Tensor, torch.Tensor]:
+    desc, h = _rebuild(routing_map, tokens_per_expert, padded_offsets, row_of_slot, status,
+                       workspace, num_experts, local_begin, pad_multiple, capacity)
+    return B.expert_swiglu_mxfp4(desc, h, rows_q.contiguous(), row_scale.contiguous(),
+                                 w_q.contiguous(), w_scale.contiguous())
+
+
+@expert_swiglu_mxfp4.register_fake
+def _(rows_q, row_scale, w_q, w_scale, routing_map, tokens_per_expert, padded_offsets,
+      row_of_slot, status, workspace, num_experts, local_begin, pad_multiple, capacity):
+    R, I = rows_q.shape[0], w_q.shape[1] // 2
+    return (rows_q.new_empty((R, I // 2), dtype=torch.uint8),
+            rows_q.new_empty((R, I // 32), dtype=torch.uint8))
+
+
+# ---------------------------------------------------------------------------
 # a whole expert-parallel layer on one GPU's share
 # ---------------------------------------------------------------------------
 def moe_layer(x, topk_idx, topk_w, experts, num_experts, local_begin=0, num_local=None,
@@ -420,4 +523,19 @@ def moe_layer_fp8(x, topk_idx, topk_w, w1_q, w1_scale, w2_q, w2_scale, num_exper
     rows_q, row_scale, *_ = dispatch_fp8(x, topk_w, *where, R)
     h_q, h_scale = expert_swiglu_fp8(rows_q, row_scale, w1_q, w1_scale, *where)
     Y = expert_gemm_fp8(h_q, h_scale, w2_q, w2_scale, *where)
+    return combine_weighted(Y, topk_w, *where)
+
+
+def moe_layer_mxfp4(x, topk_idx, topk_w, w1_q, w1_scale, w2_q, w2_scale, num_experts,
+                    local_begin=0, pad_multiple=1, capacity=0):
+    """moe_layer_fp8 with MXFP4 rows and weights: w1_q [EL,2I,H/2] (gate rows first) and w2_q
+    [EL,H,I/2] packed E2M1 codes, w1_scale [EL,2I,H/32] and w2_scale [EL,H,I/32] E8M0 bytes, as
+    quantize_mxfp4 makes them.  For serving: no autograd (the rows are codes)."""
+    num_local = w1_q.shape[0]
+    *handle, host = route(topk_idx, num_experts, local_begin, num_local, pad_multiple, capacity)
+    R = capacity if capacity > 0 else int(host[0])
+    where = (*handle, num_experts, local_begin, pad_multiple, capacity)
+    rows_q, row_scale, *_ = dispatch_mxfp4(x, topk_w, *where, R)
+    h_q, h_scale = expert_swiglu_mxfp4(rows_q, row_scale, w1_q, w1_scale, *where)
+    Y = expert_gemm_mxfp4(h_q, h_scale, w2_q, w2_scale, *where)
     return combine_weighted(Y, topk_w, *where)

@@ -417,6 +417,68 @@ int moe_expert_swiglu_fp8(const moe_desc *desc, const moe_handle *handle, const 
                           const float *w_scale, int32_t I, void *out, float *out_scale,
                           void *stream);
 
+/*
+ * Microscaled 4-bit floating point (MXFP4), for weights and for rows.  Every 32
+ * consecutive values share a power of two, an E8M0 byte b standing for 2^(b - 127);
+ * each value is an E2M1 code of 4 bits: sign, and magnitude 0, 0.5, 1, 1.5, 2, 3, 4
+ * or 6.  Two codes a byte, the first value's in the low half.
+ * moe_quantize_mxfp4, of n rows of K values:
+ *   x           device [n,K] bf16 (x_is_f32 == 0) or fp32 (1), K a positive
+ *               multiple of 32.
+ *   q           device [n,K/2] uint8 out; scale device [n,K/32] uint8 out.
+ * With a the block's largest magnitude, b - 127 = floor(log2 a) - 2, at least -127
+ * (so b = 0 for a block of zeros), and the codes are the nearest ones to
+ * x / 2^(b - 127), ties to even, magnitudes above 6 to 6.  A block with a NaN or an
+ * infinity gets b = 255 and codes of 0; b = 255 stands for NaN in every use.
+ */
+int moe_quantize_mxfp4(const void *x, int32_t x_is_f32, int64_t n, int32_t K, uint8_t *q,
+                       uint8_t *scale, void *stream);
+
+/* The values that MXFP4 codes stand for: out device [n,K] bf16 (out_is_f32 == 0) or
+ * fp32 (1), exact but where 6 * 2^(b - 127) is out of the type's range (b >= 253:
+ * codes of 4 and 6, of 2 and 3 from 254 on, are infinite). */
+int moe_dequantize_mxfp4(const uint8_t *q, const uint8_t *scale, int64_t n, int32_t K, void *out,
+                         int32_t out_is_f32, void *stream);
+
+/*
+ * MXFP4 dispatch: as moe_dispatch_fp8 with rows in MXFP4.
+ *   rows_q      device [R,H/2] uint8 out, row_scale device [R,H/32] uint8 out: of
+ *               the token's row, exactly what moe_quantize_mxfp4 makes of it.  Pad
+ *               rows and rows >= total are zero bytes with scale bytes of 0 (zero
+ *               in every use).
+ * The token is quantized once and its codes written to each of its rows.
+ */
+int moe_dispatch_mxfp4(const moe_desc *desc, const moe_handle *handle, const uint16_t *x,
+                       int32_t H, const float *topk_w, int64_t R, uint8_t *rows_q,
+                       uint8_t *row_scale, float *row_w, int32_t *row_token, int32_t *row_expert,
+                       void *stream);
+
+/*
+ * The experts' products on MXFP4 rows (moe_dispatch_mxfp4's output), as
+ * moe_expert_gemm_fp8 and moe_expert_swiglu_fp8 with
+ *   rows_q      device [R,K/2] uint8 codes, row_scale device [R,K/32] uint8, K a
+ *               positive multiple of 128 (at most 2^23),
+ *   w_q         device [EL,N,K/2] uint8 codes, w_scale device [EL,N,K/32] uint8,
+ *               N a positive multiple of 8 (gated: [EL,2I,K/2] and [EL,2I,K/32],
+ *               gate rows first, I a positive multiple of 128),
+ *   out         device [R,N] bf16; gated: out_scale == NULL: device [R,I] bf16, else
+ *               device [R,I/2] uint8 codes and out_scale device [R,I/32] uint8 of h,
+ *               what moe_quantize_mxfp4 makes of its fp32 values: the rows_q and
+ *               row_scale of a following moe_expert_gemm_mxfp4 with K = I.
+ * The products are summed by the GPU's 4-bit matrix instructions in fp32, scales
+ * among them, in a fixed order: equal calls give equal bits.  A scale byte of 255
+ * makes every output that its row (or weight row) enters NaN.  Rows, flags, errors,
+ * order and alignment as there.
+ */
+int moe_expert_gemm_mxfp4(const moe_desc *desc, const moe_handle *handle, const uint8_t *rows_q,
+                          const uint8_t *row_scale, int32_t K, int64_t R, const uint8_t *w_q,
+                          const uint8_t *w_scale, int32_t N, uint16_t *out, void *stream);
+
+int moe_expert_swiglu_mxfp4(const moe_desc *desc, const moe_handle *handle, const uint8_t *rows_q,
+                            const uint8_t *row_scale, int32_t K, int64_t R, const uint8_t *w_q,
+                            const uint8_t *w_scale, int32_t I, void *out, uint8_t *out_scale,
+                            void *stream);
+
 /* Message of the last failing call on this thread ("" if none). */
 const char *moe_last_error(void);
 
@@ -429,8 +491,9 @@ int moe_device_check(int device);
  * profiler hook).  The next moe_route_build, moe_route_build_noalloc,
  * moe_route_dispatch, moe_dispatch, moe_dispatch_fp8, moe_combine,
  * moe_combine_bwd, moe_dispatch_bwd, moe_combine_weighted,
- * moe_combine_weighted_bwd, moe_expert_gemm_fp8 or moe_expert_swiglu_fp8 call
- * made on this host thread times its own kernels into two HIP events:
+ * moe_combine_weighted_bwd, moe_expert_gemm_fp8, moe_expert_swiglu_fp8,
+ * moe_quantize_mxfp4, moe_dequantize_mxfp4, moe_dispatch_mxfp4,
+ * moe_expert_gemm_mxfp4 or moe_expert_swiglu_mxfp4 call made on this host thread times its own kernels into two HIP events:
  *   start_event  hipEvent_t (created by the caller, timing enabled) or NULL:
  *                takes the start time of the call's first kernel.
  *   stop_event   hipEvent_t or NULL: takes the end time of the call's last
