@@ -8,11 +8,15 @@ enough for what the call will write (the C ABI takes plain pointers and cannot).
 The convenience functions at the bottom (``alloc_handle``, ``route``,
 ``dispatch``, ``dispatch_fp8``, ``combine``, ``combine_bwd``, ``dispatch_bwd``,
 ``combine_weighted``, ``combine_weighted_bwd``, ``expert_gemm_fp8``,
-``expert_swiglu_fp8``) only add output allocation.  ``PreparedDispatch``,
+``expert_swiglu_fp8``, ``quantize_mxfp4``, ``dequantize_mxfp4``, ``dispatch_mxfp4``,
+``expert_gemm_mxfp4``, ``expert_swiglu_mxfp4``, ``layer_tokens``) only add output
+allocation.  ``PreparedDispatch``,
 ``PreparedCombine``, ``PreparedCombineBwd``, ``PreparedCombineWeighted``,
-``PreparedCombineWeightedBwd``, ``PreparedExpertGemmFp8`` and
-``PreparedExpertSwigluFp8`` check reused buffers once and then take only the
-step's row count; ``KernelTimer`` times one call's kernels.
+``PreparedCombineWeightedBwd``, ``PreparedExpertGemmFp8``,
+``PreparedExpertSwigluFp8``, ``PreparedExpertGemmMxfp4`` and
+``PreparedExpertSwigluMxfp4`` check reused buffers once and then take only the
+step's row count, ``PreparedLayerTokens`` nothing; ``KernelTimer`` times one
+call's kernels.
 
 The library is loaded on first use; if it has not been built this raises
 (there is no fallback path).
@@ -33,6 +37,8 @@ MOE_OK, MOE_ERR_ARG, MOE_ERR_HIDDEN, MOE_ERR_CAPACITY = 0, 1, 2, 3
 MOE_ERR_WORKSPACE, MOE_ERR_INDEX, MOE_ERR_HIP, MOE_ERR_DEVICE = 4, 5, 6, 7
 MOE_EAGER, MOE_SYNC_FREE = 0, 1
 MOE_FLAG_BAD_ID, MOE_FLAG_DUPLICATE, MOE_FLAG_ROWS_MISMATCH = 1, 2, 4
+MOE_WEIGHTS_BF16, MOE_WEIGHTS_FP8, MOE_WEIGHTS_MXFP4 = 0, 1, 2
+MOE_LAYER_MAX_SLOTS = 1024  # T * k of moe_layer_tokens at most
 MOE_NOALLOC_SCRATCH_BYTES = 4194304  # the fixed route scratch of moe_route_build_noalloc
 
 # Every symbol include/moe_mi355x.h declares.
@@ -42,6 +48,7 @@ EXPORTS = ("moe_capacity_min", "moe_route_workspace_size", "moe_route_build",
            "moe_combine_weighted", "moe_combine_weighted_bwd", "moe_expert_gemm_fp8",
            "moe_expert_swiglu_fp8", "moe_quantize_mxfp4", "moe_dequantize_mxfp4",
            "moe_dispatch_mxfp4", "moe_expert_gemm_mxfp4", "moe_expert_swiglu_mxfp4",
+           "moe_layer_tokens_workspace_size", "moe_layer_tokens",
            "moe_last_error", "moe_device_check", "moe_time_next_call")
 
 
@@ -115,6 +122,11 @@ def lib() -> ctypes.CDLL:
         L.moe_expert_gemm_mxfp4.restype = ctypes.c_int
         L.moe_expert_swiglu_mxfp4.argtypes = [pd, ph, vp, vp, i32, i64, vp, vp, i32, vp, vp, vp]
         L.moe_expert_swiglu_mxfp4.restype = ctypes.c_int
+        L.moe_layer_tokens_workspace_size.argtypes = [pd, i32]
+        L.moe_layer_tokens_workspace_size.restype = ctypes.c_size_t
+        L.moe_layer_tokens.argtypes = [pd, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp,
+                                       ctypes.c_size_t, vp, vp, vp]
+        L.moe_layer_tokens.restype = ctypes.c_int
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = ctypes.c_char_p
         L.moe_device_check.argtypes = [ctypes.c_int]
@@ -758,6 +770,102 @@ def moe_expert_swiglu_mxfp4(desc: Desc, handle: Handle, rows_q: torch.Tensor,
                                                 p[2], p[3], I, p_o, p_s, _stream(stream)))
 
 
+# ---------------------------------------------------------------------------
+# a whole layer for a few tokens
+# ---------------------------------------------------------------------------
+
+def moe_layer_tokens_workspace_size(desc: Desc, I: int) -> int:
+    n = int(lib().moe_layer_tokens_workspace_size(ctypes.byref(desc), _int32("I", I)))
+    if n == 0:
+        raise MoeError(MOE_ERR_ARG, last_error())
+    return n
+
+
+def _layer_args(desc, topk_idx, topk_w, x, w1, w2, out, w1_scale, w2_scale, workspace, flags,
+                stream):
+    """Checked arguments of moe_layer_tokens.  The weights' format and I come from w1 and w2."""
+    _here(topk_idx, topk_w, x, w1, w2, out, w1_scale, w2_scale, workspace, flags)
+    if x.dim() != 2 or w1.dim() != 3 or w2.dim() != 3:
+        raise MoeError(MOE_ERR_ARG, "x must be [T,H], w1 and w2 [EL,rows,columns]")
+    H, n, EL = x.shape[1], desc.T * desc.k, desc.num_local
+    if w1.dtype == torch.bfloat16:
+        fmt, per, types, scales = MOE_WEIGHTS_BF16, 1, _BF16, None
+    elif w1_scale is not None and w1_scale.dtype in _E8M0:
+        fmt, per, types, scales = MOE_WEIGHTS_MXFP4, 2, _FP4, _E8M0
+    else:
+        fmt, per, types, scales = MOE_WEIGHTS_FP8, 1, _FP8, _F32
+    I = w2.shape[2] * per
+    if tuple(w1.shape) != (EL, 2 * I, H // per) or tuple(w2.shape[:2]) != (EL, H):
+        raise MoeError(MOE_ERR_ARG, f"w1 must be {[EL, 2 * I, H // per]} and w2 {[EL, H, I // per]} "
+                                    f"(got {tuple(w1.shape)} and {tuple(w2.shape)})")
+    if x.shape[0] != desc.T:
+        raise MoeError(MOE_ERR_ARG, f"x has {x.shape[0]} rows, the description T={desc.T}")
+    if desc.T == 0:
+        return (None, None, None, H, I, fmt, None, None, None, None, None, 0, None, None,
+                _stream(stream))
+    if (w1_scale is None) != (scales is None) or (w2_scale is None) != (scales is None):
+        raise MoeError(MOE_ERR_ARG, "bf16 weights go without scales, E4M3 and MXFP4 weights with both")
+    p_s1 = p_s2 = None
+    if fmt == MOE_WEIGHTS_FP8:
+        shapes = (EL, 2 * I // 128, H // 128), (EL, H // 128, I // 128)
+    elif fmt == MOE_WEIGHTS_MXFP4:
+        shapes = (EL, 2 * I, H // 32), (EL, H, I // 32)
+    if scales is not None:
+        if (tuple(w1_scale.shape), tuple(w2_scale.shape)) != shapes:
+            raise MoeError(MOE_ERR_ARG, f"w1_scale must be {list(shapes[0])} and w2_scale {list(shapes[1])} "
+                                        f"(got {tuple(w1_scale.shape)} and {tuple(w2_scale.shape)})")
+        p_s1 = _dev(w1_scale, "w1_scale", scales, w1_scale.numel())
+        p_s2 = _dev(w2_scale, "w2_scale", scales, w2_scale.numel())
+    if workspace is None:
+        raise MoeError(MOE_ERR_ARG, "workspace is required")
+    _apart((out, workspace, flags), (topk_idx, topk_w, x, w1, w2, w1_scale, w2_scale))
+    return (_dev(topk_idx, "topk_idx", _I64 if desc.idx_is_i64 else _I32, n),
+            _dev(topk_w, "topk_w", _F32, n), _dev(x, "x", _BF16, desc.T * H), H, I, fmt,
+            _dev(w1, "w1", types, w1.numel()), p_s1, _dev(w2, "w2", types, w2.numel()), p_s2,
+            _dev(workspace, "workspace", _U8, 0), workspace.numel(),
+            _dev(out, "out", _BF16, desc.T * H), _dev(flags, "flags", _I32, 1, optional=True),
+            _stream(stream))
+
+
+def moe_layer_tokens(desc: Desc, topk_idx: torch.Tensor, topk_w: torch.Tensor, x: torch.Tensor,
+                     w1: torch.Tensor, w2: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor,
+                     w1_scale: torch.Tensor | None = None, w2_scale: torch.Tensor | None = None,
+                     flags: torch.Tensor | None = None, stream=None) -> int:
+    """out [T,H] bf16 = the layer of x [T,H] bf16 for T * k <= MOE_LAYER_MAX_SLOTS, in two kernels.
+    w1 [EL,2I,H] and w2 [EL,H,I] bf16; or E4M3 with fp32 scales per 128 x 128 block; or packed MXFP4
+    [EL,2I,H/2] and [EL,H,I/2] with uint8 scales [EL,2I,H/32] and [EL,H,I/32]."""
+    a = _layer_args(desc, topk_idx, topk_w, x, w1, w2, out, w1_scale, w2_scale, workspace, flags,
+                    stream)
+    return _check(lib().moe_layer_tokens(ctypes.byref(desc), *a))
+
+
+class PreparedLayerTokens:
+    """moe_layer_tokens over buffers that a loop reuses on every step, checked once; it keeps its own
+    workspace.  The tensors must stay as they are (no resize_ or set_) while the object is in use; it
+    holds references to them.  Calls of one object share its workspace: they must not overlap."""
+
+    def __init__(self, desc: Desc, topk_idx: torch.Tensor, topk_w: torch.Tensor, x: torch.Tensor,
+                 w1: torch.Tensor, w2: torch.Tensor, out: torch.Tensor,
+                 w1_scale: torch.Tensor | None = None, w2_scale: torch.Tensor | None = None,
+                 flags: torch.Tensor | None = None, stream=None):
+        ws = _layer_workspace(desc, w2, w1_scale)
+        self._desc = Desc.from_buffer_copy(desc)
+        self._args = (ctypes.byref(self._desc),
+                      *_layer_args(self._desc, topk_idx, topk_w, x, w1, w2, out, w1_scale, w2_scale, ws,
+                                   flags, stream))
+        self._fn = lib().moe_layer_tokens
+        self._keep = (topk_idx, topk_w, x, w1, w2, out, w1_scale, w2_scale, ws, flags)
+
+    def __call__(self) -> int:
+        return _check(self._fn(*self._args))
+
+
+def _layer_workspace(desc, w2, w1_scale):
+    packed = w1_scale is not None and w1_scale.dtype in _E8M0
+    return torch.empty(moe_layer_tokens_workspace_size(desc, w2.shape[-1] * (2 if packed else 1)),
+                       dtype=torch.uint8, device=w2.device)
+
+
 class _Prepared:
     """A call over buffers that a loop reuses on every step, checked once against
     the buffers' capacity; each call passes only the step's row count R.  Same
@@ -1152,6 +1260,20 @@ def expert_swiglu_mxfp4(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_sc
     moe_expert_swiglu_mxfp4(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, I, out, out_scale,
                             stream=stream)
     return out, out_scale
+
+
+def layer_tokens(desc: Desc, topk_idx: torch.Tensor, topk_w: torch.Tensor, x: torch.Tensor,
+                 w1: torch.Tensor, w2: torch.Tensor, w1_scale: torch.Tensor | None = None,
+                 w2_scale: torch.Tensor | None = None, flags: torch.Tensor | None = None, stream=None):
+    """moe_layer_tokens with a fresh output [T,H] bf16 and workspace."""
+    out = torch.empty((desc.T, x.shape[1]), dtype=torch.bfloat16, device=x.device)
+    ws = _layer_workspace(desc, w2, w1_scale)
+    moe_layer_tokens(desc, topk_idx, topk_w, x, w1, w2, out, ws, w1_scale, w2_scale, flags,
+                     stream=stream)
+    if stream is not None:  # the workspace is let go here, while that stream may still use it
+        s = _stream(stream)
+        ws.record_stream(torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream())
+    return out
 
 
 def _mx_shapes_fit(desc, rows_q, row_scale, w_q, w_scale):

@@ -357,6 +357,31 @@ int launch_product_mx(const moe_desc *desc, const moe_handle *handle, const uint
     return ok();
 }
 
+static_assert(moe::kLayerMaxSlots == MOE_LAYER_MAX_SLOTS && moe::kLayerBf16 == MOE_WEIGHTS_BF16 &&
+                  moe::kLayerFp8 == MOE_WEIGHTS_FP8 && moe::kLayerMxfp4 == MOE_WEIGHTS_MXFP4,
+              "the header's numbers");
+constexpr int32_t kLayerMaxWidth = 65536;
+
+// Argument rules of moe_layer_tokens that its workspace size goes by.
+int check_layer(const moe_desc *desc, int32_t I)
+{
+    int rc;
+    if ((rc = check_desc(desc)) != MOE_OK)
+        return rc;
+    if (desc->T * desc->k > MOE_LAYER_MAX_SLOTS)
+        return fail(MOE_ERR_ARG, "T*k must be at most %d (got %lld): larger batches take the calls one by one",
+                    MOE_LAYER_MAX_SLOTS, (long long)(desc->T * desc->k));
+    if (I <= 0 || I % 128 != 0 || I > kLayerMaxWidth)
+        return fail(MOE_ERR_ARG, "I must be a positive multiple of 128 up to %d (got %d)", kLayerMaxWidth, I);
+    return MOE_OK;
+}
+
+// The plan, then h.
+size_t layer_ws_bytes(const moe_desc *desc, int32_t I)
+{
+    return sizeof(moe::LayerPlan) + static_cast<size_t>(desc->T) * desc->k * I * 2;
+}
+
 // Argument rules shared by the quantization to MXFP4 and the way back, and its
 // arguments.
 int check_mx(int64_t n, int32_t K, const void *codes, const void *scales, const void *values, int32_t is_f32,
@@ -1095,6 +1120,75 @@ int moe_expert_swiglu_mxfp4(const moe_desc *desc, const moe_handle *handle, cons
     if ((rc = check_swiglu_out(I, R, out, out_scale)) != MOE_OK)
         return rc;
     return launch_product_mx(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, I, true, out, out_scale, stream);
+}
+
+size_t moe_layer_tokens_workspace_size(const moe_desc *desc, int32_t I)
+{
+    if (check_layer(desc, I) != MOE_OK)
+        return 0;
+    ok();
+    return layer_ws_bytes(desc, I);
+}
+
+int moe_layer_tokens(const moe_desc *desc, const void *topk_idx, const float *topk_w,
+                     const uint16_t *x, int32_t H, int32_t I, int32_t w_format, const void *w1,
+                     const void *w1_scale, const void *w2, const void *w2_scale, void *workspace,
+                     size_t workspace_bytes, uint16_t *out, int32_t *flags, void *stream)
+{
+    TimingScope timing_scope;
+    int rc;
+    if ((rc = check_layer(desc, I)) != MOE_OK)
+        return rc;
+    if ((rc = check_hidden(H)) != MOE_OK)
+        return rc;
+    if (H > kLayerMaxWidth)
+        return fail(MOE_ERR_ARG, "H must be at most %d (got %d)", kLayerMaxWidth, H);
+    if (w_format != MOE_WEIGHTS_BF16 && w_format != MOE_WEIGHTS_FP8 && w_format != MOE_WEIGHTS_MXFP4)
+        return fail(MOE_ERR_ARG, "w_format must be MOE_WEIGHTS_BF16, _FP8 or _MXFP4 (got %d)", w_format);
+    if (desc->T == 0)
+        return ok();
+    if (!topk_idx || !topk_w)
+        return fail(MOE_ERR_ARG, "topk_idx and topk_w must be non-NULL [T,k] tensors");
+    if (!x || !aligned16(x))
+        return fail(MOE_ERR_ARG, "x must be a non-NULL, 16-byte aligned [T,H] bf16 tensor");
+    if (!w1 || !aligned16(w1) || !w2 || !aligned16(w2))
+        return fail(MOE_ERR_ARG, "w1 and w2 must be non-NULL, 16-byte aligned tensors of EL experts");
+    if (w_format == MOE_WEIGHTS_BF16 && (w1_scale || w2_scale))
+        return fail(MOE_ERR_ARG, "bf16 weights have no scales (they would be ignored)");
+    if (w_format != MOE_WEIGHTS_BF16 &&
+        (!w1_scale || !aligned16(w1_scale) || !w2_scale || !aligned16(w2_scale)))
+        return fail(MOE_ERR_ARG, "w1_scale and w2_scale must be non-NULL, 16-byte aligned tensors");
+    if (!out || !aligned16(out))
+        return fail(MOE_ERR_ARG, "out must be a non-NULL, 16-byte aligned [T,H] bf16 tensor");
+    if (!workspace || !aligned16(workspace) || workspace_bytes < layer_ws_bytes(desc, I))
+        return fail(MOE_ERR_WORKSPACE, "workspace must be 16-byte aligned and hold %zu bytes (got %zu)",
+                    layer_ws_bytes(desc, I), workspace ? workspace_bytes : size_t(0));
+    moe::LayerArgs a;
+    a.idx = topk_idx;
+    a.topk_w = topk_w;
+    a.x = x;
+    a.w1 = w1;
+    a.w1_scale = w1_scale;
+    a.w2 = w2;
+    a.w2_scale = w2_scale;
+    a.plan = static_cast<moe::LayerPlan *>(workspace);
+    a.h = reinterpret_cast<uint16_t *>(a.plan + 1);
+    a.out = out;
+    a.flags = flags;
+    a.T = static_cast<int32_t>(desc->T);
+    a.k = desc->k;
+    a.slots = a.T * a.k;
+    a.E = desc->E;
+    a.lb = desc->local_begin;
+    a.EL = desc->num_local;
+    a.H = H;
+    a.I = I;
+    a.idx_i64 = desc->idx_is_i64;
+    a.parts = 1;
+    hipError_t e = moe::launch_layer(a, w_format, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess)
+        return hip_fail(e, "layer_tokens launch");
+    return ok();
 }
 
 const char *moe_last_error(void) { return g_err; }

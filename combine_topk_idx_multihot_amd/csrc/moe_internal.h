@@ -211,6 +211,37 @@ struct MxArgs {
 hipError_t launch_quantize_mx(const MxArgs &a, bool f32, hipStream_t s);
 hipError_t launch_dequantize_mx(const MxArgs &a, bool f32, hipStream_t s);
 
+// A whole layer for a few tokens (layer.hip).
+constexpr int kLayerMaxSlots = 1024;  // T * k at most
+constexpr int kLayerSingleSlots = 16; // up to this many, every slot on its own
+enum { kLayerBf16 = 0, kLayerFp8 = 1, kLayerMxfp4 = 2 }; // the weights' format
+
+// Which slots share an expert's weights: items {expert, first slot in the list, how
+// many (1 .. 16), 0}, and the slots expert by expert.
+struct LayerPlan {
+    int4 items[kLayerMaxSlots];
+    int32_t list[kLayerMaxSlots];
+    int32_t count;
+    int32_t unused[3];
+};
+
+struct LayerArgs {
+    const void *idx;        // [T,k] int32 or int64
+    const float *topk_w;    // [T,k]
+    const uint16_t *x;      // [T,H] bf16
+    const void *w1, *w1_scale; // [EL,2I,H] and its scales
+    const void *w2, *w2_scale; // [EL,H,I] and its scales
+    uint16_t *h;            // workspace: [T*k,I] bf16
+    LayerPlan *plan;        // workspace
+    uint16_t *out;          // [T,H] bf16
+    int32_t *flags;         // one word or null
+    int32_t T, k, slots;    // slots = T * k
+    int32_t E, lb, EL, H, I;
+    int32_t idx_i64;
+    int32_t parts;          // waves that share a pair of slots (set by the launcher)
+};
+hipError_t launch_layer(const LayerArgs &a, int fmt, hipStream_t s);
+
 // Kernel timing request of the calling host thread (moe_time_next_call).
 // The events ride on the kernels' own dispatch packets: the first kernel of
 // the next entry point records `start`, and every kernel of it re-records

@@ -43,6 +43,10 @@ step runs in the HIP library:
       -> (rows_q [R,H/2], row_scale [R,H/32], row_w, row_token, row_expert)
   expert_gemm_mxfp4, expert_swiglu_mxfp4: the experts' products on MXFP4 rows
       and weights, arguments as for the FP8 ones
+  layer_tokens(x, topk_idx, topk_w, w1, w2, w1_scale, w2_scale, num_experts,
+               local_begin) -> out [T,H] bf16
+      a whole layer for a few tokens (T * k <= 1024) in two kernels, weights in
+      bf16 (scales None), E4M3 or MXFP4; no handle, no autograd
 
 <handle tensors> = routing_map, tokens_per_expert, padded_offsets, row_of_slot,
 status, workspace, in that order.  The workspace carries the route's row list
@@ -52,7 +56,7 @@ number of local experts) are read off the tensors' shapes.
 
 ``moe_layer`` strings the ops together around a caller-supplied expert;
 ``moe_layer_fp8`` and ``moe_layer_mxfp4`` are the FP8 and MXFP4 layers for serving,
-dispatch to combine.
+dispatch to combine; ``moe_layer_tokens`` the layer of a few tokens in one op.
 """
 from __future__ import annotations
 
@@ -489,6 +493,27 @@ def _(rows_q, row_scale, w_q, w_scale, routing_map, tokens_per_expert, padded_of
 
 
 # ---------------------------------------------------------------------------
+# a whole layer for a few tokens
+# ---------------------------------------------------------------------------
+@torch.library.custom_op(f"{_NS}::layer_tokens", mutates_args=())
+def _layer_tokens(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor, w1: torch.Tensor,
+                  w2: torch.Tensor, w1_scale: torch.Tensor | None, w2_scale: torch.Tensor | None,
+                  num_experts: int, local_begin: int) -> torch.Tensor:
+    T, k = topk_idx.shape
+    desc = B.make_desc(T, k, num_experts, local_begin, w1.shape[0],
+                       idx_is_i64=topk_idx.dtype == torch.int64)
+    return B.layer_tokens(desc, topk_idx.contiguous(), topk_w.contiguous(), x.contiguous(),
+                          w1.contiguous(), w2.contiguous(),
+                          None if w1_scale is None else w1_scale.contiguous(),
+                          None if w2_scale is None else w2_scale.contiguous())
+
+
+@_layer_tokens.register_fake
+def _(x, topk_idx, topk_w, w1, w2, w1_scale, w2_scale, num_experts, local_begin):
+    return x.new_empty(tuple(x.shape))
+
+
+# ---------------------------------------------------------------------------
 # a whole expert-parallel layer on one GPU's share
 # ---------------------------------------------------------------------------
 def moe_layer(x, topk_idx, topk_w, experts, num_experts, local_begin=0, num_local=None,
@@ -539,3 +564,14 @@ def moe_layer_mxfp4(x, topk_idx, topk_w, w1_q, w1_scale, w2_q, w2_scale, num_exp
     h_q, h_scale = expert_swiglu_mxfp4(rows_q, row_scale, w1_q, w1_scale, *where)
     Y = expert_gemm_mxfp4(h_q, h_scale, w2_q, w2_scale, *where)
     return combine_weighted(Y, topk_w, *where)
+
+
+def moe_layer_tokens(x, topk_idx, topk_w, w1, w2, num_experts, w1_scale=None, w2_scale=None,
+                     local_begin=0):
+    """The layer with SwiGLU experts for a few tokens (T * k <= 1024), in two kernels and without
+    rows, a handle or a row count: safe to capture at every size.  x [T,H] bf16 is not quantized.
+
+    Weights: w1 [EL,2I,H] (gate rows first) and w2 [EL,H,I], bf16 without scales, or E4M3 with one
+    fp32 scale per 128 x 128 block as for moe_layer_fp8; or packed MXFP4 with E8M0 scales as for
+    moe_layer_mxfp4.  For serving: no autograd."""
+    return _layer_tokens(x, topk_idx, topk_w, w1, w2, w1_scale, w2_scale, num_experts, local_begin)

@@ -479,6 +479,51 @@ int moe_expert_swiglu_mxfp4(const moe_desc *desc, const moe_handle *handle, cons
                             const uint8_t *w_scale, int32_t I, void *out, uint8_t *out_scale,
                             void *stream);
 
+/*
+ * A whole MoE layer for a few tokens, ids to outputs, in two kernels: with slot s =
+ * (t,j) of local expert e,
+ *   h[s]   = silu(gate) * up, gate = W1[e] rows 0 .. I-1 times x[t], up = rows I .. 2I-1
+ *            times x[t],
+ *   out[t] = sum over t's local slots of topk_w[s] * (W2[e] h[s]), in ascending order.
+ * What desc says of rows (pad_multiple, mode, capacity) is checked and makes no
+ * difference: no rows are laid out, no handle is needed and nothing waits; the
+ * call is safe to record into a HIP graph.
+ *   topk_idx    device [T,k] int32 or int64, T * k <= MOE_LAYER_MAX_SLOTS; -1, an id
+ *               outside [-1, E) and an expert that is not local are empty slots.  A
+ *               repeated id counts once for each of its slots (their weights add up).
+ *   topk_w      device [T,k] fp32; those of empty slots are not used.
+ *   x           device [T,H] bf16; H a positive multiple of 256, I of 128, both at
+ *               most 65536.
+ *   w_format    MOE_WEIGHTS_BF16: w1 device [EL,2I,H] and w2 device [EL,H,I] bf16, both
+ *               scales NULL.
+ *               MOE_WEIGHTS_FP8: E4M3 codes of the same shapes, w1_scale device
+ *               [EL,2I/128,H/128] and w2_scale device [EL,H/128,I/128] fp32.
+ *               MOE_WEIGHTS_MXFP4: w1 device [EL,2I,H/2], w2 device [EL,H,I/2] packed
+ *               codes, w1_scale device [EL,2I,H/32], w2_scale device [EL,H,I/32] bytes.
+ *   workspace   device, >= moe_layer_tokens_workspace_size(desc, I) bytes, 16-byte
+ *               aligned; written and read by this call only.  Calls that share one
+ *               must not overlap.
+ *   out         device [T,H] bf16 out, rounded to nearest-even; +0 for a token without
+ *               a local slot.
+ *   flags       device [1] int32 out or NULL: MOE_FLAG_BAD_ID, MOE_FLAG_DUPLICATE.
+ * Tokens are not quantized: products of bf16 with the weights' values are summed in
+ * fp32 (E4M3: each block's sum enters with its scale), h is rounded to bf16 once.
+ * (MXFP4 values past bf16's range, scale bytes of 253 and more, are infinite or NaN.)
+ * The order of every sum is fixed by the sizes: equal calls give equal bits.  All
+ * pointers but topk_idx, topk_w and flags must be 16-byte aligned; outputs must not
+ * overlap inputs.  T == 0 launches nothing.
+ */
+#define MOE_LAYER_MAX_SLOTS 1024
+enum { MOE_WEIGHTS_BF16 = 0, MOE_WEIGHTS_FP8 = 1, MOE_WEIGHTS_MXFP4 = 2 };
+
+/* Device bytes of moe_layer_tokens' workspace (0 if the arguments are invalid). */
+size_t moe_layer_tokens_workspace_size(const moe_desc *desc, int32_t I);
+
+int moe_layer_tokens(const moe_desc *desc, const void *topk_idx, const float *topk_w,
+                     const uint16_t *x, int32_t H, int32_t I, int32_t w_format, const void *w1,
+                     const void *w1_scale, const void *w2, const void *w2_scale, void *workspace,
+                     size_t workspace_bytes, uint16_t *out, int32_t *flags, void *stream);
+
 /* Message of the last failing call on this thread ("" if none). */
 const char *moe_last_error(void);
 
@@ -493,7 +538,8 @@ int moe_device_check(int device);
  * moe_combine_bwd, moe_dispatch_bwd, moe_combine_weighted,
  * moe_combine_weighted_bwd, moe_expert_gemm_fp8, moe_expert_swiglu_fp8,
  * moe_quantize_mxfp4, moe_dequantize_mxfp4, moe_dispatch_mxfp4,
- * moe_expert_gemm_mxfp4 or moe_expert_swiglu_mxfp4 call made on this host thread times its own kernels into two HIP events:
+ * moe_expert_gemm_mxfp4, moe_expert_swiglu_mxfp4 or moe_layer_tokens call made on
+ * this host thread times its own kernels into two HIP events:
  *   start_event  hipEvent_t (created by the caller, timing enabled) or NULL:
  *                takes the start time of the call's first kernel.
  *   stop_event   hipEvent_t or NULL: takes the end time of the call's last
