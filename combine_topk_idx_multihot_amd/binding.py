@@ -122,7 +122,7 @@ def lib() -> ctypes.CDLL:
         L.moe_expert_gemm_mxfp4.restype = ctypes.c_int
         L.moe_expert_swiglu_mxfp4.argtypes = [pd, ph, vp, vp, i32, i64, vp, vp, i32, vp, vp, vp]
         L.moe_expert_swiglu_mxfp4.restype = ctypes.c_int
-        L.moe_layer_tokens_workspace_size.argtypes = [pd, i32]
+        L.moe_layer_tokens_workspace_size.argtypes = [pd, i32, i32]
         L.moe_layer_tokens_workspace_size.restype = ctypes.c_size_t
         L.moe_layer_tokens.argtypes = [pd, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp,
                                        ctypes.c_size_t, vp, vp, vp]
@@ -774,8 +774,9 @@ def moe_expert_swiglu_mxfp4(desc: Desc, handle: Handle, rows_q: torch.Tensor,
 # a whole layer for a few tokens
 # ---------------------------------------------------------------------------
 
-def moe_layer_tokens_workspace_size(desc: Desc, I: int) -> int:
-    n = int(lib().moe_layer_tokens_workspace_size(ctypes.byref(desc), _int32("I", I)))
+def moe_layer_tokens_workspace_size(desc: Desc, H: int, I: int) -> int:
+    n = int(lib().moe_layer_tokens_workspace_size(ctypes.byref(desc), _int32("H", H),
+                                                  _int32("I", I)))
     if n == 0:
         raise MoeError(MOE_ERR_ARG, last_error())
     return n
@@ -831,7 +832,8 @@ def moe_layer_tokens(desc: Desc, topk_idx: torch.Tensor, topk_w: torch.Tensor, x
                      w1: torch.Tensor, w2: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor,
                      w1_scale: torch.Tensor | None = None, w2_scale: torch.Tensor | None = None,
                      flags: torch.Tensor | None = None, stream=None) -> int:
-    """out [T,H] bf16 = the layer of x [T,H] bf16 for T * k <= MOE_LAYER_MAX_SLOTS, in two kernels.
+    """out [T,H] bf16 = the layer of x [T,H] bf16 for T * k <= MOE_LAYER_MAX_SLOTS, in two or
+    three kernels.
     w1 [EL,2I,H] and w2 [EL,H,I] bf16; or E4M3 with fp32 scales per 128 x 128 block; or packed MXFP4
     [EL,2I,H/2] and [EL,H,I/2] with uint8 scales [EL,2I,H/32] and [EL,H,I/32]."""
     a = _layer_args(desc, topk_idx, topk_w, x, w1, w2, out, w1_scale, w2_scale, workspace, flags,
@@ -862,8 +864,10 @@ class PreparedLayerTokens:
 
 def _layer_workspace(desc, w2, w1_scale):
     packed = w1_scale is not None and w1_scale.dtype in _E8M0
-    return torch.empty(moe_layer_tokens_workspace_size(desc, w2.shape[-1] * (2 if packed else 1)),
-                       dtype=torch.uint8, device=w2.device)
+    if w2.dim() != 3:
+        raise MoeError(MOE_ERR_ARG, f"w2 must be [EL,H,columns] (got {tuple(w2.shape)})")
+    n = moe_layer_tokens_workspace_size(desc, w2.shape[1], w2.shape[2] * (2 if packed else 1))
+    return torch.empty(n, dtype=torch.uint8, device=w2.device)
 
 
 class _Prepared:

@@ -360,14 +360,18 @@ int launch_product_mx(const moe_desc *desc, const moe_handle *handle, const uint
 static_assert(moe::kLayerMaxSlots == MOE_LAYER_MAX_SLOTS && moe::kLayerBf16 == MOE_WEIGHTS_BF16 &&
                   moe::kLayerFp8 == MOE_WEIGHTS_FP8 && moe::kLayerMxfp4 == MOE_WEIGHTS_MXFP4,
               "the header's numbers");
-constexpr int32_t kLayerMaxWidth = 65536;
+using moe::kLayerMaxWidth;
 
 // Argument rules of moe_layer_tokens that its workspace size goes by.
-int check_layer(const moe_desc *desc, int32_t I)
+int check_layer(const moe_desc *desc, int32_t H, int32_t I)
 {
     int rc;
     if ((rc = check_desc(desc)) != MOE_OK)
         return rc;
+    if ((rc = check_hidden(H)) != MOE_OK)
+        return rc;
+    if (H > kLayerMaxWidth)
+        return fail(MOE_ERR_ARG, "H must be at most %d (got %d)", kLayerMaxWidth, H);
     if (desc->T * desc->k > MOE_LAYER_MAX_SLOTS)
         return fail(MOE_ERR_ARG, "T*k must be at most %d (got %lld): larger batches take the calls one by one",
                     MOE_LAYER_MAX_SLOTS, (long long)(desc->T * desc->k));
@@ -376,10 +380,11 @@ int check_layer(const moe_desc *desc, int32_t I)
     return MOE_OK;
 }
 
-// The plan, then h.
-size_t layer_ws_bytes(const moe_desc *desc, int32_t I)
+// The plan, then h, then (slots that share weights) their fp32 outputs.
+size_t layer_ws_bytes(const moe_desc *desc, int32_t H, int32_t I)
 {
-    return sizeof(moe::LayerPlan) + static_cast<size_t>(desc->T) * desc->k * I * 2;
+    const size_t slots = static_cast<size_t>(desc->T) * desc->k;
+    return sizeof(moe::LayerPlan) + slots * I * 2 + (slots > moe::kLayerSingleSlots ? slots * H * 4 : 0);
 }
 
 // Argument rules shared by the quantization to MXFP4 and the way back, and its
@@ -1122,12 +1127,12 @@ int moe_expert_swiglu_mxfp4(const moe_desc *desc, const moe_handle *handle, cons
     return launch_product_mx(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, I, true, out, out_scale, stream);
 }
 
-size_t moe_layer_tokens_workspace_size(const moe_desc *desc, int32_t I)
+size_t moe_layer_tokens_workspace_size(const moe_desc *desc, int32_t H, int32_t I)
 {
-    if (check_layer(desc, I) != MOE_OK)
+    if (check_layer(desc, H, I) != MOE_OK)
         return 0;
     ok();
-    return layer_ws_bytes(desc, I);
+    return layer_ws_bytes(desc, H, I);
 }
 
 int moe_layer_tokens(const moe_desc *desc, const void *topk_idx, const float *topk_w,
@@ -1137,12 +1142,8 @@ int moe_layer_tokens(const moe_desc *desc, const void *topk_idx, const float *to
 {
     TimingScope timing_scope;
     int rc;
-    if ((rc = check_layer(desc, I)) != MOE_OK)
+    if ((rc = check_layer(desc, H, I)) != MOE_OK)
         return rc;
-    if ((rc = check_hidden(H)) != MOE_OK)
-        return rc;
-    if (H > kLayerMaxWidth)
-        return fail(MOE_ERR_ARG, "H must be at most %d (got %d)", kLayerMaxWidth, H);
     if (w_format != MOE_WEIGHTS_BF16 && w_format != MOE_WEIGHTS_FP8 && w_format != MOE_WEIGHTS_MXFP4)
         return fail(MOE_ERR_ARG, "w_format must be MOE_WEIGHTS_BF16, _FP8 or _MXFP4 (got %d)", w_format);
     if (desc->T == 0)
@@ -1160,9 +1161,9 @@ int moe_layer_tokens(const moe_desc *desc, const void *topk_idx, const float *to
         return fail(MOE_ERR_ARG, "w1_scale and w2_scale must be non-NULL, 16-byte aligned tensors");
     if (!out || !aligned16(out))
         return fail(MOE_ERR_ARG, "out must be a non-NULL, 16-byte aligned [T,H] bf16 tensor");
-    if (!workspace || !aligned16(workspace) || workspace_bytes < layer_ws_bytes(desc, I))
+    if (!workspace || !aligned16(workspace) || workspace_bytes < layer_ws_bytes(desc, H, I))
         return fail(MOE_ERR_WORKSPACE, "workspace must be 16-byte aligned and hold %zu bytes (got %zu)",
-                    layer_ws_bytes(desc, I), workspace ? workspace_bytes : size_t(0));
+                    layer_ws_bytes(desc, H, I), workspace ? workspace_bytes : size_t(0));
     moe::LayerArgs a;
     a.idx = topk_idx;
     a.topk_w = topk_w;
@@ -1173,6 +1174,7 @@ int moe_layer_tokens(const moe_desc *desc, const void *topk_idx, const float *to
     a.w2_scale = w2_scale;
     a.plan = static_cast<moe::LayerPlan *>(workspace);
     a.h = reinterpret_cast<uint16_t *>(a.plan + 1);
+    a.y = reinterpret_cast<float *>(a.h + static_cast<size_t>(desc->T) * desc->k * I);
     a.out = out;
     a.flags = flags;
     a.T = static_cast<int32_t>(desc->T);
@@ -1184,7 +1186,6 @@ int moe_layer_tokens(const moe_desc *desc, const void *topk_idx, const float *to
     a.H = H;
     a.I = I;
     a.idx_i64 = desc->idx_is_i64;
-    a.parts = 1;
     hipError_t e = moe::launch_layer(a, w_format, static_cast<hipStream_t>(stream));
     if (e != hipSuccess)
         return hip_fail(e, "layer_tokens launch");

@@ -1,23 +1,23 @@
-// layer.hip -- a whole MoE layer for a few tokens, in two kernels.
+// layer.hip -- a whole MoE layer for a few tokens, in two kernels or three.
 //
 //   h[s]   = silu(W1g[e] x[t]) * (W1u[e] x[t])          for every slot s = (t, j), e its expert
 //   out[t] = sum over t's local slots of w[s] * W2[e] h[s]
-// No rows are laid out: k_layer_up writes h (bf16, one row per slot) to the
-// workspace, k_layer_down multiplies it and sums a token's slots in its own LDS.
+// No rows are laid out: the first kernel writes h (bf16, one row per slot) to the
+// workspace, the second one multiplies it and sums a token's slots (where slots
+// share weights a third one does).
 // The weights of the experts in use are what has to be read; tokens and h are
 // small and come from the L2.  Weights are widened to bf16 in registers (E4M3 and
 // E2M1 codes are exact there, an E8M0 scale too) and multiplied with bf16 tokens
-// by the bf16 matrix instructions, in fp32: those have four times the rate that
-// the weights' bytes need, and tokens that are not quantized cost nothing here.
-// The fp32 scale of a block of E4M3 weights enters after the products of its
-// columns.  h is rounded to bf16 as the experts of a bf16 layer would; everything
-// else stays in fp32 until out.
+// in fp32; the fp32 scale of a block of E4M3 weights enters after the products of
+// its columns.  Tokens that are not quantized cost nothing here: the rates of the
+// units are several times what the weights' bytes need.  h is rounded to bf16 as
+// the experts of a bf16 layer would; everything else stays in fp32 until out.
 //
-// Both kernels come in two forms.  With few slots every slot is on its own (an
-// expert that two tokens share is read twice, the second time from the L2): a
-// workgroup needs to know one id only.  With more, slots of the same expert share
-// its weights, up to 16 of them per instruction; the list of experts in use is
-// made by one workgroup of k_layer_up for k_layer_down.
+// There are two forms.  With few slots every slot is on its own (an
+// expert that two tokens share is read twice, the second time from the L2): a wave
+// keeps its share of the token in registers and passes whole rows of weights by it.
+// With more, slots of the same expert share its weights in the matrix
+// instructions, up to 16 of them.
 #include "moe_internal.h"
 #include "mx.h"
 
@@ -30,9 +30,7 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kUpWaves = 4;
-constexpr int kDownWaves = 8;
-constexpr int kAhead = 8; // loads of weights that a lane has in flight
+constexpr int kLayerWaves = 4;
 
 __device__ __forceinline__ uint32_t two_bf16(float x, float y)
 {
@@ -40,14 +38,13 @@ __device__ __forceinline__ uint32_t two_bf16(float x, float y)
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
-// Columns that the 16 bytes of a lane hold; a step is the four chunks of the
-// lanes of a row.
+// Columns that 16 bytes of weights hold: a chunk.
 template <int FMT>
 constexpr int kChunkCols = FMT == kLayerBf16 ? 8 : FMT == kLayerFp8 ? 16 : 32;
 
-// Columns 8 j .. 8 j + 7 of a lane's chunk in bf16; `scale`: the block's (MXFP4).
+// Columns 8 j .. 8 j + 7 of a chunk in bf16; `scale`: the block's (MXFP4).
 template <int FMT>
-__device__ __forceinline__ bf16x8 eight(const u32x4 &v, int j, float scale)
+__device__ __forceinline__ u32x4 eight(const u32x4 &v, int j, float scale)
 {
     u32x4 r;
     if constexpr (FMT == kLayerBf16) {
@@ -63,69 +60,7 @@ __device__ __forceinline__ bf16x8 eight(const u32x4 &v, int j, float scale)
         r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[j], scale, 2));
         r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[j], scale, 3));
     }
-    return __builtin_bit_cast(bf16x8, r);
-}
-
-// A run of 16 weight rows as one operand: lane l has row l % 16, and a quarter of
-// each step's columns.
-struct WeightRows {
-    const uint8_t *w;     // this lane's row, at its quarter
-    const uint8_t *scale; // MXFP4: the row's scales; E4M3: those of the block of rows that
-                          // this lane's results belong to
-};
-
-// acc[j] += rows j of weights * b^T over steps first, first + stride, ...: b holds
-// 16 rows of bf16, lane l the row l % 16, `x` at its quarter of the first step.
-// acc[j][i]: weight row 4 (l / 16) + i, row l % 16 of b.
-template <int FMT, int W>
-__device__ __forceinline__ void products(const WeightRows (&rows)[W], const uint16_t *__restrict__ x, int first,
-                                         int stride, int steps, f32x4 (&acc)[W])
-{
-    constexpr int C = kChunkCols<FMT>;
-    constexpr int U = kAhead / W;
-    const int quarter = (threadIdx.x & (kWave - 1)) >> 4;
-    for (int s0 = first; s0 < steps; s0 += stride * U) {
-        u32x4 v[U][W];
-        uint32_t sc[U][W];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int s = min(s0 + u * stride, steps - 1); // (beyond the last step: unused)
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                v[u][j] = *reinterpret_cast<const u32x4 *>(rows[j].w + static_cast<int64_t>(s) * 64);
-                if constexpr (FMT == kLayerMxfp4) // the scales of the row's four blocks
-                    sc[u][j] = *reinterpret_cast<const uint32_t *>(rows[j].scale + s * 4);
-                else if constexpr (FMT == kLayerFp8)
-                    sc[u][j] = *reinterpret_cast<const uint32_t *>(rows[j].scale + (s >> 1) * 4);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int s = s0 + u * stride;
-            if (s >= steps)
-                break;
-            bf16x8 b[C / 8];
-#pragma unroll
-            for (int i = 0; i < C / 8; ++i)
-                b[i] = *reinterpret_cast<const bf16x8 *>(x + s * (4 * C) + i * 8);
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                f32x4 q = FMT == kLayerFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[j];
-                const float scale = FMT == kLayerMxfp4 ? mx_scale_operand((sc[u][j] >> (quarter * 8)) & 255u) : 1.0f;
-#pragma unroll
-                for (int i = 0; i < C / 8; ++i)
-                    q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(eight<FMT>(v[u][j], i, scale), b[i], q, 0, 0, 0);
-                if constexpr (FMT == kLayerFp8) {
-                    const float f = __uint_as_float(sc[u][j]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[j][i] = fmaf(q[i], f, acc[j][i]);
-                } else {
-                    acc[j] = q;
-                }
-            }
-        }
-    }
+    return r;
 }
 
 // Bytes of a row of n columns.
@@ -135,22 +70,22 @@ __device__ __forceinline__ int64_t row_bytes(int n)
     return FMT == kLayerBf16 ? static_cast<int64_t>(n) * 2 : FMT == kLayerFp8 ? n : n >> 1;
 }
 
-// Weight row `row` of expert e of [EL, n, K] for this lane, whose results belong to
-// row `mine` (E4M3 scales are of 128 rows).
+// Row `row` of expert e of weights [EL, n, K], and its scales: MXFP4 a byte per 32
+// columns, E4M3 an fp32 per 128.
 template <int FMT>
-__device__ __forceinline__ WeightRows weight_rows(const void *w, const void *scale, int e, int n, int K, int row,
-                                                  int mine)
+__device__ __forceinline__ const uint8_t *weight_row(const void *w, int e, int n, int K, int row)
 {
-    const int quarter = (threadIdx.x & (kWave - 1)) >> 4;
-    WeightRows r;
-    r.w = static_cast<const uint8_t *>(w) + (static_cast<int64_t>(e) * n + row) * row_bytes<FMT>(K) + quarter * 16;
-    r.scale = nullptr;
+    return static_cast<const uint8_t *>(w) + (static_cast<int64_t>(e) * n + row) * row_bytes<FMT>(K);
+}
+template <int FMT>
+__device__ __forceinline__ const uint8_t *scale_row(const void *scale, int e, int n, int K, int row)
+{
+    const uint8_t *p = static_cast<const uint8_t *>(scale);
     if constexpr (FMT == kLayerMxfp4)
-        r.scale = static_cast<const uint8_t *>(scale) + (static_cast<int64_t>(e) * n + row) * (K >> 5);
+        p += (static_cast<int64_t>(e) * n + row) * (K >> 5);
     else if constexpr (FMT == kLayerFp8)
-        r.scale = static_cast<const uint8_t *>(scale) +
-                  (static_cast<int64_t>(e) * ((n + 127) >> 7) + (mine >> 7)) * (K >> 7) * 4;
-    return r;
+        p += (static_cast<int64_t>(e) * ((n + 127) >> 7) + (row >> 7)) * (K >> 7) * 4;
+    return p;
 }
 
 // The local expert of slot s, -1 if it has none here.
@@ -189,38 +124,72 @@ __device__ void write_flags(const LayerArgs &a)
         *a.flags = flags;
 }
 
-// The partial sums of the waves of a workgroup, in the order of the waves, in wave 0.
-template <int WAVES, int W>
-__device__ __forceinline__ void add_waves(f32x4 (&acc)[W], f32x4 (*part)[W][kWave])
-{
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    if (wave > 0) {
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-            part[wave - 1][j][lane] = acc[j];
-    }
-    __syncthreads();
-    if (wave == 0) {
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-#pragma unroll
-            for (int p = 0; p < WAVES - 1; ++p)
-                acc[j] += part[p][j][lane];
-    }
-}
-
 // ---------------------------------------------------------------------------
 // every slot on its own
 // ---------------------------------------------------------------------------
-// A workgroup has one slot and 8 columns of h: the operand's rows are 8 gate rows
-// and the 8 up rows, the waves take every fourth step.  Grid: [slots][I / 8], and
-// one workgroup more for the flags where they are wanted.
-template <int FMT>
-__global__ void __launch_bounds__(kUpWaves * kWave) k_layer_up_slots(LayerArgs a)
+// Rows of weights pass by a wave 64 chunks (1 KB) at a time, lane l the chunk l of
+// them, so that a load is as wide as loads get; the same columns of the token stay
+// in registers for all rows of the wave.  Two products per instruction, rows
+// interleaved.  (With the matrix instructions, whose lanes have 16 rows of weights
+// and 4 chunks of columns, a chunk of MXFP4 needs four loads of the token beside
+// its own: one token, H = 4096, I = 1024 14.5 us for the first kernel.)
+
+// The sum over the wave's lanes, in lane 63: in rows of 16 lanes, then across them.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v)
 {
-    __shared__ f32x4 part[kUpWaves - 1][1][kWave];
-    const int tiles = a.I >> 3;
-    const int s = blockIdx.x / tiles, n0 = (blockIdx.x - s * tiles) * 8;
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float wave_sum(float v)
+{
+    v = dpp_add<0x111>(v); // row_shr:1, 2, 4, 8
+    v = dpp_add<0x112>(v);
+    v = dpp_add<0x114>(v);
+    v = dpp_add<0x118>(v);
+    v = dpp_add<0x142>(v); // row_bcast:15, 31
+    return dpp_add<0x143>(v);
+}
+
+// A chunk's products with its columns of the token, added to acc (E4M3: under the
+// block's scale).
+template <int FMT>
+__device__ __forceinline__ float chunk_dot(const u32x4 &w, uint32_t scale, const u32x4 (&x)[kChunkCols<FMT> / 8],
+                                           float acc)
+{
+    float q = FMT == kLayerFp8 ? 0.f : acc;
+    const float s = FMT == kLayerMxfp4 ? mx_scale_operand(scale) : 1.0f;
+#pragma unroll
+    for (int j = 0; j < kChunkCols<FMT> / 8; ++j) {
+        const u32x4 v = eight<FMT>(w, j, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // (copies: this compiler takes the first element for any in a bit cast of one)
+            const uint32_t a = v[i], b = x[j][i];
+            q = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), q, false);
+        }
+    }
+    return FMT == kLayerFp8 ? fmaf(q, __uint_as_float(scale), acc) : q;
+}
+
+// The scale that chunk c of a row goes with.
+template <int FMT>
+__device__ __forceinline__ uint32_t chunk_scale(const uint8_t *scales, int c)
+{
+    if constexpr (FMT == kLayerMxfp4)
+        return scales[c];
+    else if constexpr (FMT == kLayerFp8)
+        return reinterpret_cast<const uint32_t *>(scales)[c >> 3];
+    return 0;
+}
+
+// A wave has one slot and N columns of h, N gate rows and N up rows.  Grid: [slots]
+// [I / (4 N)], and one workgroup more for the flags where they are wanted.
+template <int FMT>
+__global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_up_slots(LayerArgs a)
+{
+    constexpr int N = kLayerUpCols, U = kLayerUpAhead, C = kChunkCols<FMT>;
+    const int tiles = a.I / (kLayerWaves * N);
+    const int s = blockIdx.x / tiles;
     if (s == a.slots) {
         write_flags(a);
         return;
@@ -229,105 +198,194 @@ __global__ void __launch_bounds__(kUpWaves * kWave) k_layer_up_slots(LayerArgs a
     if (e < 0)
         return;
     const int lane = threadIdx.x & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int l16 = lane & 15, quarter = lane >> 4;
-    const WeightRows rows[1] = {weight_rows<FMT>(a.w1, a.w1_scale, e, 2 * a.I, a.H,
-                                                 l16 < 8 ? n0 + l16 : a.I + n0 + l16 - 8,
-                                                 quarter < 2 ? n0 : a.I + n0)};
-    const uint16_t *x = a.x + static_cast<int64_t>(s / a.k) * a.H + quarter * kChunkCols<FMT>;
-    f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
-    products<FMT, 1>(rows, x, wave, kUpWaves, a.H / (4 * kChunkCols<FMT>), acc);
-    add_waves<kUpWaves, 1>(acc, part);
-    if (wave != 0)
-        return;
-    // gate rows in the lower half of the lanes, up rows in the upper half
-    float h[4];
+    const int n0 = ((blockIdx.x - s * tiles) * kLayerWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave)) * N;
+    const uint16_t *x = a.x + static_cast<int64_t>(s / a.k) * a.H;
+    const int64_t stride = row_bytes<FMT>(a.H);
+    const uint8_t *wg = weight_row<FMT>(a.w1, e, 2 * a.I, a.H, n0), *wu = wg + a.I * stride;
+    const uint8_t *sg = scale_row<FMT>(a.w1_scale, e, 2 * a.I, a.H, n0);
+    const uint8_t *su = scale_row<FMT>(a.w1_scale, e, 2 * a.I, a.H, a.I + n0);
+    // (N divides 128: E4M3 scales are the same for all of the wave's columns)
+    const int scale_stride = FMT == kLayerMxfp4 ? a.H >> 5 : 0;
+    float acc[2 * N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        h[i] = layer_gated(acc[0][i], __shfl_xor(acc[0][i], 32));
-    if (l16 == 0 && quarter < 2)
-        *reinterpret_cast<u32x2 *>(a.h + static_cast<int64_t>(s) * a.I + n0 + quarter * 4) =
-            u32x2{two_bf16(h[0], h[1]), two_bf16(h[2], h[3])};
-}
-
-// out[t, n] of a workgroup's columns from y[part][slot][column] in LDS: fp32, in
-// ascending slot order, the first term's product rounded, each further term one fma.
-template <int COLS>
-__device__ __forceinline__ void sum_slots(const LayerArgs &a, const float *y, int parts, int n0)
-{
-    for (int i = threadIdx.x; i < a.T * (COLS / 2); i += kDownWaves * kWave) {
-        const int t = i / (COLS / 2), c = (i - t * (COLS / 2)) * 2;
-        float s0 = 0.f, s1 = 0.f;
-        bool first = true;
-        for (int j = 0; j < a.k; ++j) {
-            const int s = t * a.k + j;
-            if (slot_expert(a, s) < 0)
-                continue;
-            const float w = a.topk_w[s];
-            float v0 = y[s * COLS + c], v1 = y[s * COLS + c + 1];
-            for (int p = 1; p < parts; ++p) {
-                v0 += y[(p * a.slots + s) * COLS + c];
-                v1 += y[(p * a.slots + s) * COLS + c + 1];
+    for (int i = 0; i < 2 * N; ++i)
+        acc[i] = 0.f;
+    const int chunks = a.H / C;
+    for (int c0 = lane; c0 < chunks + lane; c0 += U * kWave) {
+        u32x4 v[U][2 * N], xv[U][C / 8];
+        uint32_t sc[U][2 * N];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = min(c0 + u * kWave, chunks - 1); // (beyond the row: left out below)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                v[u][i] = *reinterpret_cast<const u32x4 *>(wg + i * stride + c * 16);
+                v[u][N + i] = *reinterpret_cast<const u32x4 *>(wu + i * stride + c * 16);
+                sc[u][i] = chunk_scale<FMT>(sg + i * scale_stride, c);
+                sc[u][N + i] = chunk_scale<FMT>(su + i * scale_stride, c);
             }
-            s0 = first ? v0 * w : fmaf(v0, w, s0);
-            s1 = first ? v1 * w : fmaf(v1, w, s1);
-            first = false;
+#pragma unroll
+            for (int j = 0; j < C / 8; ++j)
+                xv[u][j] = *reinterpret_cast<const u32x4 *>(x + c * C + j * 8);
         }
-        *reinterpret_cast<uint32_t *>(a.out + static_cast<int64_t>(t) * a.H + n0 + c) = two_bf16(s0, s1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool in = c0 + u * kWave < chunks;
+#pragma unroll
+            for (int i = 0; i < 2 * N; ++i) {
+                const float q = chunk_dot<FMT>(v[u][i], sc[u][i], xv[u], acc[i]);
+                acc[i] = in ? q : acc[i];
+            }
+        }
+    }
+    float h[N];
+#pragma unroll
+    for (int i = 0; i < 2 * N; ++i)
+        acc[i] = wave_sum(acc[i]);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        h[i] = layer_gated(acc[i], acc[N + i]);
+    if (lane == kWave - 1) {
+        uint32_t *o = reinterpret_cast<uint32_t *>(a.h + static_cast<int64_t>(s) * a.I + n0);
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+            o[i / 2] = two_bf16(h[i], h[i + 1]);
     }
 }
 
-// A workgroup has 8 columns of out and all slots, two at a time: the operand's rows
-// are 8 weight rows of the first one's expert and 8 of the second one's, columns 0
-// and 1 of the other operand their rows of h.  Where there are fewer pairs than
-// waves, several waves share one (a.parts of them).
+// A wave has one token and N columns of out: the rows of its slots' experts one
+// behind the other, 64 chunks at a time.  A lane's products of a chunk are
+// multiplied with its slot's weight and added up; the lanes' sums last.  Grid: [T]
+// [H / (4 N)].
 template <int FMT>
-__global__ void __launch_bounds__(kDownWaves * kWave) k_layer_down_slots(LayerArgs a)
+__global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_slots(LayerArgs a)
 {
-    extern __shared__ float y[]; // [parts][slots][8]
-    const int n0 = blockIdx.x * 8;
+    constexpr int N = kLayerDownCols, U = kLayerDownAhead, C = kChunkCols<FMT>;
+    const int tiles = a.H / (kLayerWaves * N);
+    const int t = blockIdx.x / tiles;
     const int lane = threadIdx.x & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int l16 = lane & 15, quarter = lane >> 4;
-    const int steps = a.I / (4 * kChunkCols<FMT>);
-    const int part = wave % a.parts;
-    for (int p = wave / a.parts; 2 * p < a.slots; p += kDownWaves / a.parts) {
-        const int s0 = 2 * p, s1 = min(s0 + 1, a.slots - 1);
-        int e0 = __builtin_amdgcn_readfirstlane(slot_expert(a, s0));
-        int e1 = __builtin_amdgcn_readfirstlane(slot_expert(a, s1));
-        if (e0 < 0 && e1 < 0)
-            continue;
-        // (a slot without an expert here: the other one in its place)
-        const int h0 = e0 < 0 ? s1 : s0, h1 = e1 < 0 ? s0 : s1;
-        e0 = e0 < 0 ? e1 : e0;
-        e1 = e1 < 0 ? e0 : e1;
-        const int row = n0 + (l16 & 7);
-        WeightRows rows[1] = {weight_rows<FMT>(a.w2, a.w2_scale, l16 < 8 ? e0 : e1, a.H, a.I, row, n0)};
-        if constexpr (FMT == kLayerFp8)
-            rows[0].scale = weight_rows<FMT>(a.w2, a.w2_scale, quarter < 2 ? e0 : e1, a.H, a.I, row, n0).scale;
-        const uint16_t *h = a.h + static_cast<int64_t>(l16 == 0 ? h0 : h1) * a.I + quarter * kChunkCols<FMT>;
-        f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
-        products<FMT, 1>(rows, h, part, a.parts, steps, acc);
-        // rows 0 .. 7 of column 0, rows 8 .. 15 of column 1
-        if (l16 == quarter >> 1) {
-            const int s = quarter < 2 ? s0 : s1;
-            if (quarter < 2 || s1 > s0)
-                *reinterpret_cast<f32x4 *>(y + (part * a.slots + s) * 8 + (quarter & 1) * 4) = acc[0];
+    const int n0 = ((blockIdx.x - t * tiles) * kLayerWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave)) * N;
+    // the token's local slots, one per lane (k <= 64), the first ones first
+    const int mine = lane < a.k ? slot_expert(a, t * a.k + lane) : -1;
+    uint64_t local = __ballot(mine >= 0);
+    const int count = __popcll(local);
+    const float w = mine >= 0 ? a.topk_w[t * a.k + lane] : 0.f;
+    // lane i: the i-th local slot
+    int from = 0;
+    for (int i = 0; i < count; ++i) {
+        const int b = __builtin_ctzll(local);
+        local &= local - 1;
+        from = lane == i ? b : from;
+    }
+    const int expert = __shfl(mine, from);
+    const float weight = __shfl(w, from);
+    const int per = a.I / C; // chunks of a row
+    const int total = count * per;
+    const int64_t stride = row_bytes<FMT>(a.I);
+    const int scale_stride = FMT == kLayerMxfp4 ? a.I >> 5 : 0;
+    float acc[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        acc[i] = 0.f;
+    for (int base = 0; base < total; base += U * kWave) {
+        u32x4 v[U][N], hv[U][C / 8];
+        uint32_t sc[U][N];
+        float f[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int at = min(base + u * kWave + lane, total - 1); // (beyond the last: left out below)
+            const int j = at / per, c = at - j * per;
+            const int e = __shfl(expert, j), slot = t * a.k + __shfl(from, j);
+            f[u] = __shfl(weight, j);
+            const uint8_t *wr = weight_row<FMT>(a.w2, e, a.H, a.I, n0) + c * 16;
+            const uint8_t *sr = scale_row<FMT>(a.w2_scale, e, a.H, a.I, n0);
+            const uint16_t *h = a.h + static_cast<int64_t>(slot) * a.I + c * C;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                v[u][i] = *reinterpret_cast<const u32x4 *>(wr + i * stride);
+                sc[u][i] = chunk_scale<FMT>(sr + i * scale_stride, c);
+            }
+#pragma unroll
+            for (int i = 0; i < C / 8; ++i)
+                hv[u][i] = *reinterpret_cast<const u32x4 *>(h + i * 8);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool in = base + u * kWave + lane < total;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float q = chunk_dot<FMT>(v[u][i], sc[u][i], hv[u], 0.f);
+                acc[i] = in ? fmaf(q, f[u], acc[i]) : acc[i];
+            }
         }
     }
-    __syncthreads();
-    sum_slots<8>(a, y, a.parts, n0);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        acc[i] = wave_sum(acc[i]);
+    if (lane == kWave - 1) {
+        uint32_t *o = reinterpret_cast<uint32_t *>(a.out + static_cast<int64_t>(t) * a.H + n0);
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+            o[i / 2] = two_bf16(acc[i], acc[i + 1]);
+    }
 }
 
 // ---------------------------------------------------------------------------
 // slots of an expert together
 // ---------------------------------------------------------------------------
-// What k_layer_down reads, made by one workgroup of k_layer_up: per expert in use
-// and 16 of its slots an item {expert, first of its slots in the list, how many},
-// and the slots expert by expert.  One wave; an expert's slots in ascending order.
-__device__ void make_plan(const LayerArgs &a)
+// Weights are one operand of the 16x16x32 bf16 instructions, 16 rows each, 16 slots
+// the other; a lane has row l % 16 of both and a quarter of a step's columns, one
+// chunk.  The waves of a workgroup take every fourth step, their sums meet in LDS.
+
+// acc[j] += W runs of 16 rows of weights * b^T over steps first, first + stride,
+// ...; w[j], scale[j]: this lane's row of run j, `x` its row of b.
+// acc[j][i]: weight row 4 (l / 16) + i, row l % 16 of b.
+template <int FMT, int W>
+__device__ __forceinline__ void products(const uint8_t *const (&w)[W], const uint8_t *const (&scale)[W],
+                                         const uint16_t *__restrict__ x, int first, int stride, int steps,
+                                         f32x4 (&acc)[W])
 {
-    __shared__ int32_t count[kMaxLocal], begin[kMaxLocal];
+    constexpr int C = kChunkCols<FMT>;
+    const int quarter = (threadIdx.x & (kWave - 1)) >> 4;
+    for (int s = first; s < steps; s += stride) {
+        const int c = s * 4 + quarter;
+        u32x4 v[W], b[C / 8];
+        uint32_t sc[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            v[j] = *reinterpret_cast<const u32x4 *>(w[j] + c * 16);
+            sc[j] = chunk_scale<FMT>(scale[j], c);
+        }
+#pragma unroll
+        for (int i = 0; i < C / 8; ++i)
+            b[i] = *reinterpret_cast<const u32x4 *>(x + c * C + i * 8);
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            f32x4 q = FMT == kLayerFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[j];
+            const float f = FMT == kLayerMxfp4 ? mx_scale_operand(sc[j]) : 1.0f;
+#pragma unroll
+            for (int i = 0; i < C / 8; ++i)
+                q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, eight<FMT>(v[j], i, f)),
+                                                            __builtin_bit_cast(bf16x8, b[i]), q, 0, 0, 0);
+            if constexpr (FMT == kLayerFp8) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[j][i] = fmaf(q[i], __uint_as_float(sc[j]), acc[j][i]);
+            } else {
+                acc[j] = q;
+            }
+        }
+    }
+}
+
+// What the second kernel reads, made by one workgroup of the first: per expert in
+// use and 16 of its slots an item {expert, first of its slots in the list, how
+// many}, and the slots expert by expert.
+__device__ void make_plan(const LayerArgs &a, int32_t *lds) // of 2 kMaxLocal words
+{
+    int32_t *count = lds, *begin = lds + kMaxLocal;
     const int lane = threadIdx.x & (kWave - 1);
     for (int e = threadIdx.x; e < a.EL; e += blockDim.x)
         count[e] = 0;
@@ -364,31 +422,29 @@ __device__ void make_plan(const LayerArgs &a)
             a.plan->count = items;
     }
     __syncthreads();
-    // every slot's place: its expert's first, and the earlier slots of that expert
+    // every slot's place, in any order: its results do not depend on it
     for (int s = threadIdx.x; s < a.slots; s += blockDim.x) {
         const int e = slot_expert(a, s);
-        if (e < 0)
-            continue;
-        // (any order will do: a slot's results do not depend on its place)
-        a.plan->list[atomicAdd(&begin[e], 1)] = s;
+        if (e >= 0)
+            a.plan->list[atomicAdd(&begin[e], 1)] = s;
     }
 }
 
-// A workgroup has 16 columns of h for one expert: 16 gate rows and the 16 up rows,
-// the waves every fourth step, 16 of the expert's slots at a time.  Expert
-// workgroup i: expert i, or (fewer slots than experts) the expert of slot i where
-// no earlier slot has it.  Grid: [experts or slots][I / 16], and one more for the
-// plan.
-template <int FMT>
-__global__ void __launch_bounds__(kUpWaves * kWave) k_layer_up_experts(LayerArgs a)
+// A workgroup has 16 R columns of h for one expert, their gate and up rows, 16 of
+// the expert's slots at a time.  Expert workgroup i: expert i, or (fewer slots than
+// experts) the expert of slot i where no earlier slot has it.  Grid: [experts or
+// slots][I / (16 R)], and one more for the plan.
+template <int FMT, int R>
+__global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_up_experts(LayerArgs a)
 {
-    __shared__ f32x4 part[kUpWaves - 1][2][kWave];
+    __shared__ f32x4 part[kLayerWaves][2 * R][kWave];
     __shared__ int32_t list[kLayerMaxSlots];
-    const int tiles = a.I >> 4;
-    const int i0 = blockIdx.x / tiles, n0 = (blockIdx.x - i0 * tiles) * 16;
+    static_assert(sizeof part >= 2 * kMaxLocal * sizeof(int32_t), "the plan's counters lie there");
+    const int tiles = a.I / (16 * R);
+    const int i0 = blockIdx.x / tiles, n0 = (blockIdx.x - i0 * tiles) * (16 * R);
     const bool by_slot = a.slots < a.EL;
     if (i0 == (by_slot ? a.slots : a.EL)) {
-        make_plan(a);
+        make_plan(a, reinterpret_cast<int32_t *>(part));
         if (a.flags)
             write_flags(a);
         return;
@@ -412,71 +468,157 @@ __global__ void __launch_bounds__(kUpWaves * kWave) k_layer_up_experts(LayerArgs
     if (n == 0)
         return;
     __syncthreads();
-    const WeightRows rows[2] = {weight_rows<FMT>(a.w1, a.w1_scale, e, 2 * a.I, a.H, n0 + l16, n0),
-                                weight_rows<FMT>(a.w1, a.w1_scale, e, 2 * a.I, a.H, a.I + n0 + l16, a.I + n0)};
+    // runs 0 .. R-1: gate rows, R .. 2R-1: up rows.  E4M3 scales are those of the rows
+    // of this lane's results, the same for a run (its 16 rows lie in one block of 128).
+    const uint8_t *w[2 * R], *sc[2 * R];
+#pragma unroll
+    for (int j = 0; j < 2 * R; ++j) {
+        const int row = (j < R ? 0 : a.I) + n0 + (j % R) * 16 + l16;
+        w[j] = weight_row<FMT>(a.w1, e, 2 * a.I, a.H, row);
+        sc[j] = scale_row<FMT>(a.w1_scale, e, 2 * a.I, a.H, row);
+    }
     for (int p = 0; p < n; p += 16) {
         const int s = list[min(p + l16, n - 1)];
-        const uint16_t *x = a.x + static_cast<int64_t>(s / a.k) * a.H + quarter * kChunkCols<FMT>;
-        f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        products<FMT, 2>(rows, x, wave, kUpWaves, a.H / (4 * kChunkCols<FMT>), acc);
-        add_waves<kUpWaves, 2>(acc, part);
-        if (wave == 0 && p + l16 < n) {
-            float h[4];
+        f32x4 acc[2 * R];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                h[i] = layer_gated(acc[0][i], acc[1][i]);
-            *reinterpret_cast<u32x2 *>(a.h + static_cast<int64_t>(s) * a.I + n0 + quarter * 4) =
-                u32x2{two_bf16(h[0], h[1]), two_bf16(h[2], h[3])};
+        for (int j = 0; j < 2 * R; ++j)
+            acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        products<FMT, 2 * R>(w, sc, a.x + static_cast<int64_t>(s / a.k) * a.H, wave, kLayerWaves,
+                             a.H / (4 * kChunkCols<FMT>), acc);
+#pragma unroll
+        for (int j = 0; j < 2 * R; ++j)
+            part[wave][j][lane] = acc[j];
+        __syncthreads();
+        // wave j: columns 16 j .. 16 j + 15 of the R * 16
+        if (wave < R) {
+            f32x4 g = part[0][wave][lane], u = part[0][R + wave][lane];
+#pragma unroll
+            for (int q = 1; q < kLayerWaves; ++q) {
+                g += part[q][wave][lane];
+                u += part[q][R + wave][lane];
+            }
+            if (p + l16 < n) {
+                float h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    h[i] = layer_gated(g[i], u[i]);
+                *reinterpret_cast<u32x2 *>(a.h + static_cast<int64_t>(s) * a.I + n0 + wave * 16 + quarter * 4) =
+                    u32x2{two_bf16(h[0], h[1]), two_bf16(h[2], h[3])};
+            }
         }
         if (p + 16 < n)
             __syncthreads(); // the sums are read: room for the next slots'
     }
 }
 
-// A workgroup has 16 columns of out; its waves take the plan's items in turn.
+// A workgroup has an item of the plan and kLayerDownTile columns: its slots' rows of
+// W2 h go to the workspace in fp32.  Grid: [items that there can be]
+// [H / kLayerDownTile].  (A column tile's sums by the last workgroup of it to arrive,
+// in place of a third kernel, took 288 us instead of 26 at 32 tokens, MXFP4, H =
+// 2048, I = 768, 128 experts: what one XCD wrote has to leave its L2 at every
+// workgroup's end.)
 template <int FMT>
-__global__ void __launch_bounds__(kDownWaves * kWave) k_layer_down_experts(LayerArgs a)
+__global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_experts(LayerArgs a)
 {
-    extern __shared__ float y[]; // [slots][16]
-    const int n0 = blockIdx.x * 16;
+    constexpr int W = kLayerDownTile / 16;
+    static_assert(W == kLayerWaves, "a run of 16 columns per wave");
+    __shared__ f32x4 part[kLayerWaves][W][kWave];
+    const int tiles = a.H / kLayerDownTile;
+    const int item = blockIdx.x / tiles, n0 = (blockIdx.x - item * tiles) * kLayerDownTile;
+    if (item >= a.plan->count)
+        return;
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int l16 = lane & 15, quarter = lane >> 4;
-    const int items = a.plan->count;
-    for (int i = wave; i < items; i += kDownWaves) {
-        const int4 it = a.plan->items[i];
-        const int e = __builtin_amdgcn_readfirstlane(it.x);
-        const int s = a.plan->list[it.y + min(l16, it.z - 1)];
-        const WeightRows rows[1] = {weight_rows<FMT>(a.w2, a.w2_scale, e, a.H, a.I, n0 + l16, n0)};
-        const uint16_t *h = a.h + static_cast<int64_t>(s) * a.I + quarter * kChunkCols<FMT>;
-        f32x4 acc[1] = {{0.f, 0.f, 0.f, 0.f}};
-        products<FMT, 1>(rows, h, 0, 1, a.I / (4 * kChunkCols<FMT>), acc);
-        if (l16 < it.z)
-            *reinterpret_cast<f32x4 *>(y + s * 16 + quarter * 4) = acc[0];
+    const int4 it = a.plan->items[item];
+    const int e = __builtin_amdgcn_readfirstlane(it.x);
+    const int s = a.plan->list[it.y + min(l16, it.z - 1)];
+    const uint8_t *w[W], *sc[W];
+    f32x4 acc[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        w[j] = weight_row<FMT>(a.w2, e, a.H, a.I, n0 + j * 16 + l16);
+        sc[j] = scale_row<FMT>(a.w2_scale, e, a.H, a.I, n0 + j * 16 + l16);
+        acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
+    products<FMT, W>(w, sc, a.h + static_cast<int64_t>(s) * a.I, wave, kLayerWaves, a.I / (4 * kChunkCols<FMT>), acc);
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+        part[wave][j][lane] = acc[j];
     __syncthreads();
-    sum_slots<16>(a, y, 1, n0);
+    f32x4 y = part[0][wave][lane];
+#pragma unroll
+    for (int q = 1; q < kLayerWaves; ++q)
+        y += part[q][wave][lane];
+    if (l16 < it.z)
+        *reinterpret_cast<f32x4 *>(a.y + static_cast<int64_t>(s) * a.H + n0 + wave * 16 + quarter * 4) = y;
+}
+
+// out[t, n] from the slots' rows, in ascending slot order: the first term's product
+// rounded, each further term one fma.  A thread has four columns of a token.
+__global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_sum(LayerArgs a)
+{
+    const int quads = a.H >> 2;
+    const int i = blockIdx.x * (kLayerWaves * kWave) + threadIdx.x;
+    const int t = i / quads, n = (i - t * quads) * 4; // (H is a multiple of 256: a wave has one token)
+    if (t >= a.T)
+        return;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int mine = lane < a.k ? slot_expert(a, t * a.k + lane) : -1;
+    const float w = mine >= 0 ? a.topk_w[t * a.k + lane] : 0.f;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    bool first = true;
+    uint64_t local = __ballot(mine >= 0);
+    const float *y = a.y + static_cast<int64_t>(t) * a.k * a.H + n;
+    while (local) {
+        constexpr int kBatch = 8;
+        f32x4 v[kBatch];
+        int slot[kBatch];
+        int count = 0;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            slot[b] = local ? __builtin_ctzll(local) : slot[0]; // (no more: the first one again, unused)
+            count += local != 0;
+            local &= local - 1;
+            v[b] = *reinterpret_cast<const f32x4 *>(y + static_cast<int64_t>(slot[b]) * a.H);
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const float f = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), slot[b]));
+            if (b < count) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    sum[q] = first ? v[b][q] * f : fmaf(v[b][q], f, sum[q]);
+                first = false;
+            }
+        }
+    }
+    *reinterpret_cast<u32x2 *>(a.out + static_cast<int64_t>(t) * a.H + n) =
+        u32x2{two_bf16(sum[0], sum[1]), two_bf16(sum[2], sum[3])};
 }
 
 // ---------------------------------------------------------------------------
 // launch
 // ---------------------------------------------------------------------------
 template <int FMT>
-static hipError_t launch_layer_of(const LayerArgs &a0, hipStream_t s)
+static hipError_t launch_layer_of(const LayerArgs &a, hipStream_t s)
 {
-    LayerArgs a = a0;
-    const dim3 up(kUpWaves * kWave), down(kDownWaves * kWave);
+    const dim3 blk(kLayerWaves * kWave);
     if (a.slots <= kLayerSingleSlots) {
-        const int pairs = (a.slots + 1) / 2;
-        a.parts = 1;
-        while (a.parts * 2 * pairs <= kDownWaves)
-            a.parts *= 2;
-        launch(k_layer_up_slots<FMT>, dim3(a.slots * (a.I / 8) + (a.flags ? 1 : 0)), up, 0, s, a);
-        launch(k_layer_down_slots<FMT>, dim3(a.H / 8), down, a.parts * a.slots * 8 * sizeof(float), s, a);
+        launch(k_layer_up_slots<FMT>, dim3(a.slots * (a.I / (kLayerWaves * kLayerUpCols)) + (a.flags ? 1 : 0)), blk, 0,
+               s, a);
+        launch(k_layer_down_slots<FMT>, dim3(a.T * (a.H / (kLayerWaves * kLayerDownCols))), blk, 0, s, a);
     } else {
         const int64_t groups = a.slots < a.EL ? a.slots : a.EL;
-        launch(k_layer_up_experts<FMT>, dim3(static_cast<unsigned>(groups * (a.I / 16) + 1)), up, 0, s, a);
-        launch(k_layer_down_experts<FMT>, dim3(a.H / 16), down, a.slots * 16 * sizeof(float), s, a);
+        // 32 columns per workgroup where that makes enough of them
+        const int64_t wide = groups * (a.I / 32);
+        if (wide >= 4 * kCus)
+            launch(k_layer_up_experts<FMT, 2>, dim3(static_cast<unsigned>(wide + 1)), blk, 0, s, a);
+        else
+            launch(k_layer_up_experts<FMT, 1>, dim3(static_cast<unsigned>(2 * wide + 1)), blk, 0, s, a);
+        launch(k_layer_down_experts<FMT>,
+               dim3(static_cast<unsigned>(layer_items(a.slots, a.EL) * (a.H / kLayerDownTile))), blk, 0, s, a);
+        launch(k_layer_sum, dim3((a.T * (a.H / 4) + kLayerWaves * kWave - 1) / (kLayerWaves * kWave)), blk, 0, s, a);
     }
     return hipGetLastError();
 }

@@ -213,7 +213,13 @@ hipError_t launch_dequantize_mx(const MxArgs &a, bool f32, hipStream_t s);
 
 // A whole layer for a few tokens (layer.hip).
 constexpr int kLayerMaxSlots = 1024;  // T * k at most
+constexpr int kLayerMaxWidth = 65536; // H and I at most
 constexpr int kLayerSingleSlots = 16; // up to this many, every slot on its own
+constexpr int kLayerUpCols = 2;       // columns of h per wave there
+constexpr int kLayerDownCols = 2;     // columns of out per wave there
+constexpr int kLayerUpAhead = 1;      // runs of 64 chunks that a wave has in flight
+constexpr int kLayerDownAhead = 2;
+constexpr int kLayerDownTile = 64;    // columns of out per workgroup otherwise
 enum { kLayerBf16 = 0, kLayerFp8 = 1, kLayerMxfp4 = 2 }; // the weights' format
 
 // Which slots share an expert's weights: items {expert, first slot in the list, how
@@ -225,6 +231,14 @@ struct LayerPlan {
     int32_t unused[3];
 };
 
+// The most items that `slots` slots of EL experts make: one per expert in use, and
+// one more for every 16 slots beyond its first.
+inline int64_t layer_items(int64_t slots, int64_t EL)
+{
+    const int64_t groups = slots < EL ? slots : EL;
+    return groups + (slots - groups) / 16;
+}
+
 struct LayerArgs {
     const void *idx;        // [T,k] int32 or int64
     const float *topk_w;    // [T,k]
@@ -232,13 +246,13 @@ struct LayerArgs {
     const void *w1, *w1_scale; // [EL,2I,H] and its scales
     const void *w2, *w2_scale; // [EL,H,I] and its scales
     uint16_t *h;            // workspace: [T*k,I] bf16
+    float *y;               // workspace: [T*k,H] fp32, where slots share experts' weights
     LayerPlan *plan;        // workspace
     uint16_t *out;          // [T,H] bf16
     int32_t *flags;         // one word or null
     int32_t T, k, slots;    // slots = T * k
     int32_t E, lb, EL, H, I;
     int32_t idx_i64;
-    int32_t parts;          // waves that share a pair of slots (set by the launcher)
 };
 hipError_t launch_layer(const LayerArgs &a, int fmt, hipStream_t s);
 

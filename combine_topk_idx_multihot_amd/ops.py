@@ -45,7 +45,7 @@ step runs in the HIP library:
       and weights, arguments as for the FP8 ones
   layer_tokens(x, topk_idx, topk_w, w1, w2, w1_scale, w2_scale, num_experts,
                local_begin) -> out [T,H] bf16
-      a whole layer for a few tokens (T * k <= 1024) in two kernels, weights in
+      a whole layer for a few tokens (T * k <= 1024) in two or three kernels, weights in
       bf16 (scales None), E4M3 or MXFP4; no handle, no autograd
 
 <handle tensors> = routing_map, tokens_per_expert, padded_offsets, row_of_slot,
@@ -568,8 +568,8 @@ def moe_layer_mxfp4(x, topk_idx, topk_w, w1_q, w1_scale, w2_q, w2_scale, num_exp
 
 def moe_layer_tokens(x, topk_idx, topk_w, w1, w2, num_experts, w1_scale=None, w2_scale=None,
                      local_begin=0):
-    """The layer with SwiGLU experts for a few tokens (T * k <= 1024), in two kernels and without
-    rows, a handle or a row count: safe to capture at every size.  x [T,H] bf16 is not quantized.
+    """The layer with SwiGLU experts for a few tokens (T * k <= 1024), in two or three kernels and
+    without rows, a handle or a row count: safe to capture at every size.  x [T,H] bf16 is not quantized.
 
     Weights: w1 [EL,2I,H] (gate rows first) and w2 [EL,H,I], bf16 without scales, or E4M3 with one
     fp32 scale per 128 x 128 block as for moe_layer_fp8; or packed MXFP4 with E8M0 scales as for

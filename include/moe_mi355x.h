@@ -480,11 +480,11 @@ int moe_expert_swiglu_mxfp4(const moe_desc *desc, const moe_handle *handle, cons
                             void *stream);
 
 /*
- * A whole MoE layer for a few tokens, ids to outputs, in two kernels: with slot s =
- * (t,j) of local expert e,
+ * A whole MoE layer for a few tokens, ids to outputs, in two kernels (T * k <= 16) or
+ * three: with slot s = (t,j) of local expert e,
  *   h[s]   = silu(gate) * up, gate = W1[e] rows 0 .. I-1 times x[t], up = rows I .. 2I-1
  *            times x[t],
- *   out[t] = sum over t's local slots of topk_w[s] * (W2[e] h[s]), in ascending order.
+ *   out[t] = sum over t's local slots of topk_w[s] * (W2[e] h[s]).
  * What desc says of rows (pad_multiple, mode, capacity) is checked and makes no
  * difference: no rows are laid out, no handle is needed and nothing waits; the
  * call is safe to record into a HIP graph.
@@ -500,7 +500,7 @@ int moe_expert_swiglu_mxfp4(const moe_desc *desc, const moe_handle *handle, cons
  *               [EL,2I/128,H/128] and w2_scale device [EL,H/128,I/128] fp32.
  *               MOE_WEIGHTS_MXFP4: w1 device [EL,2I,H/2], w2 device [EL,H,I/2] packed
  *               codes, w1_scale device [EL,2I,H/32], w2_scale device [EL,H,I/32] bytes.
- *   workspace   device, >= moe_layer_tokens_workspace_size(desc, I) bytes, 16-byte
+ *   workspace   device, >= moe_layer_tokens_workspace_size(desc, H, I) bytes, 16-byte
  *               aligned; written and read by this call only.  Calls that share one
  *               must not overlap.
  *   out         device [T,H] bf16 out, rounded to nearest-even; +0 for a token without
@@ -517,7 +517,7 @@ int moe_expert_swiglu_mxfp4(const moe_desc *desc, const moe_handle *handle, cons
 enum { MOE_WEIGHTS_BF16 = 0, MOE_WEIGHTS_FP8 = 1, MOE_WEIGHTS_MXFP4 = 2 };
 
 /* Device bytes of moe_layer_tokens' workspace (0 if the arguments are invalid). */
-size_t moe_layer_tokens_workspace_size(const moe_desc *desc, int32_t I);
+size_t moe_layer_tokens_workspace_size(const moe_desc *desc, int32_t H, int32_t I);
 
 int moe_layer_tokens(const moe_desc *desc, const void *topk_idx, const float *topk_w,
                      const uint16_t *x, int32_t H, int32_t I, int32_t w_format, const void *w1,

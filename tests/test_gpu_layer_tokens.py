@@ -5,10 +5,12 @@ streams, graphs, two calls at once.
 
 Bounds (u = 2^-24): products of bf16 with the weights' values are exact in fp32; a sum of n of them, in
 whatever order the matrix instructions take, is off by at most one step (2u) of the sum of magnitudes S
-per addition; the additions are the n products', one per instruction of 32 columns, one per 64 columns
-with E4M3 weights and those of up to 8 partial sums: n + n / 32 + n / 64 + 8 <= 1.1 n + 8.  silu as in
-expert_ref.swiglu.  h is rounded to bf16 (half a step, 2^-8), the combine adds k products of fp32 with
-one rounding each."""
+per addition; the additions on a product's way are at most the n products', one per instruction of 32
+columns or one per 16 columns with E4M3 weights, and those of up to 64 partial sums in a tree:
+n + n / 16 + 8 <= 1.1 n + 8.  silu as in expert_ref.swiglu.  h is rounded to bf16 (half a step, 2^-8).
+The combine adds k products of fp32 with one rounding each, or multiplies each lane's run of 8 to 32
+products with its slot's weight: those runs leave most of the 1.1 n above for the k I / 512 of them at
+most that a lane adds up, as k I / 512 <= I / 8 for k <= 64."""
 import pytest
 import torch
 
@@ -89,7 +91,7 @@ def check(fmt, d, idx, w, x, w1, s1, w2, s2, what):
     T, H, lb = d.T, x.shape[1], d.local_begin
     I = w2.shape[2] * (2 if fmt == "mxfp4" else 1)
     out = torch.full((T + 1, H), -12345.0, dtype=torch.bfloat16, device="cuda")
-    n = B.moe_layer_tokens_workspace_size(d, I)
+    n = B.moe_layer_tokens_workspace_size(d, H, I)
     ws = torch.full((n + 64,), 0x55, dtype=torch.uint8, device="cuda")
     flags = torch.full((2,), 77, dtype=torch.int32, device="cuda")
     B.moe_layer_tokens(d, idx, w, x, w1, w2, out, ws[:n], s1, s2, flags)
@@ -144,8 +146,7 @@ def test_no_local_slot_and_bad_ids(T, k, fmt):
     clean = torch.where((idx < 8) | (idx >= 16), 0.0, w)
     x[0] = float("nan")  # nor is a token without a local slot
     out = torch.empty((T, 512), dtype=torch.bfloat16, device="cuda")
-    I = 128
-    ws = torch.empty(B.moe_layer_tokens_workspace_size(d, I), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(B.moe_layer_tokens_workspace_size(d, 512, 128), dtype=torch.uint8, device="cuda")
     B.moe_layer_tokens(d, idx, w, x, rest[0], rest[2], out, ws, rest[1], rest[3])
     x = torch.where(torch.isnan(x), 0.0, x)
     want, bound = exact(fmt, x, idx.long(), clean, rest[0], rest[1], rest[2], rest[3], 8)

@@ -30,16 +30,17 @@ def test_description():
     assert layer(_desc(mode=B.MOE_SYNC_FREE, capacity=10)) == B.MOE_ERR_CAPACITY
     assert layer(_desc(T=129)) == B.MOE_ERR_ARG and "1024" in B.last_error()
     assert layer(_desc(T=1025, k=1)) == B.MOE_ERR_ARG
-    assert B.lib().moe_layer_tokens_workspace_size(ctypes.byref(_desc(T=129)), 256) == 0
+    assert B.lib().moe_layer_tokens_workspace_size(ctypes.byref(_desc(T=129)), 512, 256) == 0
 
 
 def test_sizes():
     for H in (0, -256, 128, 384):
         assert layer(H=H) == B.MOE_ERR_HIDDEN
+        assert B.lib().moe_layer_tokens_workspace_size(ctypes.byref(_desc()), H, 256) == 0
     assert layer(H=65792) == B.MOE_ERR_ARG
     for I in (0, -128, 64, 200, 65664):
         assert layer(I=I) == B.MOE_ERR_ARG, I
-        assert B.lib().moe_layer_tokens_workspace_size(ctypes.byref(_desc()), I) == 0
+        assert B.lib().moe_layer_tokens_workspace_size(ctypes.byref(_desc()), 512, I) == 0
     for fmt in (-1, 3):
         assert layer(fmt=fmt) == B.MOE_ERR_ARG and "w_format" in B.last_error()
 
@@ -56,11 +57,11 @@ def test_pointers():
 
 
 def test_workspace():
-    need = B.moe_layer_tokens_workspace_size(_desc(), 256)
-    assert need >= 4 * 8 * 256 * 2
+    need = B.moe_layer_tokens_workspace_size(_desc(), 512, 256)
+    assert need >= 4 * 8 * (256 * 2 + 512 * 4)
     assert layer(ws=None) == B.MOE_ERR_WORKSPACE and layer(ws=FAKE + 8) == B.MOE_ERR_WORKSPACE
     assert layer(n=need - 1) == B.MOE_ERR_WORKSPACE and str(need) in B.last_error()
-    assert B.moe_layer_tokens_workspace_size(_desc(T=0), 128) > 0
+    assert B.moe_layer_tokens_workspace_size(_desc(T=0), 256, 128) > 0
 
 
 def test_no_tokens_launch_nothing():
