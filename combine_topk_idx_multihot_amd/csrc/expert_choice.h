@@ -88,14 +88,16 @@ inline ExpertKernel choose_expert_kernel(const ExpertLoad &l, int K, int N, bool
 }
 
 // The same for MXFP4 rows and weights.
-inline ExpertKernel choose_mx_kernel(const ExpertLoad &l, int K, int N, bool gated)
+inline ExpertKernel choose_mx_kernel(const ExpertLoad &l, int N, bool gated)
 {
-    (void)K;
     const int cols = gated ? kTileCols / 2 : kTileCols;
     const int64_t tiles = l.groups * ((static_cast<int64_t>(N) + cols - 1) / cols);
     if (l.group_max <= 32 && tiles * l.rows_mean <= 4 * kCus)
         return ExpertKernel::rows;
-    return ExpertKernel::ring;
+    const int64_t ring_tiles = tiles * ((l.rows_mean + kRingRows - 1) / kRingRows);
+    if (l.rows_mean <= 64 || ring_tiles <= 2 * kCus)
+        return ExpertKernel::ring;
+    return ExpertKernel::tile;
 }
 
 }  // namespace moe

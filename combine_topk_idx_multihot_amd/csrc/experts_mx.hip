@@ -16,6 +16,8 @@
 #include "expert_tiles.h"
 #include "mx.h"
 
+#include <type_traits>
+
 namespace moe {
 
 constexpr int kFp4 = 4; // the instructions' number for E2M1
@@ -195,8 +197,8 @@ __global__ void __launch_bounds__(kMxSplit * kWave) k_expert_mx_rows(MxExpertArg
 // their scales, 8 bytes a row.  In a step the instruction i = 0 .. 3 takes chunk
 // 4 (l / 32) + i of lane l's row, so that the four scales of a lane are one
 // aligned word.  Where K is no multiple of 256 the last step has half as many
-// columns: its upper chunks repeat the lower ones, and the lanes that would use
-// them put zeros in place of the weights.
+// columns: its upper chunks repeat the lower ones, and the lanes that use them take
+// scales of 2^-127 on both sides: products below 2^-240, which vanish in fp32.
 // ---------------------------------------------------------------------------
 struct MxRingLds {
     static constexpr int kRows = kRingRows;
@@ -312,13 +314,10 @@ __global__ void __launch_bounds__(kMxRingWaves * kWave) k_expert_mx_ring(MxExper
                 wf[i] = *lds_at<lds_chunk>(at + mine * 128 + place_of(mine, upper * 4 + i) * 16);
                 xf[i] = *lds_at<lds_chunk>(at + L::kX + l32 * 128 + place_of(l32, upper * 4 + i) * 16);
             }
-            const uint32_t ws = *lds_at<lds_word>(at + L::kSW + mine * 8 + upper * 4);
-            const uint32_t xs = *lds_at<lds_word>(at + L::kSX + l32 * 8 + upper * 4);
-            if (cut && upper) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    wf[i] = u32x4{0u, 0u, 0u, 0u};
-            }
+            uint32_t ws = *lds_at<lds_word>(at + L::kSW + mine * 8 + upper * 4);
+            uint32_t xs = *lds_at<lds_word>(at + L::kSX + l32 * 8 + upper * 4);
+            if (cut && upper)
+                ws = xs = 0;
             acc = mfma_mx64<0>(wf[0], ws, xf[0], xs, acc);
             acc = mfma_mx64<1>(wf[1], ws, xf[1], xs, acc);
             acc = mfma_mx64<2>(wf[2], ws, xf[2], xs, acc);
@@ -371,6 +370,307 @@ __global__ void __launch_bounds__(kMxRingWaves * kWave) k_expert_mx_ring(MxExper
 }
 
 // ---------------------------------------------------------------------------
+// Products with many rows per expert: workgroups of four waves, one per CU and one
+// wave per SIMD, each taking tiles of up to 256 rows by 256 weight rows (gated: 128
+// gate and 128 up rows) one after the other.  A wave has half of the rows (32 of
+// each block of 64) and 128 weight rows: 16 accumulators of 32 x 32, which is what
+// its 512 registers hold, and the fewest LDS reads per product.  Rows, weights and
+// their scales come through LDS 256 columns (a step) at a time, in two stages: while
+// a step is worked on, the next one's data, or the first step's of the next tile, is
+// on its way.
+//
+// Per step and CU 256 32x32x64 instructions (33.6 Mflop), 68 KB into LDS and 132 KB
+// out of it.
+// ---------------------------------------------------------------------------
+constexpr int kMxTileWaves = 4;
+constexpr int kMxTileRows = 256;
+
+struct MxTileLds {
+    static constexpr uint32_t kX = kTileCols * 128;  // in a stage: weight rows, rows,
+    static constexpr uint32_t kSW = kX + kMxTileRows * 128; // scales of the weight rows,
+    static constexpr uint32_t kSX = kSW + kTileCols * 8;    // of the rows
+    static constexpr uint32_t kStage = kSX + kMxTileRows * 8;
+    static constexpr uint32_t kPre = 2 * kStage;
+    static constexpr uint32_t kOff = kPre + (kMaxLocal + 1) * 4;
+    static constexpr uint32_t kBytes = kOff + (kMaxLocal + 1) * 4;
+    static_assert(kBytes <= 160 * 1024, "LDS of a CU");
+};
+
+// Where a wave's loads of a tile come from: 8 rows each, lane l's row l / 8 and the
+// chunk that belongs at place l % 8; scales 32 rows each, two words a row.
+struct MxAim {
+    const uint8_t *w, *x, *sw, *sx;
+    uint32_t woff[8], xoff[8]; // rows' byte offsets
+    uint32_t wrow[2], xrow[2]; // offsets of rows' scales
+};
+
+template <bool GATED>
+__device__ __forceinline__ void mx_aim(const MxExpertArgs &a, const Tile &t, MxAim &m)
+{
+    constexpr int kOut = GATED ? 128 : kTileCols;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = uniform(threadIdx.x / kWave);
+    const uint32_t row_bytes = a.K >> 1, row_blocks = a.K >> 5;
+    // gated: waves 0 and 1 bring the gate rows, 2 and 3 the up rows
+    const int64_t first = static_cast<int64_t>(t.e) * (GATED ? 2 * a.N : a.N) +
+                          static_cast<int64_t>(t.ni) * kOut + (GATED && wave >= 2 ? a.N : 0);
+    const int base = GATED ? (wave & 1) * 64 : wave * 64;
+    const int last = GATED ? 127 : a.N - 1 - t.ni * kOut;
+    m.w = a.w + first * row_bytes;
+    m.sw = a.sw + first * row_blocks;
+    m.x = a.a + t.r0 * row_bytes;
+    m.sx = a.sa + t.r0 * row_blocks;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        m.woff[i] = min(base + i * 8 + (lane >> 3), last) * row_bytes;
+        // load i of the rows: rows 32 i + 8 wave .. + 7, so that fewer blocks of 64 rows take
+        // fewer loads
+        m.xoff[i] = min(i * 32 + wave * 8 + (lane >> 3), t.rows - 1) * row_bytes;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        m.wrow[i] = min(base + i * 32 + (lane >> 1), last) * row_blocks;
+        m.xrow[i] = min(i * 128 + wave * 32 + (lane >> 1), t.rows - 1) * row_blocks;
+    }
+}
+
+// Part `part` (0 .. 3) of the loads of step b, for M blocks of 64 rows, to the stage
+// at `at`; cut: the step has 128 columns, its upper chunks repeat the lower ones.
+template <int M>
+__device__ __forceinline__ void mx_send(const MxAim &m, int part, int b, bool cut, uint32_t at)
+{
+    typedef MxTileLds L;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = uniform(threadIdx.x / kWave);
+    at = uniform(at);
+    // (a row's place depends on its number modulo 16 only; all of these are 8 i + l / 8)
+#pragma unroll
+    for (int i = 2 * part; i < 2 * part + 2; ++i) {
+        int c = place_of(i * 8 + (lane >> 3), lane & 7);
+        c = cut ? c & 3 : c;
+        lds_load16(at + (wave * 8 + i) * 1024, m.w + b * 128 + (m.woff[i] + c * 16));
+        if (i < 2 * M) {
+            c = place_of(wave * 8 + (lane >> 3), lane & 7);
+            c = cut ? c & 3 : c;
+            lds_load16(at + L::kX + (i * 4 + wave) * 1024, m.x + b * 128 + (m.xoff[i] + c * 16));
+        }
+    }
+    const uint32_t word = cut ? 0 : (lane & 1) * 4;
+    if (part < 2)
+        lds_load4(at + L::kSW + (wave * 2 + part) * 256, m.sw + b * 8 + (m.wrow[part] + word));
+    else if ((part - 2) * 128 + wave * 32 < 64 * M)
+        lds_load4(at + L::kSX + ((part - 2) * 4 + wave) * 256, m.sx + b * 8 + (m.xrow[part - 2] + word));
+}
+
+// One tile with M blocks of 64 rows, whose first step has been sent for; sends for
+// the first one of `next` during the last step.
+template <int M, bool GATED, bool MX>
+__device__ __forceinline__ void mx_tile_run(const MxExpertArgs &a, const Tile &t, const Tile &next, MxAim &aim,
+                                            uint32_t &stage)
+{
+    typedef MxTileLds L;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = uniform(threadIdx.x / kWave);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int l32 = lane & 31, upper = lane >> 5;
+    const int steps = (a.K + 255) >> 8;
+    const bool half = a.K & 255;
+    const int xrow = wm * 32 + l32; // + 64 m
+    // weight row of run j: plain, 32 j of this wave's 128; gated, runs 0 and 1 gate rows, 2 and 3
+    // the up rows of the same columns
+    const int wrow = (GATED ? wn * 64 : wn * 128) + l32;
+    constexpr int kRun2 = (GATED ? 128 : 64) * 128; // from runs 0 and 1 to 2 and 3
+    uint32_t wad[4], xad[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        wad[i] = wrow * 128 + place_of(wrow, upper * 4 + i) * 16;
+        xad[i] = L::kX + xrow * 128 + place_of(xrow, upper * 4 + i) * 16;
+    }
+    const uint32_t wsad = L::kSW + wrow * 8 + upper * 4, xsad = L::kSX + xrow * 8 + upper * 4;
+    f32x16 acc[M][4];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc[m][j] = f32x16{};
+    for (int b = 0; b < steps; ++b) {
+        step_barrier<0>(); // this step's data is there, the other stage is free
+        const uint32_t at = stage, to = L::kStage - stage;
+        const bool more = b + 1 < steps, any = more || next.e >= 0;
+        const bool cut = half && b + 1 == steps;
+        const bool cut_next = half && (more ? b + 2 == steps : steps == 1);
+        const int bn = more ? b + 1 : 0;
+        if (!more && any)
+            mx_aim<GATED>(a, next, aim);
+        uint32_t ws[4], xs[M];
+        u32x4 w[2][4], x[2][M];
+        const auto read = [&](int k) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[k & 1][j] = *lds_at<lds_chunk>(at + wad[k] + (j & 1) * 4096 + (j >> 1) * kRun2);
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+                x[k & 1][m] = *lds_at<lds_chunk>(at + xad[k] + m * 8192);
+        };
+        read(0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            ws[j] = *lds_at<lds_word>(at + wsad + (j & 1) * 256 + (j >> 1) * (kRun2 / 16));
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+            xs[m] = *lds_at<lds_word>(at + xsad + m * 512);
+        if (cut && upper) { // scales of 2^-127 on both sides: products that vanish beside any other
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                ws[j] = 0;
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+                xs[m] = 0;
+        }
+        const auto multiply = [&](auto kc) {
+            constexpr int k = decltype(kc)::value;
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[m][j] = mfma_mx64<k>(w[k & 1][j], ws[j], x[k & 1][m], xs[m], acc[m][j]);
+        };
+        const auto send = [&](int part) {
+            if (any)
+                more ? mx_send<M>(aim, part, bn, cut_next, to) : mx_send<4>(aim, part, bn, cut_next, to);
+        };
+        read(1);
+        send(0);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(std::integral_constant<int, 0>{});
+        __builtin_amdgcn_sched_barrier(0);
+        read(2);
+        send(1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(std::integral_constant<int, 1>{});
+        __builtin_amdgcn_sched_barrier(0);
+        read(3);
+        send(2);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(std::integral_constant<int, 2>{});
+        __builtin_amdgcn_sched_barrier(0);
+        send(3);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(std::integral_constant<int, 3>{});
+        __builtin_amdgcn_sched_barrier(0);
+        stage = to;
+    }
+    // accumulator element i of a lane: weight row 8 (i / 4) + 4 upper + i % 4
+    if constexpr (!GATED) {
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                // as in k_expert_tile: four lanes trade, so that a store writes whole cache lines
+                u32x4 v[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    v[c] = pack_eights(acc[m][2 * p + (c >> 1)], (c & 1) * 2);
+                trade<1>(v[0], v[1]);
+                trade<1>(v[2], v[3]);
+                trade<2>(v[0], v[2]);
+                trade<2>(v[1], v[3]);
+                const int row = 64 * m + (xrow & ~3);
+                const int n = t.ni * kTileCols + wn * 128 + p * 64 + (lane & 3) * 16 + upper * 8;
+                uint16_t *o = static_cast<uint16_t *>(a.out) + (t.r0 + row) * a.N + n;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (row + i < t.rows && n < a.N)
+                        *reinterpret_cast<u32x4 *>(o + static_cast<int64_t>(i) * a.N) = v[i];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    acc[m][j][i] = gated(acc[m][j][i], acc[m][j + 2][i]);
+            if constexpr (MX) {
+                const int row = 64 * m + xrow;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    // a block of 32 columns is the 16 values of this lane and of lane ^ 32
+                    const f32x16 &h = acc[m][j];
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        top = max(top, mag_bits(h[i]));
+                    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
+                    const uint32_t sc = mx_scale(top);
+                    uint32_t lo = mx_pack_eights(f32x4{h[0], h[1], h[2], h[3]}, f32x4{h[4], h[5], h[6], h[7]}, sc);
+                    uint32_t hi = mx_pack_eights(f32x4{h[8], h[9], h[10], h[11]}, f32x4{h[12], h[13], h[14], h[15]}, sc);
+                    whole_eights(lo, hi); // 16 columns per lane
+                    const int n = t.ni * 128 + wn * 64 + j * 32;
+                    if (row < t.rows) {
+                        *reinterpret_cast<u32x2 *>(static_cast<uint8_t *>(a.out) + (t.r0 + row) * (a.N >> 1) + (n >> 1) +
+                                                   upper * 8) = u32x2{lo, hi};
+                        if (upper == 0)
+                            a.out_scale[(t.r0 + row) * (a.N >> 5) + (n >> 5)] = static_cast<uint8_t>(sc);
+                    }
+                }
+            } else {
+                u32x4 v[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    v[c] = pack_eights(acc[m][c >> 1], (c & 1) * 2);
+                trade<1>(v[0], v[1]);
+                trade<1>(v[2], v[3]);
+                trade<2>(v[0], v[2]);
+                trade<2>(v[1], v[3]);
+                const int row = 64 * m + (xrow & ~3);
+                uint16_t *o = static_cast<uint16_t *>(a.out) + (t.r0 + row) * a.N + t.ni * 128 + wn * 64 +
+                              (lane & 3) * 16 + upper * 8;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (row + i < t.rows)
+                        *reinterpret_cast<u32x4 *>(o + static_cast<int64_t>(i) * a.N) = v[i];
+            }
+        }
+    }
+}
+
+template <bool GATED, bool MX>
+__global__ void __launch_bounds__(kMxTileWaves * kWave) __attribute__((amdgpu_waves_per_eu(1, 1)))
+k_expert_mx_tile(MxExpertArgs a)
+{
+    typedef MxTileLds L;
+    extern __shared__ uint8_t tile_lds[]; // all of it by address, from 0
+    flag_mismatch(a);
+    if (uniform(threadIdx.x / kWave) == 0)
+        tile_tables<kMxTileRows>(a, L::kPre, L::kOff);
+    asm volatile("" : : "v"(tile_lds) : "memory"); // (as in k_expert_tile)
+    __syncthreads();
+    TileList<kMxTileRows> list(a, L::kPre, L::kOff);
+    Tile t = list.next(a);
+    if (t.e < 0)
+        return;
+    MxAim aim;
+    uint32_t stage = 0;
+    mx_aim<GATED>(a, t, aim);
+#pragma unroll
+    for (int part = 0; part < 4; ++part)
+        mx_send<4>(aim, part, 0, a.K < 256, 0);
+    while (t.e >= 0) {
+        const Tile next = list.next(a);
+        switch ((t.rows + 63) >> 6) {
+        case 1: mx_tile_run<1, GATED, MX>(a, t, next, aim, stage); break;
+        case 2: mx_tile_run<2, GATED, MX>(a, t, next, aim, stage); break;
+        case 3: mx_tile_run<3, GATED, MX>(a, t, next, aim, stage); break;
+        default: mx_tile_run<4, GATED, MX>(a, t, next, aim, stage); break;
+        }
+        t = next;
+    }
+    // (the last step sent for nothing, and waited for what came before)
+}
+
+// ---------------------------------------------------------------------------
 // launch
 // ---------------------------------------------------------------------------
 static hipError_t launch_mx_rows(MxExpertArgs &a, hipStream_t s)
@@ -406,12 +706,31 @@ static hipError_t launch_mx_ring(MxExpertArgs &a, hipStream_t s)
     return hipGetLastError();
 }
 
+static hipError_t launch_mx_tile(MxExpertArgs &a, hipStream_t s)
+{
+    const int cols = a.gated ? 128 : kTileCols;
+    a.ntn = (a.N + cols - 1) / cols;
+    const int64_t nb = tiles_max(a, kMxTileRows);
+    if (nb > 0x7FFFFFFF)
+        return hipErrorInvalidConfiguration;
+    const dim3 g(static_cast<unsigned>(nb < kCus ? nb : kCus)), blk(kMxTileWaves * kWave);
+    if (!a.gated)
+        launch(k_expert_mx_tile<false, false>, g, blk, MxTileLds::kBytes, s, a);
+    else if (a.out_scale)
+        launch(k_expert_mx_tile<true, true>, g, blk, MxTileLds::kBytes, s, a);
+    else
+        launch(k_expert_mx_tile<true, false>, g, blk, MxTileLds::kBytes, s, a);
+    return hipGetLastError();
+}
+
 hipError_t launch_expert_product_mx(const MxExpertArgs &a0, hipStream_t s)
 {
     MxExpertArgs a = a0;
-    if (choose_mx_kernel(a.load, a.K, a.N, a.gated != 0) == ExpertKernel::rows)
-        return launch_mx_rows(a, s);
-    return launch_mx_ring(a, s);
+    switch (choose_mx_kernel(a.load, a.N, a.gated != 0)) {
+    case ExpertKernel::rows: return launch_mx_rows(a, s);
+    case ExpertKernel::ring: return launch_mx_ring(a, s);
+    default: return launch_mx_tile(a, s);
+    }
 }
 
 }  // namespace moe
