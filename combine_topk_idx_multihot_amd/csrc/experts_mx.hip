@@ -400,8 +400,8 @@ struct MxTileLds {
 // chunk that belongs at place l % 8; scales 32 rows each, two words a row.
 struct MxAim {
     const uint8_t *w, *x, *sw, *sx;
-    uint32_t woff[8], xoff[8]; // rows' byte offsets
-    uint32_t wrow[2], xrow[2]; // offsets of rows' scales
+    uint32_t woff[8], xoff[8]; // byte offsets of rows and chunks
+    uint32_t wrow[2], xrow[2]; // of rows' scales
 };
 
 template <bool GATED>
@@ -422,10 +422,12 @@ __device__ __forceinline__ void mx_aim(const MxExpertArgs &a, const Tile &t, MxA
     m.sx = a.sa + t.r0 * row_blocks;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        m.woff[i] = min(base + i * 8 + (lane >> 3), last) * row_bytes;
+        // (a row's place depends on its number modulo 16 only)
+        m.woff[i] = min(base + i * 8 + (lane >> 3), last) * row_bytes + place_of(i * 8 + (lane >> 3), lane & 7) * 16;
         // load i of the rows: rows 32 i + 8 wave .. + 7, so that fewer blocks of 64 rows take
         // fewer loads
-        m.xoff[i] = min(i * 32 + wave * 8 + (lane >> 3), t.rows - 1) * row_bytes;
+        m.xoff[i] = min(i * 32 + wave * 8 + (lane >> 3), t.rows - 1) * row_bytes +
+                    place_of(wave * 8 + (lane >> 3), lane & 7) * 16;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -434,39 +436,45 @@ __device__ __forceinline__ void mx_aim(const MxExpertArgs &a, const Tile &t, MxA
     }
 }
 
-// Part `part` (0 .. 3) of the loads of step b, for M blocks of 64 rows, to the stage
-// at `at`; cut: the step has 128 columns, its upper chunks repeat the lower ones.
+// Load p (0 .. kMxSends - 1) of step b, for M blocks of 64 rows, to the stage at `at`:
+// first the weights' and rows' scales, two each, then weights and rows in turn, eight
+// each.  cut: the step has 128 columns, its upper chunks repeat the lower ones.
+constexpr int kMxSends = 20;
+constexpr int kMxSends0 = 12; // of them in the first round
+
 template <int M>
-__device__ __forceinline__ void mx_send(const MxAim &m, int part, int b, bool cut, uint32_t at)
+__device__ __forceinline__ void mx_send(const MxAim &m, int p, int b, bool cut, uint32_t at)
 {
     typedef MxTileLds L;
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = uniform(threadIdx.x / kWave);
     at = uniform(at);
-    // (a row's place depends on its number modulo 16 only; all of these are 8 i + l / 8)
-#pragma unroll
-    for (int i = 2 * part; i < 2 * part + 2; ++i) {
-        int c = place_of(i * 8 + (lane >> 3), lane & 7);
-        c = cut ? c & 3 : c;
-        lds_load16(at + (wave * 8 + i) * 1024, m.w + b * 128 + (m.woff[i] + c * 16));
-        if (i < 2 * M) {
-            c = place_of(wave * 8 + (lane >> 3), lane & 7);
-            c = cut ? c & 3 : c;
-            lds_load16(at + L::kX + (i * 4 + wave) * 1024, m.x + b * 128 + (m.xoff[i] + c * 16));
-        }
+    if (p < 4) {
+        const int i = p >> 1;
+        const uint32_t word = cut ? 0 : (lane & 1) * 4;
+        if ((p & 1) == 0)
+            lds_load4(at + L::kSW + (wave * 2 + i) * 256, m.sw + b * 8 + (m.wrow[i] + word));
+        else if (i * 128 < 64 * M) // (of blocks of 128 rows: more than needed where M is odd)
+            lds_load4(at + L::kSX + (i * 4 + wave) * 256, m.sx + b * 8 + (m.xrow[i] + word));
+        return;
     }
-    const uint32_t word = cut ? 0 : (lane & 1) * 4;
-    if (part < 2)
-        lds_load4(at + L::kSW + (wave * 2 + part) * 256, m.sw + b * 8 + (m.wrow[part] + word));
-    else if ((part - 2) * 128 + wave * 32 < 64 * M)
-        lds_load4(at + L::kSX + ((part - 2) * 4 + wave) * 256, m.sx + b * 8 + (m.xrow[part - 2] + word));
+    const int i = (p - 4) >> 1;
+    if ((p & 1) == 0) {
+        const uint32_t back = cut ? (place_of(i * 8 + (lane >> 3), lane & 7) & 4) * 16 : 0;
+        lds_load16(at + (wave * 8 + i) * 1024, m.w + b * 128 + (m.woff[i] - back));
+    } else if (i < 2 * M) {
+        const uint32_t back = cut ? (place_of(wave * 8 + (lane >> 3), lane & 7) & 4) * 16 : 0;
+        lds_load16(at + L::kX + (i * 4 + wave) * 1024, m.x + b * 128 + (m.xoff[i] - back));
+    }
 }
 
 // One tile with M blocks of 64 rows, whose first step has been sent for; sends for
-// the first one of `next` during the last step.
+// the first one of `next` during the last step.  `keep`: vector memory accesses (the
+// last tile's stores) newer than that, which may be on their way at the start.
+// Returns the same for the next tile.
 template <int M, bool GATED, bool MX>
-__device__ __forceinline__ void mx_tile_run(const MxExpertArgs &a, const Tile &t, const Tile &next, MxAim &aim,
-                                            uint32_t &stage)
+__device__ __forceinline__ int mx_tile_run(const MxExpertArgs &a, const Tile &t, const Tile &next, MxAim &aim,
+                                           uint32_t &stage, int keep)
 {
     typedef MxTileLds L;
     const int lane = threadIdx.x & (kWave - 1);
@@ -493,32 +501,48 @@ __device__ __forceinline__ void mx_tile_run(const MxExpertArgs &a, const Tile &t
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             acc[m][j] = f32x16{};
-    for (int b = 0; b < steps; ++b) {
-        step_barrier<0>(); // this step's data is there, the other stage is free
+    // A step: four rounds of 4 M matrix instructions, one chunk of every row each.  What the
+    // next round and the next step need is read and sent for one piece at a time behind the
+    // instructions, in exactly this order: a wave is alone on its SIMD, and whatever it issues
+    // in a run of its own leaves the matrix unit idle (with all reads and loads of a round ahead
+    // of its instructions a step took twice the time).
+    // SM: the blocks of rows to send for, at most.
+    const auto step = [&](auto smc, int bn, bool cut, bool cut_next) {
+        constexpr int SM = decltype(smc)::value;
+        // this step's data is there, the other stage is free
+        if (keep >= 32)
+            step_barrier<32>();
+        else if (keep >= 16)
+            step_barrier<16>();
+        else if (keep >= 8)
+            step_barrier<8>();
+        else if (keep >= 4)
+            step_barrier<4>();
+        else
+            step_barrier<0>();
+        keep = 0;
         const uint32_t at = stage, to = L::kStage - stage;
-        const bool more = b + 1 < steps, any = more || next.e >= 0;
-        const bool cut = half && b + 1 == steps;
-        const bool cut_next = half && (more ? b + 2 == steps : steps == 1);
-        const int bn = more ? b + 1 : 0;
-        if (!more && any)
-            mx_aim<GATED>(a, next, aim);
         uint32_t ws[4], xs[M];
         u32x4 w[2][4], x[2][M];
-        const auto read = [&](int k) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                w[k & 1][j] = *lds_at<lds_chunk>(at + wad[k] + (j & 1) * 4096 + (j >> 1) * kRun2);
-#pragma unroll
-            for (int m = 0; m < M; ++m)
-                x[k & 1][m] = *lds_at<lds_chunk>(at + xad[k] + m * 8192);
+        const auto read = [&](int k, int i) { // runs of weights, then blocks of rows
+            if (i < 4)
+                w[k & 1][i] = *lds_at<lds_chunk>(at + wad[k] + (i & 1) * 4096 + (i >> 1) * kRun2);
+            else
+                x[k & 1][i - 4] = *lds_at<lds_chunk>(at + xad[k] + (i - 4) * 8192);
         };
-        read(0);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             ws[j] = *lds_at<lds_word>(at + wsad + (j & 1) * 256 + (j >> 1) * (kRun2 / 16));
 #pragma unroll
         for (int m = 0; m < M; ++m)
             xs[m] = *lds_at<lds_word>(at + xsad + m * 512);
+        read(0, 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            read(0, i);
+#pragma unroll
+        for (int i = 5; i < 4 + M; ++i)
+            read(0, i);
         if (cut && upper) { // scales of 2^-127 on both sides: products that vanish beside any other
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -527,39 +551,40 @@ __device__ __forceinline__ void mx_tile_run(const MxExpertArgs &a, const Tile &t
             for (int m = 0; m < M; ++m)
                 xs[m] = 0;
         }
-        const auto multiply = [&](auto kc) {
+        __builtin_amdgcn_sched_barrier(0);
+        const auto round = [&](auto kc) {
             constexpr int k = decltype(kc)::value;
+            // the sends early, as the next step waits for them
+            constexpr int kReads = k < 3 ? 4 + M : 0, kSends = k == 0 ? kMxSends0 : k == 1 ? kMxSends - kMxSends0 : 0;
+            constexpr int kPieces = kReads + kSends > 0 ? kReads + kSends : 1, kSend0 = k == 0 ? 0 : kMxSends0;
 #pragma unroll
-            for (int m = 0; m < M; ++m)
+            for (int q = 0; q < 4 * M; ++q) {
+                acc[q / 4][q % 4] = mfma_mx64<k>(w[k & 1][q % 4], ws[q % 4], x[k & 1][q / 4], xs[q / 4],
+                                                 acc[q / 4][q % 4]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[m][j] = mfma_mx64<k>(w[k & 1][j], ws[j], x[k & 1][m], xs[m], acc[m][j]);
+                for (int p = q * kPieces / (4 * M); p < (q + 1) * kPieces / (4 * M) && p < kReads + kSends; ++p) {
+                    // (in turn, as many of each as there are)
+                    const int r = p * kReads / kPieces, r1 = (p + 1) * kReads / kPieces;
+                    if (r1 > r)
+                        read(k + 1, r);
+                    else
+                        mx_send<SM>(aim, kSend0 + p - r, bn, cut_next, to);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
         };
-        const auto send = [&](int part) {
-            if (any)
-                more ? mx_send<M>(aim, part, bn, cut_next, to) : mx_send<4>(aim, part, bn, cut_next, to);
-        };
-        read(1);
-        send(0);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(std::integral_constant<int, 0>{});
-        __builtin_amdgcn_sched_barrier(0);
-        read(2);
-        send(1);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(std::integral_constant<int, 1>{});
-        __builtin_amdgcn_sched_barrier(0);
-        read(3);
-        send(2);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(std::integral_constant<int, 2>{});
-        __builtin_amdgcn_sched_barrier(0);
-        send(3);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(std::integral_constant<int, 3>{});
-        __builtin_amdgcn_sched_barrier(0);
+        round(std::integral_constant<int, 0>{});
+        round(std::integral_constant<int, 1>{});
+        round(std::integral_constant<int, 2>{});
+        round(std::integral_constant<int, 3>{});
         stage = to;
-    }
+    };
+    for (int b = 0; b + 1 < steps; ++b)
+        step(std::integral_constant<int, M>{}, b + 1, false, half && b + 2 == steps);
+    // (without a next tile: this one's last step again, unused)
+    if (next.e >= 0)
+        mx_aim<GATED>(a, next, aim);
+    step(std::integral_constant<int, 4>{}, next.e >= 0 ? 0 : steps - 1, half, half && (next.e < 0 || steps == 1));
     // accumulator element i of a lane: weight row 8 (i / 4) + 4 upper + i % 4
     if constexpr (!GATED) {
 #pragma unroll
@@ -634,6 +659,9 @@ __device__ __forceinline__ void mx_tile_run(const MxExpertArgs &a, const Tile &t
             }
         }
     }
+    // (the waits above count on every one of a whole tile's stores)
+    const bool all = t.rows == 64 * M && (GATED || (t.ni + 1) * kTileCols <= a.N);
+    return all ? (GATED ? 4 * M : 8 * M) : 0;
 }
 
 template <bool GATED, bool MX>
@@ -653,21 +681,23 @@ k_expert_mx_tile(MxExpertArgs a)
         return;
     MxAim aim;
     uint32_t stage = 0;
+    int keep = 0;
     mx_aim<GATED>(a, t, aim);
 #pragma unroll
-    for (int part = 0; part < 4; ++part)
-        mx_send<4>(aim, part, 0, a.K < 256, 0);
+    for (int p = 0; p < kMxSends; ++p)
+        mx_send<4>(aim, p, 0, a.K < 256, 0);
     while (t.e >= 0) {
         const Tile next = list.next(a);
         switch ((t.rows + 63) >> 6) {
-        case 1: mx_tile_run<1, GATED, MX>(a, t, next, aim, stage); break;
-        case 2: mx_tile_run<2, GATED, MX>(a, t, next, aim, stage); break;
-        case 3: mx_tile_run<3, GATED, MX>(a, t, next, aim, stage); break;
-        default: mx_tile_run<4, GATED, MX>(a, t, next, aim, stage); break;
+        case 1: keep = mx_tile_run<1, GATED, MX>(a, t, next, aim, stage, keep); break;
+        case 2: keep = mx_tile_run<2, GATED, MX>(a, t, next, aim, stage, keep); break;
+        case 3: keep = mx_tile_run<3, GATED, MX>(a, t, next, aim, stage, keep); break;
+        default: keep = mx_tile_run<4, GATED, MX>(a, t, next, aim, stage, keep); break;
         }
         t = next;
     }
-    // (the last step sent for nothing, and waited for what came before)
+    // no load to LDS may be left when the workgroup ends
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
 }
 
 // ---------------------------------------------------------------------------
