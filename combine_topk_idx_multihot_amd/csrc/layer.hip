@@ -91,9 +91,12 @@ __device__ __forceinline__ const uint8_t *scale_row(const void *scale, int e, in
 // The local expert of slot s, -1 if it has none here.
 __device__ __forceinline__ int slot_expert(const LayerArgs &a, int s)
 {
-    const int64_t id = a.idx_i64 ? static_cast<const int64_t *>(a.idx)[s] : static_cast<const int32_t *>(a.idx)[s];
-    const int64_t e = id - a.lb;
-    return e >= 0 && e < a.EL && id < a.E ? static_cast<int>(e) : -1;
+    // both widths without a branch, so that loads of several ids go out together
+    const int32_t *p = static_cast<const int32_t *>(a.idx) + (static_cast<int64_t>(s) << a.idx_i64);
+    const int id = p[0], high = p[a.idx_i64];
+    const bool whole = !a.idx_i64 || high == 0; // (the ids that matter are not negative)
+    const int e = id - a.lb;
+    return whole && id >= a.lb && e < a.EL ? e : -1;
 }
 
 __device__ __forceinline__ float layer_gated(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
@@ -339,42 +342,102 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_slots(LayerA
 // the other; a lane has row l % 16 of both and a quarter of a step's columns, one
 // chunk.  The waves of a workgroup take every fourth step, their sums meet in LDS.
 
-// acc[j] += W runs of 16 rows of weights * b^T over steps first, first + stride,
-// ...; w[j], scale[j]: this lane's row of run j, `x` its row of b.
+// W runs of 16 rows of weights: this lane's row of each and that row's scales, and its
+// chunks of a unit of U steps.  The scales of a unit are loaded together: MXFP4 rows
+// have 4 bytes for a step, all four quarters of a row the same ones, and a load
+// for each step touched as many cache lines as the weights did (32 tokens, H = 2048, I =
+// 768: the first kernel 66 instead of 51 us).
+template <int FMT, int W, int U>
+struct Runs {
+    const uint8_t *w[W], *scale[W];
+    u32x4 v[U][W];
+    uint32_t sc[U][W];
+    __device__ __forceinline__ void load(int unit, int steps)
+    {
+        typedef uint32_t words __attribute__((ext_vector_type(U), aligned(4)));
+        const int quarter = (threadIdx.x & (kWave - 1)) >> 4;
+        const int s0 = unit * U;
+#pragma unroll
+        for (int u = 0; u < U; ++u) // (steps beyond the last: unused)
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                v[u][j] = *reinterpret_cast<const u32x4 *>(w[j] + (min(s0 + u, steps - 1) * 4 + quarter) * 16);
+        if constexpr (FMT == kLayerMxfp4) {
+            if (s0 + U <= steps) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    const words q = *reinterpret_cast<const words *>(scale[j] + s0 * 4);
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        sc[u][j] = q[u];
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        sc[u][j] = reinterpret_cast<const uint32_t *>(scale[j])[min(s0 + u, steps - 1)];
+            }
+        } else if constexpr (FMT == kLayerFp8) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < W; ++j) // two steps to a scale; (unit * U is even)
+                    sc[u][j] = u & 1 ? sc[u - 1][j]
+                                     : reinterpret_cast<const uint32_t *>(scale[j])[min(s0 + u, steps - 1) >> 1];
+        }
+    }
+};
+
+// acc[j] += run j * b^T over units first, first + kLayerWaves, ..., the first of which
+// has been loaded (where there is one); `x`: this lane's row of b, zeros where it has
+// none (not `mine`).
 // acc[j][i]: weight row 4 (l / 16) + i, row l % 16 of b.
-template <int FMT, int W>
-__device__ __forceinline__ void products(const uint8_t *const (&w)[W], const uint8_t *const (&scale)[W],
-                                         const uint16_t *__restrict__ x, int first, int stride, int steps,
-                                         f32x4 (&acc)[W])
+template <int FMT, int W, int U>
+__device__ __forceinline__ void products(Runs<FMT, W, U> &r, const uint16_t *__restrict__ x, bool mine, int first,
+                                         int steps, f32x4 (&acc)[W])
 {
+    static_assert(U % 2 == 0, "E4M3 scales are of two steps");
     constexpr int C = kChunkCols<FMT>;
     const int quarter = (threadIdx.x & (kWave - 1)) >> 4;
-    for (int s = first; s < steps; s += stride) {
-        const int c = s * 4 + quarter;
-        u32x4 v[W], b[C / 8];
-        uint32_t sc[W];
+    for (int unit = first; unit * U < steps; unit += kLayerWaves) {
+        if (unit != first)
+            r.load(unit, steps);
+        u32x4 b[U][C / 8];
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            v[j] = *reinterpret_cast<const u32x4 *>(w[j] + c * 16);
-            sc[j] = chunk_scale<FMT>(scale[j], c);
-        }
-#pragma unroll
-        for (int i = 0; i < C / 8; ++i)
-            b[i] = *reinterpret_cast<const u32x4 *>(x + c * C + i * 8);
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-            f32x4 q = FMT == kLayerFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[j];
-            const float f = FMT == kLayerMxfp4 ? mx_scale_operand(sc[j]) : 1.0f;
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < C / 8; ++i)
-                q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, eight<FMT>(v[j], i, f)),
-                                                            __builtin_bit_cast(bf16x8, b[i]), q, 0, 0, 0);
-            if constexpr (FMT == kLayerFp8) {
+                b[u][i] = u32x4{0u, 0u, 0u, 0u};
+        if (mine) { // (rows that are not there cost nothing)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[j][i] = fmaf(q[i], __uint_as_float(sc[j]), acc[j][i]);
-            } else {
-                acc[j] = q;
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < C / 8; ++i)
+                    b[u][i] = *reinterpret_cast<const u32x4 *>(x + (min(unit * U + u, steps - 1) * 4 + quarter) * C + i * 8);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (unit * U + u < steps) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    f32x4 q = FMT == kLayerFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[j];
+                    const float f =
+                        FMT == kLayerMxfp4 ? mx_scale_operand((r.sc[u][j] >> (quarter * 8)) & 255u) : 1.0f;
+#pragma unroll
+                    for (int i = 0; i < C / 8; ++i)
+                        q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8, eight<FMT>(r.v[u][j], i, f)),
+                            __builtin_bit_cast(bf16x8, b[u][i]), q, 0, 0, 0);
+                    if constexpr (FMT == kLayerFp8) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc[j][i] = fmaf(q[i], __uint_as_float(r.sc[u][j]), acc[j][i]);
+                    } else {
+                        acc[j] = q;
+                    }
+                }
             }
         }
     }
@@ -430,18 +493,19 @@ __device__ void make_plan(const LayerArgs &a, int32_t *lds) // of 2 kMaxLocal wo
     }
 }
 
-// A workgroup has 16 R columns of h for one expert, their gate and up rows, 16 of
-// the expert's slots at a time.  Expert workgroup i: expert i, or (fewer slots than
-// experts) the expert of slot i where no earlier slot has it.  Grid: [experts or
-// slots][I / (16 R)], and one more for the plan.
-template <int FMT, int R>
+// A workgroup has 16 columns of h for one expert, their gate and up rows, its waves
+// every fourth unit of them; 16 of the expert's slots at a time.  Expert workgroup i:
+// expert i, or (fewer slots than experts) the expert of slot i where no earlier slot has
+// it.  Grid: [experts or slots][I / 16], and one more for the plan.
+template <int FMT>
 __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_up_experts(LayerArgs a)
 {
-    __shared__ f32x4 part[kLayerWaves][2 * R][kWave];
+    __shared__ f32x4 part[kLayerWaves][2][kWave];
     __shared__ int32_t list[kLayerMaxSlots];
     static_assert(sizeof part >= 2 * kMaxLocal * sizeof(int32_t), "the plan's counters lie there");
-    const int tiles = a.I / (16 * R);
-    const int i0 = blockIdx.x / tiles, n0 = (blockIdx.x - i0 * tiles) * (16 * R);
+    constexpr int U = kLayerUnit;
+    const int tiles = a.I >> 4;
+    const int i0 = blockIdx.x / tiles, n0 = (blockIdx.x - i0 * tiles) * 16;
     const bool by_slot = a.slots < a.EL;
     if (i0 == (by_slot ? a.slots : a.EL)) {
         make_plan(a, reinterpret_cast<int32_t *>(part));
@@ -455,54 +519,57 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_up_experts(LayerA
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int l16 = lane & 15, quarter = lane >> 4;
+    // gate rows and up rows.  E4M3 scales are those of the rows of this lane's results, the
+    // same for a run (its 16 rows lie in one block of 128).
+    Runs<FMT, 2, U> runs;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        runs.w[j] = weight_row<FMT>(a.w1, e, 2 * a.I, a.H, j * a.I + n0 + l16);
+        runs.scale[j] = scale_row<FMT>(a.w1_scale, e, 2 * a.I, a.H, j * a.I + n0 + l16);
+    }
+    const int steps = a.H / (4 * kChunkCols<FMT>);
     int n = 0;
-    for (int base = 0; base < a.slots; base += kWave) {
-        const int s = base + lane;
-        const uint64_t m = __ballot(s < a.slots && slot_expert(a, s) == e);
-        if (by_slot && n == 0 && m && base + __builtin_ctzll(m) < i0)
-            return; // an earlier slot's workgroups have this expert
-        if (wave == 0 && (m >> lane & 1))
-            list[n + __popcll(m & ((1ull << lane) - 1))] = s;
-        n += __popcll(m);
+    for (int base = 0; base < a.slots; base += 4 * kWave) {
+        int id[4]; // (all loads first)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            id[i] = slot_expert(a, min(base + i * kWave + lane, a.slots - 1));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s = base + i * kWave + lane;
+            const uint64_t m = __ballot(s < a.slots && id[i] == e);
+            if (by_slot && n == 0 && m && base + i * kWave + __builtin_ctzll(m) < i0)
+                return; // an earlier slot's workgroups have this expert
+            if (wave == 0 && (m >> lane & 1))
+                list[n + __popcll(m & ((1ull << lane) - 1))] = s;
+            n += __popcll(m);
+        }
     }
     if (n == 0)
         return;
+    runs.load(min(wave, (steps - 1) / U), steps);
     __syncthreads();
-    // runs 0 .. R-1: gate rows, R .. 2R-1: up rows.  E4M3 scales are those of the rows
-    // of this lane's results, the same for a run (its 16 rows lie in one block of 128).
-    const uint8_t *w[2 * R], *sc[2 * R];
-#pragma unroll
-    for (int j = 0; j < 2 * R; ++j) {
-        const int row = (j < R ? 0 : a.I) + n0 + (j % R) * 16 + l16;
-        w[j] = weight_row<FMT>(a.w1, e, 2 * a.I, a.H, row);
-        sc[j] = scale_row<FMT>(a.w1_scale, e, 2 * a.I, a.H, row);
-    }
     for (int p = 0; p < n; p += 16) {
         const int s = list[min(p + l16, n - 1)];
-        f32x4 acc[2 * R];
-#pragma unroll
-        for (int j = 0; j < 2 * R; ++j)
-            acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-        products<FMT, 2 * R>(w, sc, a.x + static_cast<int64_t>(s / a.k) * a.H, wave, kLayerWaves,
-                             a.H / (4 * kChunkCols<FMT>), acc);
-#pragma unroll
-        for (int j = 0; j < 2 * R; ++j)
-            part[wave][j][lane] = acc[j];
+        f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        if (p)
+            runs.load(min(wave, (steps - 1) / U), steps);
+        products(runs, a.x + static_cast<int64_t>(s / a.k) * a.H, p + l16 < n, wave, steps, acc);
+        part[wave][0][lane] = acc[0];
+        part[wave][1][lane] = acc[1];
         __syncthreads();
-        // wave j: columns 16 j .. 16 j + 15 of the R * 16
-        if (wave < R) {
-            f32x4 g = part[0][wave][lane], u = part[0][R + wave][lane];
+        if (wave == 0) {
 #pragma unroll
             for (int q = 1; q < kLayerWaves; ++q) {
-                g += part[q][wave][lane];
-                u += part[q][R + wave][lane];
+                acc[0] += part[q][0][lane];
+                acc[1] += part[q][1][lane];
             }
             if (p + l16 < n) {
                 float h[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    h[i] = layer_gated(g[i], u[i]);
-                *reinterpret_cast<u32x2 *>(a.h + static_cast<int64_t>(s) * a.I + n0 + wave * 16 + quarter * 4) =
+                    h[i] = layer_gated(acc[0][i], acc[1][i]);
+                *reinterpret_cast<u32x2 *>(a.h + static_cast<int64_t>(s) * a.I + n0 + quarter * 4) =
                     u32x2{two_bf16(h[0], h[1]), two_bf16(h[2], h[3])};
             }
         }
@@ -520,7 +587,7 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_up_experts(LayerA
 template <int FMT>
 __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_experts(LayerArgs a)
 {
-    constexpr int W = kLayerDownTile / 16;
+    constexpr int W = kLayerDownTile / 16, U = kLayerUnit;
     static_assert(W == kLayerWaves, "a run of 16 columns per wave");
     __shared__ f32x4 part[kLayerWaves][W][kWave];
     const int tiles = a.H / kLayerDownTile;
@@ -532,16 +599,18 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_experts(Laye
     const int l16 = lane & 15, quarter = lane >> 4;
     const int4 it = a.plan->items[item];
     const int e = __builtin_amdgcn_readfirstlane(it.x);
-    const int s = a.plan->list[it.y + min(l16, it.z - 1)];
-    const uint8_t *w[W], *sc[W];
+    const int steps = a.I / (4 * kChunkCols<FMT>);
+    Runs<FMT, W, U> runs;
     f32x4 acc[W];
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-        w[j] = weight_row<FMT>(a.w2, e, a.H, a.I, n0 + j * 16 + l16);
-        sc[j] = scale_row<FMT>(a.w2_scale, e, a.H, a.I, n0 + j * 16 + l16);
+        runs.w[j] = weight_row<FMT>(a.w2, e, a.H, a.I, n0 + j * 16 + l16);
+        runs.scale[j] = scale_row<FMT>(a.w2_scale, e, a.H, a.I, n0 + j * 16 + l16);
         acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    products<FMT, W>(w, sc, a.h + static_cast<int64_t>(s) * a.I, wave, kLayerWaves, a.I / (4 * kChunkCols<FMT>), acc);
+    runs.load(min(wave, (steps - 1) / U), steps);
+    const int s = a.plan->list[it.y + min(l16, it.z - 1)];
+    products(runs, a.h + static_cast<int64_t>(s) * a.I, l16 < it.z, wave, steps, acc);
 #pragma unroll
     for (int j = 0; j < W; ++j)
         part[wave][j][lane] = acc[j];
@@ -604,18 +673,13 @@ template <int FMT>
 static hipError_t launch_layer_of(const LayerArgs &a, hipStream_t s)
 {
     const dim3 blk(kLayerWaves * kWave);
-    if (a.slots <= kLayerSingleSlots) {
+    if (layer_singles(a.slots, a.E)) {
         launch(k_layer_up_slots<FMT>, dim3(a.slots * (a.I / (kLayerWaves * kLayerUpCols)) + (a.flags ? 1 : 0)), blk, 0,
                s, a);
         launch(k_layer_down_slots<FMT>, dim3(a.T * (a.H / (kLayerWaves * kLayerDownCols))), blk, 0, s, a);
     } else {
         const int64_t groups = a.slots < a.EL ? a.slots : a.EL;
-        // 32 columns per workgroup where that makes enough of them
-        const int64_t wide = groups * (a.I / 32);
-        if (wide >= 4 * kCus)
-            launch(k_layer_up_experts<FMT, 2>, dim3(static_cast<unsigned>(wide + 1)), blk, 0, s, a);
-        else
-            launch(k_layer_up_experts<FMT, 1>, dim3(static_cast<unsigned>(2 * wide + 1)), blk, 0, s, a);
+        launch(k_layer_up_experts<FMT>, dim3(static_cast<unsigned>(groups * (a.I / 16) + 1)), blk, 0, s, a);
         launch(k_layer_down_experts<FMT>,
                dim3(static_cast<unsigned>(layer_items(a.slots, a.EL) * (a.H / kLayerDownTile))), blk, 0, s, a);
         launch(k_layer_sum, dim3((a.T * (a.H / 4) + kLayerWaves * kWave - 1) / (kLayerWaves * kWave)), blk, 0, s, a);

@@ -214,13 +214,21 @@ hipError_t launch_dequantize_mx(const MxArgs &a, bool f32, hipStream_t s);
 // A whole layer for a few tokens (layer.hip).
 constexpr int kLayerMaxSlots = 1024;  // T * k at most
 constexpr int kLayerMaxWidth = 65536; // H and I at most
-constexpr int kLayerSingleSlots = 16; // up to this many, every slot on its own
-constexpr int kLayerUpCols = 2;       // columns of h per wave there
-constexpr int kLayerDownCols = 2;     // columns of out per wave there
+constexpr int kLayerUpCols = 2;       // every slot on its own: columns of h per wave
+constexpr int kLayerDownCols = 2;     // columns of out per wave
 constexpr int kLayerUpAhead = 1;      // runs of 64 chunks that a wave has in flight
 constexpr int kLayerDownAhead = 2;
 constexpr int kLayerDownTile = 64;    // columns of out per workgroup otherwise
+constexpr int kLayerUnit = 2;         // steps of a unit there
 enum { kLayerBf16 = 0, kLayerFp8 = 1, kLayerMxfp4 = 2 }; // the weights' format
+
+// Whether every slot is on its own: up to 16 of them, or one per expert on average.
+// Together / on its own, us: top-8 of 128, H = 2048, I = 768: T = 4 MXFP4 27.9 / 19.2,
+// E4M3 37.5 / 27.6; T = 8 41.6 / 31.7, 58.0 / 48.2, bf16 102 / 90; T = 16 59.6 / 54.2, 87.3 /
+// 86.2, 156 / 169; T = 24 70.7 / 77.0, 102 / 123, 185 / 245.  Top-2 of 16, H = 4096, I = 1024,
+// E4M3: T = 9 37.7 / 31.6, T = 12 39.9 / 38.9; top-2 of 8, I = 2048, MXFP4: T = 9 32.9 / 36.2, T =
+// 12 34.1 / 45.5.  5 tokens, top-6 of 64, half of them local, bf16: 34.5 / 22.6.
+inline bool layer_singles(int64_t slots, int64_t E) { return slots <= 16 || slots <= E; }
 
 // Which slots share an expert's weights: items {expert, first slot in the list, how
 // many (1 .. 16), 0}, and the slots expert by expert.

@@ -115,7 +115,8 @@ SHAPES = [
     (1, 17, 32, 0, 32, 256, 256), (1, 64, 100, 0, 100, 256, 128), (5, 6, 64, 16, 32, 2048, 768),
     (9, 4, 300, 100, 200, 512, 384), (33, 8, 128, 0, 128, 1024, 256), (64, 4, 4, 0, 4, 768, 128),
     (100, 3, 1024, 0, 1024, 256, 128), (128, 8, 16, 0, 16, 512, 256), (1024, 1, 8, 4, 4, 256, 128),
-    (31, 33, 64, 0, 64, 256, 128),
+    (31, 33, 64, 0, 64, 256, 128), (8, 4, 32, 0, 32, 1280, 384), (3, 11, 32, 0, 32, 768, 128), (2, 9, 16, 8, 8, 256, 640),
+    (40, 2, 16, 0, 16, 4096, 128), (17, 1, 4, 1, 3, 2304, 1152),
 ]
 
 

@@ -58,7 +58,9 @@ def test_pointers():
 
 def test_workspace():
     need = B.moe_layer_tokens_workspace_size(_desc(), 512, 256)
-    assert need >= 4 * 8 * (256 * 2 + 512 * 4)
+    assert need >= 4 * 8 * 256 * 2
+    # slots that share experts' weights: fp32 rows of them too
+    assert B.moe_layer_tokens_workspace_size(_desc(T=17), 512, 256) >= 17 * 8 * (256 * 2 + 512 * 4)
     assert layer(ws=None) == B.MOE_ERR_WORKSPACE and layer(ws=FAKE + 8) == B.MOE_ERR_WORKSPACE
     assert layer(n=need - 1) == B.MOE_ERR_WORKSPACE and str(need) in B.last_error()
     assert B.moe_layer_tokens_workspace_size(_desc(T=0), 256, 128) > 0
