@@ -545,11 +545,14 @@ def moe_dispatch_bwd(desc: Desc, handle: Handle, grad_rows: torch.Tensor, H: int
 # The calls below launch on the current device, so every tensor must be there
 # (each pointer is only valid on its own device).
 def _here(*tensors):
-    cur = torch.cuda.current_device() if torch.cuda.is_available() else None
+    cur = -1
     for t in tensors:
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != cur:
-            raise MoeError(MOE_ERR_ARG, f"a tensor is on {t.device}, the call runs on the current "
-                                        f"device cuda:{cur}")
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            if cur < 0:
+                cur = torch.cuda.current_device()
+            if t.get_device() != cur:
+                raise MoeError(MOE_ERR_ARG, f"a tensor is on {t.device}, the call runs on the "
+                                            f"current device cuda:{cur}")
 
 
 def _handle_here(handle: Handle, desc: Desc):
@@ -563,16 +566,23 @@ def _handle_here(handle: Handle, desc: Desc):
 
 # Their workgroups write outputs while others still read inputs.
 def _apart(outs, ins):
-    def span(t):
-        return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
-    outs = [t for t in outs if t is not None and t.numel()]
-    for i, t in enumerate(outs):
-        a, b = span(t)
-        for o in (*ins, *outs[:i]):
-            if o is not None and o.numel():
-                c, e = span(o)
-                if a < e and c < b:
-                    raise MoeError(MOE_ERR_ARG, "an output overlaps an input or another output")
+    spans = []
+    for group, out in ((outs, True), (ins, False)):
+        for t in group:
+            if t is not None:
+                n = t.nbytes
+                if n:
+                    p = t.data_ptr()
+                    spans.append((p, p + n, out))
+    spans.sort()
+    out_end = any_end = 0  # of the spans that start no later
+    for a, b, out in spans:
+        if a < (any_end if out else out_end):
+            raise MoeError(MOE_ERR_ARG, "an output overlaps an input or another output")
+        if b > any_end:
+            any_end = b
+        if out and b > out_end:
+            out_end = b
 
 
 def _int32(name: str, v) -> int:

@@ -87,15 +87,26 @@ inline ExpertKernel choose_expert_kernel(const ExpertLoad &l, int K, int N, bool
     return ExpertKernel::tile;
 }
 
-// The same for MXFP4 rows and weights.
+// The same for MXFP4 rows and weights (K: any).  Times in us, each call alone with its
+// weights in HBM.
 inline ExpertKernel choose_mx_kernel(const ExpertLoad &l, int N, bool gated)
 {
     const int cols = gated ? kTileCols / 2 : kTileCols;
     const int64_t tiles = l.groups * ((static_cast<int64_t>(N) + cols - 1) / cols);
-    if (l.group_max <= 32 && tiles * l.rows_mean <= 4 * kCus)
+    // One pass of 16 rows of a few experts (rows / ring): top-8 of 128, K = 768, N = 2048:
+    // T = 1 6.6 / 6.7, T = 2 9.5 / 9.0, T = 4 15.1 / 12.4; K = 2048, N = 4096, T = 1 15.1 / 16.4;
+    // gated, K = 2048, N = 768: T = 1 10.0 / 11.1, T = 2 16.3 / 15.0; one expert, 16 rows 8.3 /
+    // 8.5, 32 rows 14.0 / 9.0.
+    if (l.group_max <= 16 && 2 * tiles * l.rows_mean <= kCus)
         return ExpertKernel::rows;
+    // Tiles of 32 rows (ring / tile): E experts with r rows each, K = 2048, N = 4096: E = 64:
+    // r = 64 124 / 109, r = 128 184 / 117; E = 1, r = 512 12.3 / 24.1; E = 4: r = 256 27.7 / 27.4, r =
+    // 512 43.6 / 27.9.  N = 512, E = 16: r = 128 12.7 / 21.5, r = 512 27.3 / 27.1.  E = 128, K = 768,
+    // N = 2048: r = 16 42.5 / 44.6, r = 32 46.8 / 47.0, r = 64 56.5 / 52.7.  Gated, K = 2048, N =
+    // 768: E = 64: r = 32 50.5 / 50.6, r = 64 54.4 / 55.0, r = 96 65.2 / 57.4; E = 4, r = 512 19.6 / 28.8;
+    // E = 16: r = 128 24.7 / 27.1, r = 256 37.8 / 32.7.
     const int64_t ring_tiles = tiles * ((l.rows_mean + kRingRows - 1) / kRingRows);
-    if (l.rows_mean <= 64 || ring_tiles <= 2 * kCus)
+    if (l.rows_mean <= kRingRows || ring_tiles <= 2 * kCus)
         return ExpertKernel::ring;
     return ExpertKernel::tile;
 }
