@@ -28,6 +28,14 @@ __device__ __forceinline__ i32x8 widen(const u32x4 &v)
                  0, 0, 0, 0};
 }
 
+// silu(g) * u, with the reciprocal instruction (off by one step at most) for the
+// division: a tile of 256 x 128 values takes 1.9 us less (of 24), and h is rounded to 8 or
+// 2 bits next.
+__device__ __forceinline__ float mx_gated(float g, float u)
+{
+    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
+
 // c + a * b^T over 128 columns: a and b hold 16 rows each, lane l the row l % 16
 // and a block of 32 columns, sa and sb that block's scale in the lowest byte.
 __device__ __forceinline__ f32x4 mfma_mx128(const u32x4 &a, uint32_t sa, const u32x4 &b, uint32_t sb, const f32x4 &c)
@@ -147,7 +155,7 @@ __global__ void __launch_bounds__(kMxSplit * kWave) k_expert_mx_rows(MxExpertArg
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        acc[j][i] = gated(acc[j][i], acc[j + 2][i]);
+                        acc[j][i] = mx_gated(acc[j][i], acc[j + 2][i]);
             }
             uint32_t b = 0;
             if constexpr (MX) {
@@ -339,7 +347,7 @@ __global__ void __launch_bounds__(kMxRingWaves * kWave) k_expert_mx_ring(MxExper
         // h in place of the gate: the first 8 elements
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            acc[i] = gated(acc[i], acc[8 + i]);
+            acc[i] = mx_gated(acc[i], acc[8 + i]);
         const int n = t.ni * kOut + wave * 16 + upper * 8;
         if constexpr (MX) {
             // two waves share a block of 32 columns
@@ -616,7 +624,7 @@ __device__ __forceinline__ int mx_tile_run(const MxExpertArgs &a, const Tile &t,
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    acc[m][j][i] = gated(acc[m][j][i], acc[m][j + 2][i]);
+                    acc[m][j][i] = mx_gated(acc[m][j][i], acc[m][j + 2][i]);
             if constexpr (MX) {
                 const int row = 64 * m + xrow;
 #pragma unroll

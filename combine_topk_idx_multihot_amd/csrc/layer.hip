@@ -494,9 +494,8 @@ __device__ void make_plan(const LayerArgs &a, int32_t *lds) // of 2 kMaxLocal wo
 }
 
 // A workgroup has 16 columns of h for one expert, their gate and up rows, its waves
-// every fourth unit of them; 16 of the expert's slots at a time.  Expert workgroup i:
-// expert i, or (fewer slots than experts) the expert of slot i where no earlier slot has
-// it.  Grid: [experts or slots][I / 16], and one more for the plan.
+// every fourth unit of them; 16 of the expert's slots at a time.  Grid: [experts][I / 16]
+// (there are more slots than experts), and one more for the plan.
 template <int FMT>
 __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_up_experts(LayerArgs a)
 {
@@ -505,17 +504,13 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_up_experts(LayerA
     static_assert(sizeof part >= 2 * kMaxLocal * sizeof(int32_t), "the plan's counters lie there");
     constexpr int U = kLayerUnit;
     const int tiles = a.I >> 4;
-    const int i0 = blockIdx.x / tiles, n0 = (blockIdx.x - i0 * tiles) * 16;
-    const bool by_slot = a.slots < a.EL;
-    if (i0 == (by_slot ? a.slots : a.EL)) {
+    const int e = blockIdx.x / tiles, n0 = (blockIdx.x - e * tiles) * 16;
+    if (e == a.EL) {
         make_plan(a, reinterpret_cast<int32_t *>(part));
         if (a.flags)
             write_flags(a);
         return;
     }
-    const int e = __builtin_amdgcn_readfirstlane(by_slot ? slot_expert(a, i0) : i0);
-    if (e < 0)
-        return;
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int l16 = lane & 15, quarter = lane >> 4;
@@ -538,8 +533,6 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_up_experts(LayerA
         for (int i = 0; i < 4; ++i) {
             const int s = base + i * kWave + lane;
             const uint64_t m = __ballot(s < a.slots && id[i] == e);
-            if (by_slot && n == 0 && m && base + i * kWave + __builtin_ctzll(m) < i0)
-                return; // an earlier slot's workgroups have this expert
             if (wave == 0 && (m >> lane & 1))
                 list[n + __popcll(m & ((1ull << lane) - 1))] = s;
             n += __popcll(m);
@@ -678,8 +671,7 @@ static hipError_t launch_layer_of(const LayerArgs &a, hipStream_t s)
                s, a);
         launch(k_layer_down_slots<FMT>, dim3(a.T * (a.H / (kLayerWaves * kLayerDownCols))), blk, 0, s, a);
     } else {
-        const int64_t groups = a.slots < a.EL ? a.slots : a.EL;
-        launch(k_layer_up_experts<FMT>, dim3(static_cast<unsigned>(groups * (a.I / 16) + 1)), blk, 0, s, a);
+        launch(k_layer_up_experts<FMT>, dim3(a.EL * (a.I / 16) + 1), blk, 0, s, a);
         launch(k_layer_down_experts<FMT>,
                dim3(static_cast<unsigned>(layer_items(a.slots, a.EL) * (a.H / kLayerDownTile))), blk, 0, s, a);
         launch(k_layer_sum, dim3((a.T * (a.H / 4) + kLayerWaves * kWave - 1) / (kLayerWaves * kWave)), blk, 0, s, a);

@@ -8,7 +8,8 @@ product   y = sum over K columns.  A 4-bit matrix instruction (64 or 128 columns
           wherever in the sum the bits are lost).  K / 64 instructions and up to 3 additions of
           partial sums, each within that of S, the sum of all magnitudes:
           |y - exact| <= (K / 64 + 3) 2^-22 S.
-silu      as in expert_ref.swiglu, from the bounds of the two products.
+silu      as in expert_ref.swiglu, from the bounds of the two products, but with a reciprocal (within one
+          step, 2u) and a product (u) where that has a division (u): 2u |h| more.
 codes     of a value known within err: every code lies between those of the two ends of its interval, the
           block's power between those of the ends of the largest magnitude's.
 """
@@ -91,6 +92,12 @@ def product(rows_q, row_scale, w_q, w_scale, off):
         y.append(a @ w.T)
         bound.append((K / 64 + 3) * 2.0 ** -22 * (a.abs() @ w.abs().T) + ref.TINY)
     return torch.cat(y), torch.cat(bound)
+
+
+def swiglu(y, bound):
+    """fp64 h and the bound on an fp32 evaluation of it."""
+    h, err = ref.swiglu(y, bound)
+    return h, err + 2 * ref.U * h.abs()
 
 
 def check_codes(codes, scales, h, err, what):
