@@ -1056,7 +1056,7 @@ int moe_quantize_mxfp4(const void *x, int32_t x_is_f32, int64_t n, int32_t K, ui
     a.out = nullptr;
     a.codes = q;
     a.scales = scale;
-    a.chunks = n * (K / 8);
+    a.runs = n * (K / (x_is_f32 ? 4 : 8));
     hipError_t e = moe::launch_quantize_mx(a, x_is_f32, static_cast<hipStream_t>(stream));
     if (e != hipSuccess)
         return hip_fail(e, "quantize_mxfp4 launch");
@@ -1077,7 +1077,7 @@ int moe_dequantize_mxfp4(const uint8_t *q, const uint8_t *scale, int64_t n, int3
     a.out = out;
     a.codes = const_cast<uint8_t *>(q);
     a.scales = const_cast<uint8_t *>(scale);
-    a.chunks = n * (K / 8);
+    a.runs = n * (K / (out_is_f32 ? 4 : 8));
     hipError_t e = moe::launch_dequantize_mx(a, out_is_f32, static_cast<hipStream_t>(stream));
     if (e != hipSuccess)
         return hip_fail(e, "dequantize_mxfp4 launch");

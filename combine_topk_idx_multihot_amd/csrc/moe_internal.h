@@ -200,13 +200,13 @@ struct MxExpertArgs : ProductArgs {
 };
 hipError_t launch_expert_product_mx(const MxExpertArgs &a, hipStream_t s);
 
-// Quantization to MXFP4 and back (mx.hip): `chunks` runs of 8 values.
+// Quantization to MXFP4 and back (mx.hip): `runs` of 16 bytes of values.
 struct MxArgs {
     const void *values;     // bf16 or fp32 (quantization)
     void *out;              // bf16 or fp32 (the way back)
     uint8_t *codes;
     uint8_t *scales;
-    int64_t chunks;
+    int64_t runs;
 };
 hipError_t launch_quantize_mx(const MxArgs &a, bool f32, hipStream_t s);
 hipError_t launch_dequantize_mx(const MxArgs &a, bool f32, hipStream_t s);
