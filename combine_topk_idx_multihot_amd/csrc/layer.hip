@@ -136,6 +136,9 @@ __device__ void write_flags(const LayerArgs &a)
 // interleaved.  (With the matrix instructions, whose lanes have 16 rows of weights
 // and 4 chunks of columns, a chunk of MXFP4 needs four loads of the token beside
 // its own: one token, H = 4096, I = 1024 14.5 us for the first kernel.)
+// The two kernels, us (bytes): one token, top-8 of 128, E4M3, H = 2048, I = 768 6.4 (25 MB)
+// and 5.6 (13 MB), MXFP4, H = 4096, I = 1024 8.1 (36 MB) and 6.1 (18 MB): latency counts
+// as much as HBM.  5 tokens, top-6 of 64, half of them local, bf16 14.8 (70 MB) and 8.6 (35 MB).
 
 // The sum over the wave's lanes, in lane 63: in rows of 16 lanes, then across them.
 template <int CTRL>
@@ -341,6 +344,10 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_slots(LayerA
 // Weights are one operand of the 16x16x32 bf16 instructions, 16 rows each, 16 slots
 // the other; a lane has row l % 16 of both and a quarter of a step's columns, one
 // chunk.  The waves of a workgroup take every fourth step, their sums meet in LDS.
+// 32 tokens, top-8 of 128, H = 2048, I = 768, MXFP4: 51.8 us (185 MB, 3.6 TB/s), 28.7 (95 MB, 3.3
+// TB/s) and 4.8 for the sums; a load takes 64 bytes from each of 16 rows, and the address units are
+// busy 72 % of the first kernel's cycles.  Both formats of wider weights are nearer to HBM's
+// rate: all three kernels 110 us with E4M3 (4.8 TB/s), 204 with bf16 (5.2 TB/s).
 
 // W runs of 16 rows of weights: this lane's row of each and that row's scales, and its
 // chunks of a unit of U steps.  The scales of a unit are loaded together: MXFP4 rows

@@ -1378,6 +1378,7 @@ __device__ __forceinline__ u32x2 e4m3_pack8(const float (&y)[8])
 
 // MX: MXFP4 rows instead, blocks of 32 with a byte each: a lane's 8 elements make
 // one word of codes, a block is four lanes (mx.h).
+// 16384 tokens, top-8, H = 4096, padded to 16, MXFP4: 76 us for 422 MB (5.5 TB/s: HBM); one token 3.4 us.
 template <int SEG, bool MX>
 __device__ __forceinline__ void quant_token(const RowArgs &a, int64_t bid)
 {
