@@ -854,7 +854,8 @@ def moe_layer_tokens(desc: Desc, topk_idx: torch.Tensor, topk_w: torch.Tensor, x
 class PreparedLayerTokens:
     """moe_layer_tokens over buffers that a loop reuses on every step, checked once; it keeps its own
     workspace.  The tensors must stay as they are (no resize_ or set_) while the object is in use; it
-    holds references to them.  Calls of one object share its workspace: they must not overlap."""
+    holds references to them.  It may be let go while calls are on their way: the workspace is not handed out
+    before its stream is done with it.  Calls of one object share its workspace: they must not overlap."""
 
     def __init__(self, desc: Desc, topk_idx: torch.Tensor, topk_w: torch.Tensor, x: torch.Tensor,
                  w1: torch.Tensor, w2: torch.Tensor, out: torch.Tensor,
@@ -866,10 +867,18 @@ class PreparedLayerTokens:
                       *_layer_args(self._desc, topk_idx, topk_w, x, w1, w2, out, w1_scale, w2_scale, ws,
                                    flags, stream))
         self._fn = lib().moe_layer_tokens
+        _used_on(ws, stream)
         self._keep = (topk_idx, topk_w, x, w1, w2, out, w1_scale, w2_scale, ws, flags)
 
     def __call__(self) -> int:
         return _check(self._fn(*self._args))
+
+
+def _used_on(t, stream):
+    """Tell the allocator that calls on `stream` (None: the one it has it for) use t, a fresh tensor."""
+    if stream is not None and t.is_cuda:
+        s = _stream(stream)
+        t.record_stream(torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream())
 
 
 def _layer_workspace(desc, w2, w1_scale):
@@ -981,8 +990,8 @@ class PreparedExpertSwigluMxfp4(_Prepared):
     def __init__(self, desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scale: torch.Tensor,
                  K: int, w_q: torch.Tensor, w_scale: torch.Tensor, I: int, out: torch.Tensor,
                  out_scale: torch.Tensor | None = None, stream=None):
-        per_row = _positive("I", I) if out_scale is None else max(1, I // 2)
-        cap = min(2 * rows_q.numel() // _positive("K", K), out.numel() // per_row)
+        half = 1 if out_scale is None else 2  # codes a byte
+        cap = min(2 * rows_q.numel() // _positive("K", K), half * out.numel() // _positive("I", I))
         p = _product_ptrs(desc, handle, rows_q, row_scale, K, cap, w_q, w_scale, 2 * I, True)
         p_o, p_s = _swiglu_out(out, out_scale, cap, I, True)
         _apart((out, out_scale), (rows_q, row_scale, w_q, w_scale))
@@ -1284,9 +1293,7 @@ def layer_tokens(desc: Desc, topk_idx: torch.Tensor, topk_w: torch.Tensor, x: to
     ws = _layer_workspace(desc, w2, w1_scale)
     moe_layer_tokens(desc, topk_idx, topk_w, x, w1, w2, out, ws, w1_scale, w2_scale, flags,
                      stream=stream)
-    if stream is not None:  # the workspace is let go here, while that stream may still use it
-        s = _stream(stream)
-        ws.record_stream(torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream())
+    _used_on(ws, stream)  # (let go here, while that stream may still use it)
     return out
 
 

@@ -95,8 +95,9 @@ __device__ __forceinline__ int slot_expert(const LayerArgs &a, int s)
     const int32_t *p = static_cast<const int32_t *>(a.idx) + (static_cast<int64_t>(s) << a.idx_i64);
     const int id = p[0], high = p[a.idx_i64];
     const bool whole = !a.idx_i64 || high == 0; // (the ids that matter are not negative)
-    const int e = id - a.lb;
-    return whole && id >= a.lb && e < a.EL ? e : -1;
+    // (without a sign: an id below lb, however far, becomes one above every expert)
+    const uint32_t e = static_cast<uint32_t>(id) - static_cast<uint32_t>(a.lb);
+    return whole && e < static_cast<uint32_t>(a.EL) ? static_cast<int>(e) : -1;
 }
 
 __device__ __forceinline__ float layer_gated(float g, float u) { return g / (1.0f + __expf(-g)) * u; }

@@ -266,6 +266,66 @@ def test_in_a_graph(T, fmt):
         assert torch.equal(out[1], B.layer_tokens(d, idx, w, first, w1, w2, s1, s2))
 
 
+@pytest.mark.parametrize("T", [1, 2, 30])
+@pytest.mark.parametrize("i64", [False, True])
+def test_ids_far_out_of_range(i64, T):
+    """Ids whose distance from local_begin passes 31 bits, and 64-bit ones whose low half is an expert."""
+    d, idx, w, x, w1, s1, w2, s2 = make("mxfp4", T, 6, 16, 5, 9, 512, 256, seed=T, i64=i64)
+    far = [-(1 << 31), (1 << 31) - 1, 16, -2]
+    far += [(1 << 32) + 7, -(1 << 32) + 7, (1 << 40) + 5, -(1 << 63)] if i64 else [4 - (1 << 31), -(1 << 30)]
+    for n, v in enumerate(far):
+        idx[n % T, n % 6] = v
+    check("mxfp4", d, idx, w, x, w1, s1, w2, s2, f"{T} {i64}")
+
+
+def test_prepared_let_go_while_its_stream_is_busy():
+    """The workspace of an object that is gone is not handed out before its stream is done."""
+    d, idx, w, x, w1, s1, w2, s2 = make("mxfp4", 40, 4, 16, 0, 16, 512, 256)
+    want = B.layer_tokens(d, idx, w, x, w1, w2, s1, s2)
+    out = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    call = B.PreparedLayerTokens(d, idx, w, x, w1, w2, out, s1, s2, stream=st)
+    n = B.moe_layer_tokens_workspace_size(d, 512, 256)
+    where = next(t for t in call._keep if t is not None and t.dtype == torch.uint8 and t.numel() == n).data_ptr()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(100_000_000)
+    call()
+    del call
+    again = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert where not in [t.data_ptr() for t in again] or st.query()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("T", [2, 40])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_weights_past_32_bits(fmt, T):
+    """The first and the last expert of weights of more than 2^32 bytes each."""
+    H, I = 4096, 4096
+    EL = {"bf16": 130, "fp8": 258, "mxfp4": 514}[fmt]
+    g = torch.Generator(device="cuda").manual_seed(T)
+    few1, few2 = weights(fmt, 2, 2 * I, H, g), weights(fmt, 2, H, I, g)
+
+    def spread(t):
+        if t is None:
+            return None
+        big = torch.empty((EL, *t.shape[1:]), dtype=t.dtype, device="cuda")
+        big[0], big[-1] = t[0], t[1]
+        return big
+
+    w1, s1, w2, s2 = (spread(t) for t in (*few1, *few2))
+    assert w2.nbytes > 1 << 32 and w1.nbytes > 1 << 33
+    x = torch.randn((T, H), generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.rand((T, 14), generator=g, device="cuda")
+    ids = torch.full((T, 14), -1, dtype=torch.int32, device="cuda")
+    ids[:, 3], ids[::2, 9] = EL - 1, 0
+    d = B.make_desc(T, 14, EL)
+    out = B.layer_tokens(d, ids, w, x, w1, w2, s1, s2)
+    small = torch.where(ids == EL - 1, 1, ids).long()
+    ref.check_bf16(out, *exact(fmt, x, small, w, few1[0], few1[1], few2[0], few2[1], 0), fmt)
+
+
 def test_beside_the_fp8_layer():
     """One token: the E4M3 layer that quantizes rows and h lies as near as those roundings let it."""
     d, idx, w, x, w1, s1, w2, s2 = make("fp8", 1, 8, 64, 0, 64, 1024, 512, empty=0.0)

@@ -388,6 +388,64 @@ def test_eager_fewer_rows_than_routed():
     assert int(L.h.status[1]) & B.MOE_FLAG_ROWS_MISMATCH
 
 
+def test_past_32_bits():
+    """Values, codes, rows, weights and outputs of more than 2^32 bytes."""
+    n, K = (1 << 18) + 5, 1 << 15  # 8.6e9 values
+    last = slice(n - 9, n)
+    x = torch.empty((n, K), dtype=torch.bfloat16, device="cuda").normal_()
+    q, s = B.quantize_mxfp4(x)
+    assert q.nbytes > 1 << 32
+    for r in (slice(0, 3), last):
+        want_q, want_s = mx.make(x[r])
+        assert torch.equal(q[r], want_q) and torch.equal(s[r], want_s)
+    # dispatch: the token's codes, at its row
+    idx = torch.arange(n, dtype=torch.int32, device="cuda").view(n, 1) % 4
+    d = B.make_desc(n, 1, 4)
+    h, _ = B.route(d, idx)
+    rows_q, row_scale, _, rt, _ = B.dispatch_mxfp4(d, h, x)
+    for r in (slice(0, 3), last):
+        t = rt[r].long()
+        assert torch.equal(rows_q[r], q[t]) and torch.equal(row_scale[r], s[t])
+    y = B.dequantize_mxfp4(q, s)
+    assert torch.equal(y[last].double(), mx.values(q[last], s[last]))
+    del x, q, s, y
+    # rows past 2^32 bytes, then outputs
+    g = torch.Generator(device="cuda").manual_seed(1)
+    off = h.padded_offsets.tolist()
+    w, ws = mx.make_weights(4, 16, K, g)
+    out = B.expert_gemm_mxfp4(d, h, rows_q, row_scale, w, ws)
+    r = slice(off[-1] - 9, off[-1])
+    want = mx.product(rows_q[r], row_scale[r], w[3:], ws[3:], [0, 9])
+    ref.check_bf16(out[r], *want, "rows")
+    a, sa = rows_q[:, :64].contiguous(), row_scale[:, :4].contiguous()
+    del rows_q, row_scale, out
+    w, ws = mx.make_weights(4, 2 * 8320, 128, g)
+    out = B.expert_gemm_mxfp4(d, h, a, sa, w, ws)
+    assert out.nbytes > 1 << 33
+    ref.check_bf16(out[r], *mx.product(a[r], sa[r], w[3:], ws[3:], [0, 9]), "outputs")
+    out, _ = B.expert_swiglu_mxfp4(d, h, a, sa, w, ws, torch.bfloat16)
+    assert out.nbytes > 1 << 32
+    ref.check_bf16(out[r], *mx.swiglu(*mx.product(a[r], sa[r], w[3:], ws[3:], [0, 9])), "gated")
+
+
+@pytest.mark.parametrize("rows", [1, 30, 700])
+def test_weights_past_32_bits(rows):
+    """The last expert of weights of more than 2^32 bytes, in each of the kernels."""
+    E, N, K = 260, 8192, 4096
+    L = Layer(K, counts=[rows] + [0] * (E - 2) + [rows], seed=rows)
+    few, few_s = mx.make_weights(2, N, K, L.g)
+    w = torch.empty((E, N, K // 2), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros((E, N, K // 32), dtype=torch.uint8, device="cuda")
+    w[0], w[-1], ws[0], ws[-1] = few[0], few[1], few_s[0], few_s[1]
+    assert w.nbytes > 1 << 32
+    where = [0, rows, 2 * rows]
+    y, bound = mx.product(L.rows_q, L.row_scale, few, few_s, where)
+    out = B.expert_gemm_mxfp4(L.d, L.h, L.rows_q, L.row_scale, w, ws)
+    ref.check_bf16(out, y, bound, "plain")
+    out, _ = B.expert_swiglu_mxfp4(L.d, L.h, L.rows_q, L.row_scale, w, ws, torch.bfloat16)
+    ref.check_bf16(out, *mx.swiglu(y, bound), "gated")
+
+
 def test_no_tokens():
     d = B.make_desc(0, 2, 4)
     h, _ = B.route(d, torch.empty((0, 2), dtype=torch.int32, device="cuda"))

@@ -115,6 +115,14 @@ def test_binding_refusals(fmt):
             call(*good[:i], None, *good[i + 1:])
 
 
+def test_prepared_products_refuse_sizes_before_anything_else():
+    q = torch.zeros((8, 64), dtype=torch.uint8)
+    for K, I in ((128, 0), (128, -128), (0, 128), (-128, 128)):
+        for out, scale in ((torch.zeros((8, 128), dtype=torch.bfloat16), None), (q, q)):
+            with pytest.raises(B.MoeError, match="positive"):
+                B.PreparedExpertSwigluMxfp4(B.make_desc(4, 2, 8), None, q, q, K, q, q, I, out, scale)
+
+
 def test_op_fake_shape_and_registration():
     schema = str(torch.ops.moe_mi355x.layer_tokens.default._schema)
     assert schema.startswith("moe_mi355x::layer_tokens(") and "!" not in schema
