@@ -18,25 +18,14 @@
 // keeps its share of the token in registers and passes whole rows of weights by it.
 // With more, slots of the same expert share its weights in the matrix
 // instructions, up to 16 of them.
-#include "moe_internal.h"
+#include "expert_tiles.h"
 #include "mx.h"
 
 namespace moe {
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kLayerWaves = 4;
-
-__device__ __forceinline__ uint32_t two_bf16(float x, float y)
-{
-    const f32x2 v = {x, y};
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
-}
 
 // Columns that 16 bytes of weights hold: a chunk.
 template <int FMT>
@@ -100,14 +89,11 @@ __device__ __forceinline__ int slot_expert(const LayerArgs &a, int s)
     return whole && e < static_cast<uint32_t>(a.EL) ? static_cast<int>(e) : -1;
 }
 
-__device__ __forceinline__ float layer_gated(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
-
-// The flags of the ids, by one workgroup.
-__device__ void write_flags(const LayerArgs &a)
+// The flags of the ids, by one workgroup; `flags`: a word of its LDS.
+__device__ void write_flags(const LayerArgs &a, int *flags)
 {
-    __shared__ int flags;
     if (threadIdx.x == 0)
-        flags = 0;
+        *flags = 0;
     __syncthreads();
     const auto id = [&](int s) {
         return a.idx_i64 ? static_cast<const int64_t *>(a.idx)[s]
@@ -121,11 +107,11 @@ __device__ void write_flags(const LayerArgs &a)
                 if (id(o) == mine)
                     f |= 2;
         if (f)
-            atomicOr(&flags, f);
+            atomicOr(flags, f);
     }
     __syncthreads();
     if (threadIdx.x == 0)
-        *a.flags = flags;
+        *a.flags = *flags;
 }
 
 // ---------------------------------------------------------------------------
@@ -197,8 +183,9 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_up_slots(LayerArg
     constexpr int N = kLayerUpCols, U = kLayerUpAhead, C = kChunkCols<FMT>;
     const int tiles = a.I / (kLayerWaves * N);
     const int s = blockIdx.x / tiles;
+    __shared__ int flags;
     if (s == a.slots) {
-        write_flags(a);
+        write_flags(a, &flags);
         return;
     }
     const int e = __builtin_amdgcn_readfirstlane(slot_expert(a, s));
@@ -252,12 +239,12 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_up_slots(LayerArg
         acc[i] = wave_sum(acc[i]);
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        h[i] = layer_gated(acc[i], acc[N + i]);
+        h[i] = gated(acc[i], acc[N + i]);
     if (lane == kWave - 1) {
         uint32_t *o = reinterpret_cast<uint32_t *>(a.h + static_cast<int64_t>(s) * a.I + n0);
 #pragma unroll
         for (int i = 0; i < N; i += 2)
-            o[i / 2] = two_bf16(h[i], h[i + 1]);
+            o[i / 2] = pack_bf16(h[i], h[i + 1]);
     }
 }
 
@@ -335,26 +322,21 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_slots(LayerA
         uint32_t *o = reinterpret_cast<uint32_t *>(a.out + static_cast<int64_t>(t) * a.H + n0);
 #pragma unroll
         for (int i = 0; i < N; i += 2)
-            o[i / 2] = two_bf16(acc[i], acc[i + 1]);
+            o[i / 2] = pack_bf16(acc[i], acc[i + 1]);
     }
 }
 
 // ---------------------------------------------------------------------------
-// slots of an expert together
+// slots of an expert together, bf16 and E4M3
 // ---------------------------------------------------------------------------
 // Weights are one operand of the 16x16x32 bf16 instructions, 16 rows each, 16 slots
 // the other; a lane has row l % 16 of both and a quarter of a step's columns, one
 // chunk.  The waves of a workgroup take every fourth step, their sums meet in LDS.
-// 32 tokens, top-8 of 128, H = 2048, I = 768, MXFP4: 51.8 us (185 MB, 3.6 TB/s), 28.7 (95 MB, 3.3
-// TB/s) and 4.8 for the sums; a load takes 64 bytes from each of 16 rows, and the address units are
-// busy 72 % of the first kernel's cycles.  Both formats of wider weights are nearer to HBM's
-// rate: all three kernels 110 us with E4M3 (4.8 TB/s), 204 with bf16 (5.2 TB/s).
+// 32 tokens, top-8 of 128, H = 2048, I = 768: all three kernels 110 us with E4M3 (4.8 TB/s), 204 with
+// bf16 weights (5.2 TB/s).
 
 // W runs of 16 rows of weights: this lane's row of each and that row's scales, and its
-// chunks of a unit of U steps.  The scales of a unit are loaded together: MXFP4 rows
-// have 4 bytes for a step, all four quarters of a row the same ones, and a load
-// for each step touched as many cache lines as the weights did (32 tokens, H = 2048, I =
-// 768: the first kernel 66 instead of 51 us).
+// chunks of a unit of U steps.
 template <int FMT, int W, int U>
 struct Runs {
     const uint8_t *w[W], *scale[W];
@@ -362,7 +344,6 @@ struct Runs {
     uint32_t sc[U][W];
     __device__ __forceinline__ void load(int unit, int steps)
     {
-        typedef uint32_t words __attribute__((ext_vector_type(U), aligned(4)));
         const int quarter = (threadIdx.x & (kWave - 1)) >> 4;
         const int s0 = unit * U;
 #pragma unroll
@@ -370,23 +351,7 @@ struct Runs {
 #pragma unroll
             for (int j = 0; j < W; ++j)
                 v[u][j] = *reinterpret_cast<const u32x4 *>(w[j] + (min(s0 + u, steps - 1) * 4 + quarter) * 16);
-        if constexpr (FMT == kLayerMxfp4) {
-            if (s0 + U <= steps) {
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    const words q = *reinterpret_cast<const words *>(scale[j] + s0 * 4);
-#pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        sc[u][j] = q[u];
-                }
-            } else {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int j = 0; j < W; ++j)
-                        sc[u][j] = reinterpret_cast<const uint32_t *>(scale[j])[min(s0 + u, steps - 1)];
-            }
-        } else if constexpr (FMT == kLayerFp8) {
+        if constexpr (FMT == kLayerFp8) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -431,12 +396,10 @@ __device__ __forceinline__ void products(Runs<FMT, W, U> &r, const uint16_t *__r
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
                     f32x4 q = FMT == kLayerFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[j];
-                    const float f =
-                        FMT == kLayerMxfp4 ? mx_scale_operand((r.sc[u][j] >> (quarter * 8)) & 255u) : 1.0f;
 #pragma unroll
                     for (int i = 0; i < C / 8; ++i)
                         q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, eight<FMT>(r.v[u][j], i, f)),
+                            __builtin_bit_cast(bf16x8, eight<FMT>(r.v[u][j], i, 1.0f)),
                             __builtin_bit_cast(bf16x8, b[u][i]), q, 0, 0, 0);
                     if constexpr (FMT == kLayerFp8) {
 #pragma unroll
@@ -516,7 +479,7 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_up_experts(LayerA
     if (e == a.EL) {
         make_plan(a, reinterpret_cast<int32_t *>(part));
         if (a.flags)
-            write_flags(a);
+            write_flags(a, list);
         return;
     }
     const int lane = threadIdx.x & (kWave - 1);
@@ -569,9 +532,9 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_up_experts(LayerA
                 float h[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    h[i] = layer_gated(acc[0][i], acc[1][i]);
+                    h[i] = gated(acc[0][i], acc[1][i]);
                 *reinterpret_cast<u32x2 *>(a.h + static_cast<int64_t>(s) * a.I + n0 + quarter * 4) =
-                    u32x2{two_bf16(h[0], h[1]), two_bf16(h[2], h[3])};
+                    u32x2{pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3])};
             }
         }
         if (p + 16 < n)
@@ -582,8 +545,8 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_up_experts(LayerA
 // A workgroup has an item of the plan and kLayerDownTile columns: its slots' rows of
 // W2 h go to the workspace in fp32.  Grid: [items that there can be]
 // [H / kLayerDownTile].  (A column tile's sums by the last workgroup of it to arrive,
-// in place of a third kernel, took 288 us instead of 26 at 32 tokens, MXFP4, H =
-// 2048, I = 768, 128 experts: what one XCD wrote has to leave its L2 at every
+// in place of a third kernel, took 288 us instead of 26 at 32 tokens, H = 2048, I = 768, 128
+// experts, MXFP4 weights read in this form: what one XCD wrote has to leave its L2 at every
 // workgroup's end.)
 template <int FMT>
 __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_experts(LayerArgs a)
@@ -624,6 +587,238 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_experts(Laye
         *reinterpret_cast<f32x4 *>(a.y + static_cast<int64_t>(s) * a.H + n0 + wave * 16 + quarter * 4) = y;
 }
 
+// ---------------------------------------------------------------------------
+// slots of an expert together, MXFP4
+// ---------------------------------------------------------------------------
+// Rows of 4-bit weights are short: a load of 16 rows has 64 bytes of each, and the address
+// units are busy before HBM is.  So weights come through LDS, whole lines at a time, and so do
+// the tokens (or rows of h): workgroups walk a list of tiles of one expert, up to 16 of its slots
+// and 128 weight rows (64 gate and 64 up rows, or 128 rows of W2); their steps of 256 columns go
+// through a ring of three stages, two of them, across tiles, on their way at any time.  A
+// wave has 32 weight rows for all columns: two runs of 16, in the first kernel gate and up
+// rows of the same columns of h.
+//
+// A stage: 128 weight rows of 128 bytes (place_of), their scales, 8 bytes a row, and 16 rows of
+// bf16 (those beyond the tile's slots repeat the last one, and their results are dropped).
+struct LayerRing {
+    static constexpr int kStages = 3;
+    static constexpr uint32_t kSW = 128 * 128;      // in a stage: weight rows, their scales,
+    static constexpr uint32_t kX = kSW + 128 * 8;   // rows of bf16
+    static constexpr uint32_t kStage = kX + 16 * 512;
+    static constexpr uint32_t kExpert = kStages * kStage;           // the slots' experts, 16 bits each
+    static constexpr uint32_t kItem = kExpert + kLayerMaxSlots * 2; // items: expert * 64 + pass, 16 bits
+    static constexpr uint32_t kCount = kItem + kLayerMaxSlots * 2;  // how many
+    static constexpr uint32_t kList = kCount + 16;                  // [wave][16] slots of a tile, 16 bits
+    static constexpr uint32_t kBytes = kList + kLayerWaves * 16 * 2;
+    static_assert(2 * (kBytes + 512) <= 160 * 1024, "two workgroups per CU");
+    static_assert(kStages * kStage >= kMaxLocal * 4, "the counters lie in the stages");
+    static_assert(kLayerMaxSlots <= 16 * 64 && kMaxLocal <= 1024, "16 bits for an item");
+};
+constexpr int kLayerRingLoads = 7; // loads of a wave per step
+
+typedef __attribute__((address_space(3))) uint16_t *lds_half;
+typedef const __attribute__((address_space(3))) u32x2 *lds_pair;
+
+// The slots' experts, and per expert in use and 16 of its slots an item, experts in order.
+__device__ __forceinline__ void ring_tables(const LayerArgs &a)
+{
+    typedef LayerRing L;
+    const int lane = threadIdx.x & (kWave - 1);
+    for (int e = threadIdx.x; e < a.EL; e += blockDim.x)
+        *lds_at<lds_int>(e * 4) = 0;
+    __syncthreads();
+    for (int s = threadIdx.x; s < a.slots; s += blockDim.x) {
+        const int e = slot_expert(a, s);
+        *lds_at<lds_half>(L::kExpert + s * 2) = static_cast<uint16_t>(e); // (none: 65535)
+        if (e >= 0)
+            __hip_atomic_fetch_add(lds_at<lds_int>(e * 4), 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    }
+    __syncthreads();
+    if (threadIdx.x < kWave) {
+        int items = 0;
+        for (int base = 0; base < a.EL; base += kWave) {
+            const int e = base + lane;
+            const int m = e < a.EL ? (*lds_at<lds_int>(e * 4) + 15) >> 4 : 0;
+            int in = m;
+#pragma unroll
+            for (int o = 1; o < kWave; o <<= 1) {
+                const int u = __shfl_up(in, o);
+                if (lane >= o)
+                    in += u;
+            }
+            for (int i = 0; i < m; ++i)
+                *lds_at<lds_half>(L::kItem + (items + in - m + i) * 2) = static_cast<uint16_t>(e * 64 + i);
+            items += __shfl(in, kWave - 1);
+        }
+        if (lane == 0)
+            *lds_at<lds_int>(L::kCount) = items;
+    }
+    __syncthreads(); // (the counters are read: room for the stages)
+}
+
+// The slots of an item, in ascending order, to this wave's list; how many.
+__device__ __forceinline__ int ring_slots(const LayerArgs &a, int item)
+{
+    typedef LayerRing L;
+    const int lane = threadIdx.x & (kWave - 1);
+    const uint32_t list = L::kList + uniform(threadIdx.x / kWave) * 32;
+    const int e = item >> 6, first = (item & 63) * 16;
+    int n = 0;
+    for (int base = 0; base < a.slots && n < first + 16; base += kWave) {
+        const int s = base + lane;
+        const bool in = s < a.slots && *lds_at<lds_half>(L::kExpert + s * 2) == e;
+        const uint64_t m = __ballot(in);
+        const int rank = n + __popcll(m & ((1ull << lane) - 1)) - first;
+        if (in && rank >= 0 && rank < 16)
+            *lds_at<lds_half>(list + rank * 2) = static_cast<uint16_t>(s);
+        n += __popcll(m);
+    }
+    __builtin_amdgcn_wave_barrier(); // (a wave's LDS accesses are in order)
+    return min(16, n - first);
+}
+
+template <bool UP>
+__global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_ring(LayerArgs a)
+{
+    typedef LayerRing L;
+    extern __shared__ uint8_t ring_lds[]; // from 0, and the kernel's only LDS
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = uniform(threadIdx.x / kWave);
+    const int l16 = lane & 15, quarter = lane >> 4;
+    // (the compiler does not see the loads to LDS: the array's address escapes)
+    asm volatile("" : : "v"(ring_lds) : "memory");
+    if (UP && a.flags && blockIdx.x == gridDim.x - 1) {
+        write_flags(a, reinterpret_cast<int *>(ring_lds));
+        return;
+    }
+    ring_tables(a);
+    const int K = UP ? a.H : a.I, N = UP ? 2 * a.I : a.H; // columns and rows of an expert's weights
+    const int ntn = UP ? a.I / 64 : a.H / 128;
+    const int tiles = uniform(*lds_at<lds_int>(L::kCount)) * ntn;
+    const int stride = gridDim.x - (UP && a.flags ? 1 : 0);
+    const int steps = (K + 255) >> 8;
+    const bool half = K & 255; // the last step has 128 columns
+    const uint32_t row_bytes = K >> 1, row_blocks = K >> 5;
+    const uint8_t *const weights = static_cast<const uint8_t *>(UP ? a.w1 : a.w2);
+    const uint8_t *const scales = static_cast<const uint8_t *>(UP ? a.w1_scale : a.w2_scale);
+    const uint8_t *const rows = reinterpret_cast<const uint8_t *>(UP ? a.x : a.h);
+
+    // ---- loads: the tile and step to send for, and where it goes
+    int to = blockIdx.x - stride, to_b = steps, to_stage = 0;
+    uint32_t woff[4], wrow = 0;
+    const uint8_t *wbase = nullptr, *swbase = nullptr, *xrow[2] = {};
+    const auto send = [&]() {
+        if (to >= tiles)
+            return;
+        if (to_b == steps) {
+            to += stride;
+            if (to >= tiles)
+                return;
+            to_b = 0;
+            const int which = to / ntn, ni = to - which * ntn;
+            const int item = uniform(*lds_at<lds_half>(L::kItem + which * 2));
+            const int n = ring_slots(a, item);
+            const int64_t first = static_cast<int64_t>(item >> 6) * N +
+                                  (UP ? ni * 64 + (wave >= 2 ? a.I : 0) + (wave & 1) * 32 : ni * 128 + wave * 32);
+            wbase = weights + first * row_bytes;
+            swbase = scales + first * row_blocks;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                woff[i] = (i * 8 + (lane >> 3)) * row_bytes;
+            wrow = (lane >> 1) * row_blocks;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int s = *lds_at<lds_half>(L::kList + wave * 32 + min(wave * 4 + i * 2 + (lane >> 5), n - 1) * 2);
+                xrow[i] = rows + static_cast<int64_t>(UP ? s / a.k : s) * K * 2;
+            }
+        }
+        const bool cut = half && to_b + 1 == steps;
+        const uint32_t at = uniform(to_stage) * L::kStage;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            int c = place_of(wave * 32 + i * 8 + (lane >> 3), lane & 7);
+            c = cut ? c & 3 : c;
+            lds_load16(at + (wave * 4 + i) * 1024, wbase + to_b * 128 + (woff[i] + c * 16));
+        }
+        lds_load4(at + L::kSW + wave * 256, swbase + to_b * 8 + (wrow + (cut ? 0 : (lane & 1) * 4)));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            int c = (lane & 31) ^ ((wave * 4 + i * 2 + (lane >> 5)) & 7);
+            c = cut ? c & 15 : c;
+            lds_load16(at + L::kX + (wave * 2 + i) * 1024, xrow[i] + to_b * 512 + c * 16);
+        }
+        ++to_b;
+        to_stage = to_stage + 1 == L::kStages ? 0 : to_stage + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < L::kStages - 1; ++i)
+        send();
+
+    // ---- products
+    int stage = 0;
+    for (int t = blockIdx.x; t < tiles; t += stride) {
+        f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        for (int b = 0; b < steps; ++b) {
+            // this step's loads are there: the next step's are newer
+            if (to >= tiles)
+                step_barrier<0>();
+            else
+                step_barrier<(L::kStages - 2) * kLayerRingLoads>();
+            send(); // over the stage before, which every wave is done with
+            const uint32_t at = stage * L::kStage;
+            int mine[2];
+            u32x2 sc[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                mine[j] = UP ? j * 64 + wave * 16 + l16 : wave * 32 + j * 16 + l16;
+                sc[j] = *lds_at<lds_pair>(at + L::kSW + mine[j] * 8);
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) { // 128 columns
+                if (u == 1 && half && b + 1 == steps)
+                    break;
+                u32x4 x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[i] = *lds_at<lds_chunk>(at + L::kX + l16 * 512 + ((u * 16 + quarter * 4 + i) ^ (l16 & 7)) * 16);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const u32x4 w = *lds_at<lds_chunk>(at + mine[j] * 128 + place_of(mine[j], u * 4 + quarter) * 16);
+                    const uint32_t word = sc[j][u];
+                    const float f = mx_scale_operand((word >> (quarter * 8)) & 255u);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8, eight<kLayerMxfp4>(w, i, f)), __builtin_bit_cast(bf16x8, x[i]),
+                            acc[j], 0, 0, 0);
+                }
+            }
+            stage = stage + 1 == L::kStages ? 0 : stage + 1;
+        }
+        // acc[j][i]: weight row 4 quarter + i of run j, slot l16 of the tile
+        const int which = t / ntn, ni = t - which * ntn;
+        const int n = ring_slots(a, uniform(*lds_at<lds_half>(L::kItem + which * 2)));
+        if (l16 < n) {
+            const int64_t s = *lds_at<lds_half>(L::kList + wave * 32 + l16 * 2);
+            if constexpr (UP) {
+                float h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    h[i] = gated(acc[0][i], acc[1][i]);
+                *reinterpret_cast<u32x2 *>(a.h + s * a.I + ni * 64 + wave * 16 + quarter * 4) =
+                    u32x2{pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3])};
+            } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    *reinterpret_cast<f32x4 *>(a.y + s * a.H + ni * 128 + wave * 32 + j * 16 + quarter * 4) = acc[j];
+            }
+        }
+    }
+    // no load to LDS may be left when the workgroup ends
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+}
+
+// ---------------------------------------------------------------------------
 // out[t, n] from the slots' rows, in ascending slot order: the first term's product
 // rounded, each further term one fma.  A thread has four columns of a token.
 __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_sum(LayerArgs a)
@@ -664,7 +859,7 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_sum(LayerArgs a)
         }
     }
     *reinterpret_cast<u32x2 *>(a.out + static_cast<int64_t>(t) * a.H + n) =
-        u32x2{two_bf16(sum[0], sum[1]), two_bf16(sum[2], sum[3])};
+        u32x2{pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3])};
 }
 
 // ---------------------------------------------------------------------------
@@ -678,12 +873,20 @@ static hipError_t launch_layer_of(const LayerArgs &a, hipStream_t s)
         launch(k_layer_up_slots<FMT>, dim3(a.slots * (a.I / (kLayerWaves * kLayerUpCols)) + (a.flags ? 1 : 0)), blk, 0,
                s, a);
         launch(k_layer_down_slots<FMT>, dim3(a.T * (a.H / (kLayerWaves * kLayerDownCols))), blk, 0, s, a);
+        return hipGetLastError();
+    }
+    const int64_t items = layer_items(a.slots, a.EL);
+    if constexpr (FMT == kLayerMxfp4) {
+        const int64_t up = items * (a.I / 64), down = items * (a.H / 128), most = 2 * kCus;
+        launch(k_layer_ring<true>, dim3(static_cast<unsigned>(up < most ? up : most) + (a.flags ? 1 : 0)), blk,
+               LayerRing::kBytes, s, a);
+        launch(k_layer_ring<false>, dim3(static_cast<unsigned>(down < most ? down : most)), blk, LayerRing::kBytes, s, a);
     } else {
         launch(k_layer_up_experts<FMT>, dim3(a.EL * (a.I / 16) + 1), blk, 0, s, a);
         launch(k_layer_down_experts<FMT>,
-               dim3(static_cast<unsigned>(layer_items(a.slots, a.EL) * (a.H / kLayerDownTile))), blk, 0, s, a);
-        launch(k_layer_sum, dim3((a.T * (a.H / 4) + kLayerWaves * kWave - 1) / (kLayerWaves * kWave)), blk, 0, s, a);
+               dim3(static_cast<unsigned>(items * (a.H / kLayerDownTile))), blk, 0, s, a);
     }
+    launch(k_layer_sum, dim3((a.T * (a.H / 4) + kLayerWaves * kWave - 1) / (kLayerWaves * kWave)), blk, 0, s, a);
     return hipGetLastError();
 }
 

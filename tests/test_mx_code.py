@@ -100,3 +100,18 @@ def test_lds_by_address_has_no_static_neighbour(tmp_path):
     by_address = {name: int(size) for size, name in sizes if re.search("16k_expert_mx_(ring|tile)", name)}
     assert len(by_address) == 6 and not any(by_address.values()), by_address
     assert all(int(size) > 0 for size, name in sizes if "16k_expert_mx_rows" in name)
+
+
+def test_layer_ring_has_no_static_lds(tmp_path):
+    """The layer's ring kernels address their dynamic LDS from 0, too."""
+    if not os.path.exists(os.path.join(LLVM, "llvm-objdump")):
+        pytest.skip("no llvm-objdump")
+    B.lib()
+    lib = shutil.copy(B.LIB_PATH, tmp_path)
+    run = dict(cwd=tmp_path, check=True, text=True, capture_output=True)
+    subprocess.run([os.path.join(LLVM, "llvm-objdump"), "--offloading", os.path.basename(lib)], **run)
+    code = [f for f in sorted(tmp_path.iterdir()) if "gfx950" in f.name and b"12k_layer_ring" in f.read_bytes()]
+    notes = subprocess.run([os.path.join(LLVM, "llvm-readelf"), "--notes", str(code[0])], **run).stdout
+    sizes = [int(size) for size, name in re.findall(r"\.group_segment_fixed_size: (\d+).*?\.name: +(\S+)", notes, re.S)
+             if "12k_layer_ring" in name]
+    assert sizes == [0, 0]
