@@ -222,13 +222,20 @@ constexpr int kLayerDownTile = 64;    // columns of out per workgroup otherwise
 constexpr int kLayerUnit = 2;         // steps of a unit there
 enum { kLayerBf16 = 0, kLayerFp8 = 1, kLayerMxfp4 = 2 }; // the weights' format
 
-// Whether every slot is on its own: up to 16 of them, or one per expert on average.
-// Together / on its own, us: top-8 of 128, H = 2048, I = 768: T = 4 MXFP4 27.9 / 19.2,
-// E4M3 37.5 / 27.6; T = 8 41.6 / 31.7, 58.0 / 48.2, bf16 102 / 90; T = 16 59.6 / 54.2, 87.3 /
-// 86.2, 156 / 169; T = 24 70.7 / 77.0, 102 / 123, 185 / 245.  Top-2 of 16, H = 4096, I = 1024,
-// E4M3: T = 9 37.7 / 31.6, T = 12 39.9 / 38.9; top-2 of 8, I = 2048, MXFP4: T = 9 32.9 / 36.2, T =
-// 12 34.1 / 45.5.  5 tokens, top-6 of 64, half of them local, bf16: 34.5 / 22.6.
-inline bool layer_singles(int64_t slots, int64_t E) { return slots <= 16 || slots <= E; }
+// Whether every slot is on its own: up to 16 of them, or one per expert on average (MXFP4: 5
+// for 8 experts).
+// Together / on its own, us: top-8 of 128, H = 2048, I = 768, E4M3: T = 4 37.5 / 27.6, T = 8
+// 58.0 / 48.2, bf16 102 / 90; T = 16 87.3 / 86.2, 156 / 169; T = 24 102 / 123, 185 / 245.
+// Top-2 of 16, H = 4096, I = 1024, E4M3: T = 9 37.7 / 31.6, T = 12 39.9 / 38.9.  5 tokens, top-6 of 64,
+// half of them local, bf16: 34.5 / 22.6.
+// MXFP4: the first of these T = 4 27.3 / 18.9, T = 8 36.7 / 32.0, T = 10 39.9 / 38.3, T = 12 42.9 /
+// 43.0, T = 16 46.2 / 54.6; top-2 of 32, H = 4096, I = 1024: T = 10 29.0 / 29.5, T = 16 36.2 / 42.7;
+// top-8 of 64, H = 4096, I = 2048: T = 6 98 / 107; of 256, 64 of them local: T = 24 101 / 121; top-2
+// of 8, H = I = 2048: T = 8 21.7 / 20.8.
+inline bool layer_singles(int64_t slots, int64_t E, bool mx)
+{
+    return slots <= 16 || (mx ? 8 * slots <= 5 * E : slots <= E);
+}
 
 // Which slots share an expert's weights: items {expert, first slot in the list, how
 // many (1 .. 16), 0}, and the slots expert by expert.
