@@ -17,7 +17,9 @@
 // expert that two tokens share is read twice, the second time from the L2): a wave
 // keeps its share of the token in registers and passes whole rows of weights by it.
 // With more, slots of the same expert share its weights in the matrix
-// instructions, up to 16 of them.
+// instructions, up to 16 of them; a third kernel adds up a token's slots.  (These sums by the
+// last workgroup of a column tile to arrive took 288 us instead of 26 at 32 tokens, H = 2048, I =
+// 768, 128 experts: what one XCD wrote has to leave its L2 at every workgroup's end.)
 #include "expert_tiles.h"
 #include "mx.h"
 
@@ -327,304 +329,56 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_slots(LayerA
 }
 
 // ---------------------------------------------------------------------------
-// slots of an expert together, bf16 and E4M3
+// slots of an expert together
 // ---------------------------------------------------------------------------
-// Weights are one operand of the 16x16x32 bf16 instructions, 16 rows each, 16 slots
-// the other; a lane has row l % 16 of both and a quarter of a step's columns, one
-// chunk.  The waves of a workgroup take every fourth step, their sums meet in LDS.
-// 32 tokens, top-8 of 128, H = 2048, I = 768: all three kernels 110 us with E4M3 (4.8 TB/s), 204 with
-// bf16 weights (5.2 TB/s).
-
-// W runs of 16 rows of weights: this lane's row of each and that row's scales, and its
-// chunks of a unit of U steps.
-template <int FMT, int W, int U>
-struct Runs {
-    const uint8_t *w[W], *scale[W];
-    u32x4 v[U][W];
-    uint32_t sc[U][W];
-    __device__ __forceinline__ void load(int unit, int steps)
-    {
-        const int quarter = (threadIdx.x & (kWave - 1)) >> 4;
-        const int s0 = unit * U;
-#pragma unroll
-        for (int u = 0; u < U; ++u) // (steps beyond the last: unused)
-#pragma unroll
-            for (int j = 0; j < W; ++j)
-                v[u][j] = *reinterpret_cast<const u32x4 *>(w[j] + (min(s0 + u, steps - 1) * 4 + quarter) * 16);
-        if constexpr (FMT == kLayerFp8) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int j = 0; j < W; ++j) // two steps to a scale; (unit * U is even)
-                    sc[u][j] = u & 1 ? sc[u - 1][j]
-                                     : reinterpret_cast<const uint32_t *>(scale[j])[min(s0 + u, steps - 1) >> 1];
-        }
-    }
-};
-
-// acc[j] += run j * b^T over units first, first + kLayerWaves, ..., the first of which
-// has been loaded (where there is one); `x`: this lane's row of b, zeros where it has
-// none (not `mine`).
-// acc[j][i]: weight row 4 (l / 16) + i, row l % 16 of b.
-template <int FMT, int W, int U>
-__device__ __forceinline__ void products(Runs<FMT, W, U> &r, const uint16_t *__restrict__ x, bool mine, int first,
-                                         int steps, f32x4 (&acc)[W])
-{
-    static_assert(U % 2 == 0, "E4M3 scales are of two steps");
-    constexpr int C = kChunkCols<FMT>;
-    const int quarter = (threadIdx.x & (kWave - 1)) >> 4;
-    for (int unit = first; unit * U < steps; unit += kLayerWaves) {
-        if (unit != first)
-            r.load(unit, steps);
-        u32x4 b[U][C / 8];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < C / 8; ++i)
-                b[u][i] = u32x4{0u, 0u, 0u, 0u};
-        if (mine) { // (rows that are not there cost nothing)
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < C / 8; ++i)
-                    b[u][i] = *reinterpret_cast<const u32x4 *>(x + (min(unit * U + u, steps - 1) * 4 + quarter) * C + i * 8);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (unit * U + u < steps) {
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    f32x4 q = FMT == kLayerFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[j];
-#pragma unroll
-                    for (int i = 0; i < C / 8; ++i)
-                        q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, eight<FMT>(r.v[u][j], i, 1.0f)),
-                            __builtin_bit_cast(bf16x8, b[u][i]), q, 0, 0, 0);
-                    if constexpr (FMT == kLayerFp8) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc[j][i] = fmaf(q[i], __uint_as_float(r.sc[u][j]), acc[j][i]);
-                    } else {
-                        acc[j] = q;
-                    }
-                }
-            }
-        }
-    }
-}
-
-// What the second kernel reads, made by one workgroup of the first: per expert in
-// use and 16 of its slots an item {expert, first of its slots in the list, how
-// many}, and the slots expert by expert.
-__device__ void make_plan(const LayerArgs &a, int32_t *lds) // of 2 kMaxLocal words
-{
-    int32_t *count = lds, *begin = lds + kMaxLocal;
-    const int lane = threadIdx.x & (kWave - 1);
-    for (int e = threadIdx.x; e < a.EL; e += blockDim.x)
-        count[e] = 0;
-    __syncthreads();
-    for (int s = threadIdx.x; s < a.slots; s += blockDim.x) {
-        const int e = slot_expert(a, s);
-        if (e >= 0)
-            atomicAdd(&count[e], 1);
-    }
-    __syncthreads();
-    if (threadIdx.x < kWave) {
-        int slots = 0, items = 0;
-        for (int base = 0; base < a.EL; base += kWave) {
-            const int e = base + lane;
-            const int n = e < a.EL ? count[e] : 0, m = (n + 15) >> 4;
-            int in = n, im = m;
-#pragma unroll
-            for (int o = 1; o < kWave; o <<= 1) {
-                const int un = __shfl_up(in, o), um = __shfl_up(im, o);
-                if (lane >= o) {
-                    in += un;
-                    im += um;
-                }
-            }
-            if (e < a.EL)
-                begin[e] = slots + in - n;
-            for (int i = 0; i < m; ++i)
-                a.plan->items[items + im - m + i] =
-                    make_int4(e, slots + in - n + 16 * i, min(16, n - 16 * i), 0);
-            slots += __shfl(in, kWave - 1);
-            items += __shfl(im, kWave - 1);
-        }
-        if (lane == 0)
-            a.plan->count = items;
-    }
-    __syncthreads();
-    // every slot's place, in any order: its results do not depend on it
-    for (int s = threadIdx.x; s < a.slots; s += blockDim.x) {
-        const int e = slot_expert(a, s);
-        if (e >= 0)
-            a.plan->list[atomicAdd(&begin[e], 1)] = s;
-    }
-}
-
-// A workgroup has 16 columns of h for one expert, their gate and up rows, its waves
-// every fourth unit of them; 16 of the expert's slots at a time.  Grid: [experts][I / 16]
-// (there are more slots than experts), and one more for the plan.
-template <int FMT>
-__global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_up_experts(LayerArgs a)
-{
-    __shared__ f32x4 part[kLayerWaves][2][kWave];
-    __shared__ int32_t list[kLayerMaxSlots];
-    static_assert(sizeof part >= 2 * kMaxLocal * sizeof(int32_t), "the plan's counters lie there");
-    constexpr int U = kLayerUnit;
-    const int tiles = a.I >> 4;
-    const int e = blockIdx.x / tiles, n0 = (blockIdx.x - e * tiles) * 16;
-    if (e == a.EL) {
-        make_plan(a, reinterpret_cast<int32_t *>(part));
-        if (a.flags)
-            write_flags(a, list);
-        return;
-    }
-    const int lane = threadIdx.x & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int l16 = lane & 15, quarter = lane >> 4;
-    // gate rows and up rows.  E4M3 scales are those of the rows of this lane's results, the
-    // same for a run (its 16 rows lie in one block of 128).
-    Runs<FMT, 2, U> runs;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        runs.w[j] = weight_row<FMT>(a.w1, e, 2 * a.I, a.H, j * a.I + n0 + l16);
-        runs.scale[j] = scale_row<FMT>(a.w1_scale, e, 2 * a.I, a.H, j * a.I + n0 + l16);
-    }
-    const int steps = a.H / (4 * kChunkCols<FMT>);
-    int n = 0;
-    for (int base = 0; base < a.slots; base += 4 * kWave) {
-        int id[4]; // (all loads first)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            id[i] = slot_expert(a, min(base + i * kWave + lane, a.slots - 1));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int s = base + i * kWave + lane;
-            const uint64_t m = __ballot(s < a.slots && id[i] == e);
-            if (wave == 0 && (m >> lane & 1))
-                list[n + __popcll(m & ((1ull << lane) - 1))] = s;
-            n += __popcll(m);
-        }
-    }
-    if (n == 0)
-        return;
-    runs.load(min(wave, (steps - 1) / U), steps);
-    __syncthreads();
-    for (int p = 0; p < n; p += 16) {
-        const int s = list[min(p + l16, n - 1)];
-        f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        if (p)
-            runs.load(min(wave, (steps - 1) / U), steps);
-        products(runs, a.x + static_cast<int64_t>(s / a.k) * a.H, p + l16 < n, wave, steps, acc);
-        part[wave][0][lane] = acc[0];
-        part[wave][1][lane] = acc[1];
-        __syncthreads();
-        if (wave == 0) {
-#pragma unroll
-            for (int q = 1; q < kLayerWaves; ++q) {
-                acc[0] += part[q][0][lane];
-                acc[1] += part[q][1][lane];
-            }
-            if (p + l16 < n) {
-                float h[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    h[i] = gated(acc[0][i], acc[1][i]);
-                *reinterpret_cast<u32x2 *>(a.h + static_cast<int64_t>(s) * a.I + n0 + quarter * 4) =
-                    u32x2{pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3])};
-            }
-        }
-        if (p + 16 < n)
-            __syncthreads(); // the sums are read: room for the next slots'
-    }
-}
-
-// A workgroup has an item of the plan and kLayerDownTile columns: its slots' rows of
-// W2 h go to the workspace in fp32.  Grid: [items that there can be]
-// [H / kLayerDownTile].  (A column tile's sums by the last workgroup of it to arrive,
-// in place of a third kernel, took 288 us instead of 26 at 32 tokens, H = 2048, I = 768, 128
-// experts, MXFP4 weights read in this form: what one XCD wrote has to leave its L2 at every
-// workgroup's end.)
-template <int FMT>
-__global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_experts(LayerArgs a)
-{
-    constexpr int W = kLayerDownTile / 16, U = kLayerUnit;
-    static_assert(W == kLayerWaves, "a run of 16 columns per wave");
-    __shared__ f32x4 part[kLayerWaves][W][kWave];
-    const int tiles = a.H / kLayerDownTile;
-    const int item = blockIdx.x / tiles, n0 = (blockIdx.x - item * tiles) * kLayerDownTile;
-    if (item >= a.plan->count)
-        return;
-    const int lane = threadIdx.x & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int l16 = lane & 15, quarter = lane >> 4;
-    const int4 it = a.plan->items[item];
-    const int e = __builtin_amdgcn_readfirstlane(it.x);
-    const int steps = a.I / (4 * kChunkCols<FMT>);
-    Runs<FMT, W, U> runs;
-    f32x4 acc[W];
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-        runs.w[j] = weight_row<FMT>(a.w2, e, a.H, a.I, n0 + j * 16 + l16);
-        runs.scale[j] = scale_row<FMT>(a.w2_scale, e, a.H, a.I, n0 + j * 16 + l16);
-        acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-    runs.load(min(wave, (steps - 1) / U), steps);
-    const int s = a.plan->list[it.y + min(l16, it.z - 1)];
-    products(runs, a.h + static_cast<int64_t>(s) * a.I, l16 < it.z, wave, steps, acc);
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-        part[wave][j][lane] = acc[j];
-    __syncthreads();
-    f32x4 y = part[0][wave][lane];
-#pragma unroll
-    for (int q = 1; q < kLayerWaves; ++q)
-        y += part[q][wave][lane];
-    if (l16 < it.z)
-        *reinterpret_cast<f32x4 *>(a.y + static_cast<int64_t>(s) * a.H + n0 + wave * 16 + quarter * 4) = y;
-}
-
-// ---------------------------------------------------------------------------
-// slots of an expert together, MXFP4
-// ---------------------------------------------------------------------------
-// Rows of 4-bit weights are short: a load of 16 rows has 64 bytes of each, and the address
-// units are busy before HBM is.  So weights come through LDS, whole lines at a time, and so do
-// the tokens (or rows of h): workgroups walk a list of tiles of one expert, up to 16 of its slots
-// and 128 weight rows (64 gate and 64 up rows, or 128 rows of W2); their steps of 256 columns go
-// through a ring of three stages, two of them, across tiles, on their way at any time.  A
-// wave has 32 weight rows for all columns: two runs of 16, in the first kernel gate and up
-// rows of the same columns of h.
+// Weights are one operand of the 16x16x32 bf16 instructions, 16 rows each, 16 slots the
+// other; a lane has row l % 16 of both and a quarter of the columns of four chunks.
+// Weights come through LDS, whole lines at a time, and so do the tokens (or rows of h):
+// workgroups walk a list of tiles of one expert, up to 16 of its slots and 128 weight rows (64 gate and
+// 64 up rows, or 128 rows of W2); their steps of 128 bytes of each row go through a ring of
+// three stages (bf16: four), all but one of them, across tiles, on their way at any time.  A wave
+// has 32 weight rows for all columns: two runs of 16, in the first kernel gate and up rows
+// of the same columns of h.
+// (Weights from HBM to registers, a load taking 64 bytes of 16 rows, whose address units were busy
+// 72 % of the cycles with MXFP4: top-8 of 128, H = 2048, I = 768, 32 tokens MXFP4 86 us instead
+// of 63, E4M3 123 / 109, bf16 206 / 218; 128 tokens 142 / 99, 181 / 139, 274 / 256; top-2 of 8, H =
+// I = 2048, 256 tokens 85 / 53, 104 / 68, 169 / 87.)
 //
-// A stage: 128 weight rows of 128 bytes (place_of), their scales, 8 bytes a row, and 16 rows of
-// bf16.  A wave brings four of these, or none where the tile has no slots for them: what the
-// stage holds there enters only results that are dropped (all 16 always: 64.7 us instead of 62.9 at 32
-// tokens of the layer below).
+// A stage: 128 weight rows of 128 bytes (place_of), their scales (MXFP4 8 bytes a row; E4M3
+// each wave's two, of its runs' blocks), and 16 rows of bf16.  Where the tile has no slots for a wave's
+// rows it brings none: what the stage holds there enters only results that are dropped (all
+// 16 always: 64.7 us instead of 62.9 at 32 tokens, MXFP4).
+template <int FMT>
 struct LayerRing {
-    static constexpr int kStages = 3;
-    static constexpr uint32_t kSW = 128 * 128;      // in a stage: weight rows, their scales,
-    static constexpr uint32_t kX = kSW + 128 * 8;   // rows of bf16
-    static constexpr uint32_t kStage = kX + 16 * 512;
+    static constexpr int kStages = FMT == kLayerBf16 ? 4 : 3;
+    static constexpr int kCols = 8 * kChunkCols<FMT>; // columns of a step
+    static constexpr int kXBytes = 2 * kCols;         // a row of bf16 in it
+    static constexpr int kXRows = 1024 / kXBytes;     // such rows that a load of a wave brings
+    static constexpr int kXLoads = kXRows < 4 ? 4 / kXRows : 1; // loads of a wave for them
+    static constexpr uint32_t kSW = 128 * 128;    // in a stage: weight rows, their scales,
+    static constexpr uint32_t kX = kSW + (FMT == kLayerBf16 ? 0 : 128 * 8); // rows of bf16
+    static constexpr uint32_t kStage = kX + 16 * kXBytes;
+    static constexpr int kLoads = 4 + (FMT != kLayerBf16); // loads of a wave per step, but for rows of bf16
+    // where row r of bf16 keeps its chunk c, and which chunk is at place c (rows in whose way
+    // 16 others lie on the same banks)
+    __device__ static __forceinline__ int place(int r, int c) { return kXBytes < 256 ? place_of(r, c) : c ^ (r & 15); }
     static constexpr uint32_t kExpert = kStages * kStage;           // the slots' experts, 16 bits each
     static constexpr uint32_t kItem = kExpert + kLayerMaxSlots * 2; // items: expert * 64 + pass, 16 bits
     static constexpr uint32_t kCount = kItem + kLayerMaxSlots * 2;  // how many
     static constexpr uint32_t kList = kCount + 16;                  // [wave][16] slots of a tile, 16 bits
     static constexpr uint32_t kBytes = kList + kLayerWaves * 16 * 2;
     static_assert(2 * (kBytes + 512) <= 160 * 1024, "two workgroups per CU");
-    static_assert(kStages * kStage >= kMaxLocal * 4, "the counters lie in the stages");
+    static_assert(kStages * kStage <= 0xFFFF * 2 && kStages * kStage >= kMaxLocal * 4, "the counters lie in the stages");
     static_assert(kLayerMaxSlots <= 16 * 64 && kMaxLocal <= 1024, "16 bits for an item");
 };
-constexpr int kLayerRingLoads = 7; // loads of a wave per step
-
 typedef __attribute__((address_space(3))) uint16_t *lds_half;
 typedef const __attribute__((address_space(3))) u32x2 *lds_pair;
 
 // The slots' experts, and per expert in use and 16 of its slots an item, experts in order.
+template <int FMT>
 __device__ __forceinline__ void ring_tables(const LayerArgs &a)
 {
-    typedef LayerRing L;
+    typedef LayerRing<FMT> L;
     const int lane = threadIdx.x & (kWave - 1);
     for (int e = threadIdx.x; e < a.EL; e += blockDim.x)
         *lds_at<lds_int>(e * 4) = 0;
@@ -659,9 +413,10 @@ __device__ __forceinline__ void ring_tables(const LayerArgs &a)
 }
 
 // The slots of an item, in ascending order, to this wave's list; how many.
+template <int FMT>
 __device__ __forceinline__ int ring_slots(const LayerArgs &a, int item)
 {
-    typedef LayerRing L;
+    typedef LayerRing<FMT> L;
     const int lane = threadIdx.x & (kWave - 1);
     const uint32_t list = L::kList + uniform(threadIdx.x / kWave) * 32;
     const int e = item >> 6, first = (item & 63) * 16;
@@ -679,10 +434,11 @@ __device__ __forceinline__ int ring_slots(const LayerArgs &a, int item)
     return min(16, n - first);
 }
 
-template <bool UP>
+template <int FMT, bool UP>
 __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_ring(LayerArgs a)
 {
-    typedef LayerRing L;
+    typedef LayerRing<FMT> L;
+    constexpr int C = kChunkCols<FMT>;
     extern __shared__ uint8_t ring_lds[]; // from 0, and the kernel's only LDS
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = uniform(threadIdx.x / kWave);
@@ -693,14 +449,14 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_ring(LayerArgs a)
         write_flags(a, reinterpret_cast<int *>(ring_lds));
         return;
     }
-    ring_tables(a);
+    ring_tables<FMT>(a);
     const int K = UP ? a.H : a.I, N = UP ? 2 * a.I : a.H; // columns and rows of an expert's weights
     const int ntn = UP ? a.I / 64 : a.H / 128;
     const int tiles = uniform(*lds_at<lds_int>(L::kCount)) * ntn;
     const int stride = gridDim.x - (UP && a.flags ? 1 : 0);
-    const int steps = (K + 255) >> 8;
-    const bool half = K & 255; // the last step has 128 columns
-    const uint32_t row_bytes = K >> 1, row_blocks = K >> 5;
+    const int steps = (K + L::kCols - 1) / L::kCols;
+    const bool half = K & (L::kCols - 1); // the last step has half of the columns (MXFP4)
+    const uint32_t row_stride = static_cast<uint32_t>(row_bytes<FMT>(K)), row_blocks = K >> 5;
     const uint8_t *const weights = static_cast<const uint8_t *>(UP ? a.w1 : a.w2);
     const uint8_t *const scales = static_cast<const uint8_t *>(UP ? a.w1_scale : a.w2_scale);
     const uint8_t *const rows = reinterpret_cast<const uint8_t *>(UP ? a.x : a.h);
@@ -708,7 +464,7 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_ring(LayerArgs a)
     // ---- loads: the tile and step to send for, and where it goes
     int to = blockIdx.x - stride, to_b = steps, to_stage = 0;
     uint32_t woff[4], wrow = 0;
-    const uint8_t *wbase = nullptr, *swbase = nullptr, *xrow[2] = {};
+    const uint8_t *wbase = nullptr, *swbase = nullptr, *xrow[L::kXLoads] = {};
     bool with_x = true; // the newest loads have rows of bf16 among them
     const auto send = [&]() {
         if (to >= tiles)
@@ -720,19 +476,25 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_ring(LayerArgs a)
             to_b = 0;
             const int which = to / ntn, ni = to - which * ntn;
             const int item = uniform(*lds_at<lds_half>(L::kItem + which * 2));
-            const int n = ring_slots(a, item);
+            const int n = ring_slots<FMT>(a, item);
             const int64_t first = static_cast<int64_t>(item >> 6) * N +
                                   (UP ? ni * 64 + (wave >= 2 ? a.I : 0) + (wave & 1) * 32 : ni * 128 + wave * 32);
-            wbase = weights + first * row_bytes;
-            swbase = scales + first * row_blocks;
+            wbase = weights + first * row_stride;
+            if constexpr (FMT == kLayerMxfp4) {
+                swbase = scales + first * row_blocks;
+                wrow = (lane >> 1) * row_blocks;
+            } else if constexpr (FMT == kLayerFp8) { // (a run's rows lie in one block) lane j: run j % 2
+                const int row = UP ? (lane & 1) * a.I + ni * 64 : ni * 128;
+                swbase = scale_row<FMT>(scales, item >> 6, N, K, row);
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                woff[i] = (i * 8 + (lane >> 3)) * row_bytes;
-            wrow = (lane >> 1) * row_blocks;
-            with_x = wave * 4 < n;
+                woff[i] = (i * 8 + (lane >> 3)) * row_stride;
+            with_x = wave * L::kXLoads * L::kXRows < n;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int s = *lds_at<lds_half>(L::kList + wave * 32 + min(wave * 4 + i * 2 + (lane >> 5), n - 1) * 2);
+            for (int i = 0; i < L::kXLoads; ++i) {
+                const int r = (wave * L::kXLoads + i) * L::kXRows + lane * 16 / L::kXBytes;
+                const int s = *lds_at<lds_half>(L::kList + wave * 32 + min(r, n - 1) * 2);
                 xrow[i] = rows + static_cast<int64_t>(UP ? s / a.k : s) * K * 2;
             }
         }
@@ -744,14 +506,18 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_ring(LayerArgs a)
             c = cut ? c & 3 : c;
             lds_load16(at + (wave * 4 + i) * 1024, wbase + to_b * 128 + (woff[i] + c * 16));
         }
-        lds_load4(at + L::kSW + wave * 256, swbase + to_b * 8 + (wrow + (cut ? 0 : (lane & 1) * 4)));
+        if constexpr (FMT == kLayerMxfp4)
+            lds_load4(at + L::kSW + wave * 256, swbase + to_b * 8 + (wrow + (cut ? 0 : (lane & 1) * 4)));
+        else if constexpr (FMT == kLayerFp8)
+            lds_load4(at + L::kSW + wave * 256, swbase + to_b * 4);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < L::kXLoads; ++i) {
             if (!with_x)
                 break;
-            int c = (lane & 31) ^ ((wave * 4 + i * 2 + (lane >> 5)) & 7);
-            c = cut ? c & 15 : c;
-            lds_load16(at + L::kX + (wave * 2 + i) * 1024, xrow[i] + to_b * 512 + c * 16);
+            const int r = (wave * L::kXLoads + i) * L::kXRows + lane * 16 / L::kXBytes;
+            int c = L::place(r, lane & (L::kXBytes / 16 - 1));
+            c = cut ? c & (L::kXBytes / 32 - 1) : c;
+            lds_load16(at + L::kX + (wave * L::kXLoads + i) * 1024, xrow[i] + to_b * L::kXBytes + c * 16);
         }
         ++to_b;
         to_stage = to_stage + 1 == L::kStages ? 0 : to_stage + 1;
@@ -769,43 +535,58 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_ring(LayerArgs a)
             if (to >= tiles)
                 step_barrier<0>();
             else if (with_x)
-                step_barrier<(L::kStages - 2) * kLayerRingLoads>();
+                step_barrier<(L::kStages - 2) * L::kLoads + L::kXLoads>(); // (of steps but the newest: at least)
             else
-                step_barrier<(L::kStages - 2) * (kLayerRingLoads - 2)>();
+                step_barrier<(L::kStages - 2) * L::kLoads>();
             send(); // over the stage before, which every wave is done with
             const uint32_t at = stage * L::kStage;
             int mine[2];
             u32x2 sc[2];
+            f32x4 sum[2]; // E4M3: of this step, whose columns have one scale
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 mine[j] = UP ? j * 64 + wave * 16 + l16 : wave * 32 + j * 16 + l16;
-                sc[j] = *lds_at<lds_pair>(at + L::kSW + mine[j] * 8);
+                sc[j] = u32x2{0u, 0u};
+                if constexpr (FMT == kLayerMxfp4)
+                    sc[j] = *lds_at<lds_pair>(at + L::kSW + mine[j] * 8);
+                sum[j] = FMT == kLayerFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[j];
             }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) { // 128 columns
+            for (int u = 0; u < 2; ++u) { // four chunks of a row
                 if (u == 1 && half && b + 1 == steps)
                     break;
-                u32x4 x[4];
+                u32x4 x[C / 8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[i] = *lds_at<lds_chunk>(at + L::kX + l16 * 512 + ((u * 16 + quarter * 4 + i) ^ (l16 & 7)) * 16);
+                for (int i = 0; i < C / 8; ++i)
+                    x[i] = *lds_at<lds_chunk>(at + L::kX + l16 * L::kXBytes +
+                                              L::place(l16, (u * 4 + quarter) * (C / 8) + i) * 16);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const u32x4 w = *lds_at<lds_chunk>(at + mine[j] * 128 + place_of(mine[j], u * 4 + quarter) * 16);
                     const uint32_t word = sc[j][u];
                     const float f = mx_scale_operand((word >> (quarter * 8)) & 255u);
 #pragma unroll
+                    for (int i = 0; i < C / 8; ++i)
+                        sum[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, eight<FMT>(w, i, f)),
+                                                                         __builtin_bit_cast(bf16x8, x[i]), sum[j], 0, 0, 0);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if constexpr (FMT == kLayerFp8) {
+                    const float f = *lds_at<lds_float>(at + L::kSW + wave * 256 + j * 4);
+#pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, eight<kLayerMxfp4>(w, i, f)), __builtin_bit_cast(bf16x8, x[i]),
-                            acc[j], 0, 0, 0);
+                        acc[j][i] = fmaf(sum[j][i], f, acc[j][i]);
+                } else {
+                    acc[j] = sum[j];
                 }
             }
             stage = stage + 1 == L::kStages ? 0 : stage + 1;
         }
         // acc[j][i]: weight row 4 quarter + i of run j, slot l16 of the tile
         const int which = t / ntn, ni = t - which * ntn;
-        const int n = ring_slots(a, uniform(*lds_at<lds_half>(L::kItem + which * 2)));
+        const int n = ring_slots<FMT>(a, uniform(*lds_at<lds_half>(L::kItem + which * 2)));
         if (l16 < n) {
             const int64_t s = *lds_at<lds_half>(L::kList + wave * 32 + l16 * 2);
             if constexpr (UP) {
@@ -884,16 +665,11 @@ static hipError_t launch_layer_of(const LayerArgs &a, hipStream_t s)
         return hipGetLastError();
     }
     const int64_t items = layer_items(a.slots, a.EL);
-    if constexpr (FMT == kLayerMxfp4) {
-        const int64_t up = items * (a.I / 64), down = items * (a.H / 128), most = 2 * kCus;
-        launch(k_layer_ring<true>, dim3(static_cast<unsigned>(up < most ? up : most) + (a.flags ? 1 : 0)), blk,
-               LayerRing::kBytes, s, a);
-        launch(k_layer_ring<false>, dim3(static_cast<unsigned>(down < most ? down : most)), blk, LayerRing::kBytes, s, a);
-    } else {
-        launch(k_layer_up_experts<FMT>, dim3(a.EL * (a.I / 16) + 1), blk, 0, s, a);
-        launch(k_layer_down_experts<FMT>,
-               dim3(static_cast<unsigned>(items * (a.H / kLayerDownTile))), blk, 0, s, a);
-    }
+    const int64_t up = items * (a.I / 64), down = items * (a.H / 128), most = 2 * kCus;
+    launch(k_layer_ring<FMT, true>, dim3(static_cast<unsigned>(up < most ? up : most) + (a.flags ? 1 : 0)), blk,
+           LayerRing<FMT>::kBytes, s, a);
+    launch(k_layer_ring<FMT, false>, dim3(static_cast<unsigned>(down < most ? down : most)), blk,
+           LayerRing<FMT>::kBytes, s, a);
     launch(k_layer_sum, dim3((a.T * (a.H / 4) + kLayerWaves * kWave - 1) / (kLayerWaves * kWave)), blk, 0, s, a);
     return hipGetLastError();
 }

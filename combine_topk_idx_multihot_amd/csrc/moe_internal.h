@@ -218,33 +218,16 @@ constexpr int kLayerUpCols = 2;       // every slot on its own: columns of h per
 constexpr int kLayerDownCols = 2;     // columns of out per wave
 constexpr int kLayerUpAhead = 1;      // runs of 64 chunks that a wave has in flight
 constexpr int kLayerDownAhead = 2;
-constexpr int kLayerDownTile = 64;    // columns of out per workgroup otherwise
-constexpr int kLayerUnit = 2;         // steps of a unit there
 enum { kLayerBf16 = 0, kLayerFp8 = 1, kLayerMxfp4 = 2 }; // the weights' format
 
-// Whether every slot is on its own: up to 16 of them, or one per expert on average (MXFP4: 5
-// for 8 experts).
-// Together / on its own, us: top-8 of 128, H = 2048, I = 768, E4M3: T = 4 37.5 / 27.6, T = 8
-// 58.0 / 48.2, bf16 102 / 90; T = 16 87.3 / 86.2, 156 / 169; T = 24 102 / 123, 185 / 245.
-// Top-2 of 16, H = 4096, I = 1024, E4M3: T = 9 37.7 / 31.6, T = 12 39.9 / 38.9.  5 tokens, top-6 of 64,
-// half of them local, bf16: 34.5 / 22.6.
-// MXFP4: the first of these T = 4 27.3 / 18.9, T = 8 36.7 / 32.0, T = 10 39.9 / 38.3, T = 12 42.9 /
-// 43.0, T = 16 46.2 / 54.6; top-2 of 32, H = 4096, I = 1024: T = 10 29.0 / 29.5, T = 16 36.2 / 42.7;
-// top-8 of 64, H = 4096, I = 2048: T = 6 98 / 107; of 256, 64 of them local: T = 24 101 / 121; top-2
-// of 8, H = I = 2048: T = 8 21.7 / 20.8.
-inline bool layer_singles(int64_t slots, int64_t E, bool mx)
-{
-    return slots <= 16 || (mx ? 8 * slots <= 5 * E : slots <= E);
-}
-
-// Which slots share an expert's weights: items {expert, first slot in the list, how
-// many (1 .. 16), 0}, and the slots expert by expert.
-struct LayerPlan {
-    int4 items[kLayerMaxSlots];
-    int32_t list[kLayerMaxSlots];
-    int32_t count;
-    int32_t unused[3];
-};
+// Whether every slot is on its own: up to 16 of them, or 7 for 8 experts (MXFP4: 5).
+// Together / on its own, us: top-8 of 128, H = 2048, I = 768: E4M3 T = 4 36.5 / 27.9, T = 8 54.9 /
+// 47.4, T = 12 69.9 / 67.4, T = 16 80.9 / 86.6; bf16 T = 8 115 / 93, T = 12 142 / 130, T = 16 161 / 169;
+// MXFP4 T = 4 27.3 / 18.9, T = 8 36.7 / 32.0, T = 10 39.9 / 38.3, T = 12 42.9 / 43.0, T = 16 46.2 / 54.6.
+// Top-2 of 32, H = 4096, I = 1024: E4M3 T = 10 42.2 / 38.5, T = 14 53.1 / 50.6; bf16 86.9 / 80.8, 111 /
+// 107; MXFP4 29.0 / 29.5, T = 16 36.2 / 42.7.  Top-8 of 64, H = 4096, I = 2048, T = 6: E4M3 182 / 185,
+// bf16 346 / 373, MXFP4 98 / 107.  Top-2 of 8, H = I = 2048, T = 8: 29.1 / 23.5, 39.3 / 46.3, 21.7 / 20.8.
+inline bool layer_singles(int64_t slots, int64_t E, bool mx) { return slots <= 16 || 8 * slots <= (mx ? 5 : 7) * E; }
 
 // The most items that `slots` slots of EL experts make: one per expert in use, and
 // one more for every 16 slots beyond its first.
@@ -262,7 +245,6 @@ struct LayerArgs {
     const void *w2, *w2_scale; // [EL,H,I] and its scales
     uint16_t *h;            // workspace: [T*k,I] bf16
     float *y;               // workspace: [T*k,H] fp32, where slots share experts' weights
-    LayerPlan *plan;        // workspace
     uint16_t *out;          // [T,H] bf16
     int32_t *flags;         // one word or null
     int32_t T, k, slots;    // slots = T * k
