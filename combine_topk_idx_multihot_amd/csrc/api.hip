@@ -380,11 +380,11 @@ int check_layer(const moe_desc *desc, int32_t H, int32_t I)
     return MOE_OK;
 }
 
-// h, then (slots that share weights) their fp32 outputs; more than none for no tokens.
+// h (rounded, then what that left), then (slots that share weights) their fp32 outputs; more than none for no tokens.
 size_t layer_ws_bytes(const moe_desc *desc, int32_t H, int32_t I)
 {
     const size_t slots = static_cast<size_t>(desc->T) * desc->k;
-    return 16 + slots * I * 2 + (moe::layer_singles(slots, desc->E, true) ? 0 : slots * H * 4);
+    return 16 + slots * I * 4 + (moe::layer_singles(slots, desc->E, true) ? 0 : slots * H * 4);
 }
 
 // Argument rules shared by the quantization to MXFP4 and the way back, and its
@@ -1173,7 +1173,7 @@ int moe_layer_tokens(const moe_desc *desc, const void *topk_idx, const float *to
     a.w2 = w2;
     a.w2_scale = w2_scale;
     a.h = static_cast<uint16_t *>(workspace);
-    a.y = reinterpret_cast<float *>(a.h + static_cast<size_t>(desc->T) * desc->k * I);
+    a.y = reinterpret_cast<float *>(a.h + 2 * static_cast<size_t>(desc->T) * desc->k * I);
     a.out = out;
     a.flags = flags;
     a.T = static_cast<int32_t>(desc->T);

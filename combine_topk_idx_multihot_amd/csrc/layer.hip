@@ -10,8 +10,10 @@
 // E2M1 codes are exact there, an E8M0 scale too) and multiplied with bf16 tokens
 // in fp32; the fp32 scale of a block of E4M3 weights enters after the products of
 // its columns.  Tokens that are not quantized cost nothing here: the rates of the
-// units are several times what the weights' bytes need.  h is rounded to bf16 as
-// the experts of a bf16 layer would; everything else stays in fp32 until out.
+// units are several times what the weights' bytes need.  Where slots share weights h is
+// rounded to bf16, as the experts of a bf16 layer would; where every slot is on its own it is
+// two bf16 terms, its rounding and the rest, about 16 bits in all (the outputs' error against 64 bits is then the
+// final rounding's, 0.0017 instead of 0.0024 relative).  Everything else stays in fp32 until out.
 //
 // There are two forms.  With few slots every slot is on its own (an
 // expert that two tokens share is read twice, the second time from the L2): a wave
@@ -128,6 +130,7 @@ __device__ void write_flags(const LayerArgs &a, int *flags)
 // The two kernels, us (bytes): one token, top-8 of 128, E4M3, H = 2048, I = 768 6.4 (25 MB)
 // and 5.6 (13 MB), MXFP4, H = 4096, I = 1024 8.1 (36 MB) and 6.1 (18 MB): latency counts
 // as much as HBM.  5 tokens, top-6 of 64, half of them local, bf16 14.8 (70 MB) and 8.6 (35 MB).
+// (The second ones with h rounded to bf16; the second term costs 0.4, 1.7 and 3.8 us.)
 
 // The sum over the wave's lanes, in lane 63: in rows of 16 lanes, then across them.
 template <int CTRL>
@@ -244,9 +247,15 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_up_slots(LayerArg
         h[i] = gated(acc[i], acc[N + i]);
     if (lane == kWave - 1) {
         uint32_t *o = reinterpret_cast<uint32_t *>(a.h + static_cast<int64_t>(s) * a.I + n0);
+        uint32_t *rest = o + static_cast<int64_t>(a.slots) * a.I / 2;
 #pragma unroll
-        for (int i = 0; i < N; i += 2)
-            o[i / 2] = pack_bf16(h[i], h[i + 1]);
+        for (int i = 0; i < N; i += 2) {
+            const uint32_t top = pack_bf16(h[i], h[i + 1]);
+            o[i / 2] = top;
+            // what the rounding leaves (nothing of an infinity)
+            const float x = h[i] - __uint_as_float(top << 16), y = h[i + 1] - __uint_as_float(top & 0xFFFF0000u);
+            rest[i / 2] = pack_bf16(fabsf(x) < INFINITY ? x : 0.f, fabsf(y) < INFINITY ? y : 0.f);
+        }
     }
 }
 
@@ -285,7 +294,7 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_slots(LayerA
     for (int i = 0; i < N; ++i)
         acc[i] = 0.f;
     for (int base = 0; base < total; base += U * kWave) {
-        u32x4 v[U][N], hv[U][C / 8];
+        u32x4 v[U][N], hv[U][C / 8], rest[U][C / 8];
         uint32_t sc[U][N];
         float f[U];
 #pragma unroll
@@ -303,8 +312,10 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_slots(LayerA
                 sc[u][i] = chunk_scale<FMT>(sr + i * scale_stride, c);
             }
 #pragma unroll
-            for (int i = 0; i < C / 8; ++i)
+            for (int i = 0; i < C / 8; ++i) {
                 hv[u][i] = *reinterpret_cast<const u32x4 *>(h + i * 8);
+                rest[u][i] = *reinterpret_cast<const u32x4 *>(h + static_cast<int64_t>(a.slots) * a.I + i * 8);
+            }
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -312,7 +323,7 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_slots(LayerA
             const bool in = base + u * kWave + lane < total;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float q = chunk_dot<FMT>(v[u][i], sc[u][i], hv[u], 0.f);
+                const float q = chunk_dot<FMT>(v[u][i], sc[u][i], hv[u], chunk_dot<FMT>(v[u][i], sc[u][i], rest[u], 0.f));
                 acc[i] = in ? fmaf(q, f[u], acc[i]) : acc[i];
             }
         }
