@@ -384,7 +384,7 @@ int check_layer(const moe_desc *desc, int32_t H, int32_t I)
 size_t layer_ws_bytes(const moe_desc *desc, int32_t H, int32_t I)
 {
     const size_t slots = static_cast<size_t>(desc->T) * desc->k;
-    return 16 + slots * I * 4 + (moe::layer_singles(slots, desc->E, true) ? 0 : slots * H * 4);
+    return 16 + slots * I * 4 + (moe::layer_singles(slots, desc->E, moe::kLayerMxfp4) ? 0 : slots * H * 4);
 }
 
 // Argument rules shared by the quantization to MXFP4 and the way back, and its

@@ -672,7 +672,7 @@ template <int FMT>
 static hipError_t launch_layer_of(const LayerArgs &a, hipStream_t s)
 {
     const dim3 blk(kLayerWaves * kWave);
-    if (layer_singles(a.slots, a.E, FMT == kLayerMxfp4)) {
+    if (layer_singles(a.slots, a.E, FMT)) {
         launch(k_layer_up_slots<FMT>, dim3(a.slots * (a.I / (kLayerWaves * kLayerUpCols)) + (a.flags ? 1 : 0)), blk, 0,
                s, a);
         launch(k_layer_down_slots<FMT>, dim3(a.T * (a.H / (kLayerWaves * kLayerDownCols))), blk, 0, s, a);

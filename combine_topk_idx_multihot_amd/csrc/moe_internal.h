@@ -220,14 +220,16 @@ constexpr int kLayerUpAhead = 1;      // runs of 64 chunks that a wave has in fl
 constexpr int kLayerDownAhead = 2;
 enum { kLayerBf16 = 0, kLayerFp8 = 1, kLayerMxfp4 = 2 }; // the weights' format
 
-// Whether every slot is on its own: up to 16 of them, or 7 for 8 experts (MXFP4: 5).
-// Together / on its own, us: top-8 of 128, H = 2048, I = 768: E4M3 T = 4 36.5 / 27.9, T = 8 54.9 /
-// 47.4, T = 12 69.9 / 67.4, T = 16 80.9 / 86.6; bf16 T = 8 115 / 93, T = 12 142 / 130, T = 16 161 / 169;
-// MXFP4 T = 4 27.3 / 18.9, T = 8 36.7 / 32.0, T = 10 39.9 / 38.3, T = 12 42.9 / 43.0, T = 16 46.2 / 54.6.
-// Top-2 of 32, H = 4096, I = 1024: E4M3 T = 10 42.2 / 38.5, T = 14 53.1 / 50.6; bf16 86.9 / 80.8, 111 /
-// 107; MXFP4 29.0 / 29.5, T = 16 36.2 / 42.7.  Top-8 of 64, H = 4096, I = 2048, T = 6: E4M3 182 / 185,
-// bf16 346 / 373, MXFP4 98 / 107.  Top-2 of 8, H = I = 2048, T = 8: 29.1 / 23.5, 39.3 / 46.3, 21.7 / 20.8.
-inline bool layer_singles(int64_t slots, int64_t E, bool mx) { return slots <= 16 || 8 * slots <= (mx ? 5 : 7) * E; }
+// Whether every slot is on its own: up to 16 of them, or 7 (E4M3 5, MXFP4 3) for 8 experts.
+// Together / on its own, us: top-8 of 128, H = 2048, I = 768: bf16 T = 8 115 / 93, T = 12 142 / 134,
+// T = 16 161 / 169; E4M3 T = 8 54.9 / 52.3, T = 10 60.8 / 62.6, T = 12 69.9 / 73.7; MXFP4 T = 4 27.3 /
+// 22.4, T = 8 36.7 / 37.9, T = 10 39.9 / 45.1.  Top-2 of 32, H = 4096, I = 1024: bf16 T = 10 86.9 / 82.0, T =
+// 14 111 / 108; E4M3 42.2 / 40.9, 53.1 / 54.1; MXFP4 T = 10 29.0 / 37.0.  Top-2 of 8, H = I = 2048,
+// T = 8: 39.3 / 47.9, 29.1 / 25.9, 21.7 / 23.7.
+inline bool layer_singles(int64_t slots, int64_t E, int fmt)
+{
+    return slots <= 16 || 8 * slots <= (fmt == kLayerBf16 ? 7 : fmt == kLayerFp8 ? 5 : 3) * E;
+}
 
 // The most items that `slots` slots of EL experts make: one per expert in use, and
 // one more for every 16 slots beyond its first.
