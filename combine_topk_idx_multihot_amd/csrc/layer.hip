@@ -2,7 +2,7 @@
 //
 //   h[s]   = silu(W1g[e] x[t]) * (W1u[e] x[t])          for every slot s = (t, j), e its expert
 //   out[t] = sum over t's local slots of w[s] * W2[e] h[s]
-// No rows are laid out: the first kernel writes h (bf16, one row per slot) to the
+// No rows are laid out: the first kernel writes h (a row of bf16 per slot, or two) to the
 // workspace, the second one multiplies it and sums a token's slots (where slots
 // share weights a third one does).
 // The weights of the experts in use are what has to be read; tokens and h are
