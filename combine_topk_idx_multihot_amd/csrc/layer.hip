@@ -2,7 +2,7 @@
 //
 //   h[s]   = silu(W1g[e] x[t]) * (W1u[e] x[t])          for every slot s = (t, j), e its expert
 //   out[t] = sum over t's local slots of w[s] * W2[e] h[s]
-// No rows are laid out: the first kernel writes h (a row of bf16 per slot, or two) to the
+// No rows are laid out: the first kernel writes h (two rows of bf16 per slot) to the
 // workspace, the second one multiplies it and sums a token's slots (where slots
 // share weights a third one does).
 // The weights of the experts in use are what has to be read; tokens and h are
@@ -10,10 +10,9 @@
 // E2M1 codes are exact there, an E8M0 scale too) and multiplied with bf16 tokens
 // in fp32; the fp32 scale of a block of E4M3 weights enters after the products of
 // its columns.  Tokens that are not quantized cost nothing here: the rates of the
-// units are several times what the weights' bytes need.  Where slots share weights h is
-// rounded to bf16, as the experts of a bf16 layer would; where every slot is on its own it is
-// two bf16 terms, its rounding and the rest, about 16 bits in all (the outputs' error against 64 bits is then the
-// final rounding's, 0.0017 instead of 0.0024 relative).  Everything else stays in fp32 until out.
+// units are several times what the weights' bytes need.  h is two bf16 terms, its rounding and
+// the rest, about 16 bits in all (the outputs' error against 64 bits is then the final rounding's, 0.0017 instead of
+// 0.0024 relative).  Everything else stays in fp32 until out.
 //
 // There are two forms.  With few slots every slot is on its own (an
 // expert that two tokens share is read twice, the second time from the L2): a wave
@@ -79,6 +78,14 @@ __device__ __forceinline__ const uint8_t *scale_row(const void *scale, int e, in
     else if constexpr (FMT == kLayerFp8)
         p += (static_cast<int64_t>(e) * ((n + 127) >> 7) + (row >> 7)) * (K >> 7) * 4;
     return p;
+}
+
+// What the rounding of x and y to `top` leaves (nothing of an infinity), in bf16 itself.
+__device__ __forceinline__ uint32_t rest_bf16(float x, float y, uint32_t top)
+{
+    x -= __uint_as_float(top << 16);
+    y -= __uint_as_float(top & 0xFFFF0000u);
+    return pack_bf16(fabsf(x) < INFINITY ? x : 0.f, fabsf(y) < INFINITY ? y : 0.f);
 }
 
 // The local expert of slot s, -1 if it has none here.
@@ -252,9 +259,7 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_up_slots(LayerArg
         for (int i = 0; i < N; i += 2) {
             const uint32_t top = pack_bf16(h[i], h[i + 1]);
             o[i / 2] = top;
-            // what the rounding leaves (nothing of an infinity)
-            const float x = h[i] - __uint_as_float(top << 16), y = h[i + 1] - __uint_as_float(top & 0xFFFF0000u);
-            rest[i / 2] = pack_bf16(fabsf(x) < INFINITY ? x : 0.f, fabsf(y) < INFINITY ? y : 0.f);
+            rest[i / 2] = rest_bf16(h[i], h[i + 1], top);
         }
     }
 }
@@ -346,8 +351,8 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_slots(LayerA
 // other; a lane has row l % 16 of both and a quarter of the columns of four chunks.
 // Weights come through LDS, whole lines at a time, and so do the tokens (or rows of h):
 // workgroups walk a list of tiles of one expert, up to 16 of its slots and 128 weight rows (64 gate and
-// 64 up rows, or 128 rows of W2); their steps of 128 bytes of each row go through a ring of
-// three stages (bf16: four), all but one of them, across tiles, on their way at any time.  A wave
+// 64 up rows, or 128 rows of W2); their steps of 128 bytes of each row (64 where MXFP4 goes with two
+// terms of h) go through a ring of three or four stages, all but one of them, across tiles, on their way at any time.  A wave
 // has 32 weight rows for all columns: two runs of 16, in the first kernel gate and up rows
 // of the same columns of h.
 // (Weights from HBM to registers, a load taking 64 bytes of 16 rows, whose address units were busy
@@ -358,41 +363,53 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_slots(LayerA
 // Bound by HBM: 32 tokens with MXFP4 weights 41.5 and 23.6 us (186 and 95 MB: 4.5 and 4.0 TB/s), and
 // 4.8 us for the sums.
 //
-// A stage: 128 weight rows of 128 bytes (place_of), their scales (MXFP4 8 bytes a row; E4M3
-// each wave's two, of its runs' blocks), and 16 rows of bf16.  Where the tile has no slots for a wave's
-// rows it brings none: what the stage holds there enters only results that are dropped (all
-// 16 always: 64.7 us instead of 62.9 at 32 tokens, MXFP4).
-template <int FMT>
+// A stage: 128 weight rows, their scales (MXFP4 a byte per 32 columns; E4M3 each wave's two, of
+// its runs' blocks), and 16 rows of bf16: tokens, or rows of h, once for each term.  Where the tile has no slots for
+// a wave's rows it brings none: what the stage holds there enters only results that are dropped (all 16
+// always: 64.7 us instead of 62.9 at 32 tokens, MXFP4).
+//
+// The second kernel multiplies both terms of h with the weights that it has widened.  Top-8 of 128, H = 2048, I = 768, whole
+// layer, one term / two: MXFP4 T = 8 39.7 / 41.6, T = 32 68.6 / 72.9, T = 128 99.7 / 104.6; E4M3 T = 32 106.8 / 107.0,
+// T = 128 134 / 137; bf16 T = 32 215 / 212.  With MXFP4 weights and steps of 128 bytes, whose 1 KB per slot leaves room
+// for two stages, T = 16 to 256 take 1 us less with a last half step to treat apart; eight waves that share three such
+// stages, one workgroup per CU, 1 to 3 us more (fewer and larger tiles in the last round).
+template <int FMT, bool UP>
 struct LayerRing {
-    static constexpr int kStages = FMT == kLayerBf16 ? 4 : 3;
-    static constexpr int kCols = 8 * kChunkCols<FMT>; // columns of a step
-    static constexpr int kXBytes = 2 * kCols;         // a row of bf16 in it
+    static constexpr int kPlanes = UP ? 1 : 2; // of rows of bf16: tokens, or h's two terms
+    static constexpr int kStages = UP ? (FMT == kLayerBf16 ? 4 : 3) : (FMT == kLayerMxfp4 ? 4 : 3);
+    static constexpr int kChunks = !UP && FMT == kLayerMxfp4 ? 4 : 8; // of 16 bytes, of a weight row in a step
+    static constexpr int kCols = kChunks * kChunkCols<FMT>; // columns of a step
+    static constexpr int kWRows = 64 / kChunks;       // weight rows that a load of a wave brings
+    static constexpr int kWLoads = 32 / kWRows;       // loads of a wave for its 32
+    static constexpr int kXBytes = 2 * kCols;         // a row of bf16 in a step
     static constexpr int kXRows = 1024 / kXBytes;     // such rows that a load of a wave brings
-    static constexpr int kXLoads = kXRows < 4 ? 4 / kXRows : 1; // loads of a wave for them
-    static constexpr uint32_t kSW = 128 * 128;    // in a stage: weight rows, their scales,
-    static constexpr uint32_t kX = kSW + (FMT == kLayerBf16 ? 0 : 128 * 8); // rows of bf16
-    static constexpr uint32_t kStage = kX + 16 * kXBytes;
-    static constexpr int kLoads = 4 + (FMT != kLayerBf16); // loads of a wave per step, but for rows of bf16
+    static constexpr int kXLoads = kXRows < 4 ? 4 / kXRows : 1; // loads of a wave for a plane of them
+    static constexpr uint32_t kSW = 128 * 16 * kChunks; // in a stage: weight rows, their scales,
+    static constexpr uint32_t kX = kSW + (FMT == kLayerBf16 ? 0 : kLayerWaves * 256); // planes of 16 rows of bf16
+    static constexpr uint32_t kPlane = 16 * kXBytes;
+    static constexpr uint32_t kStage = kX + kPlanes * kPlane;
+    static constexpr int kLoads = kWLoads + (FMT != kLayerBf16); // loads of a wave per step, but for rows of bf16
     // where row r of bf16 keeps its chunk c, and which chunk is at place c (rows in whose way
-    // 16 others lie on the same banks)
+    // 16 others lie on the same banks); the same of weight rows
     __device__ static __forceinline__ int place(int r, int c) { return kXBytes < 256 ? place_of(r, c) : c ^ (r & 15); }
+    __device__ static __forceinline__ int wplace(int r, int c) { return kChunks == 8 ? place_of(r, c) : c ^ ((r >> 2) & 3); }
     static constexpr uint32_t kExpert = kStages * kStage;           // the slots' experts, 16 bits each
     static constexpr uint32_t kItem = kExpert + kLayerMaxSlots * 2; // items: expert * 64 + pass, 16 bits
     static constexpr uint32_t kCount = kItem + kLayerMaxSlots * 2;  // how many
     static constexpr uint32_t kList = kCount + 16;                  // [wave][16] slots of a tile, 16 bits
     static constexpr uint32_t kBytes = kList + kLayerWaves * 16 * 2;
     static_assert(2 * (kBytes + 512) <= 160 * 1024, "two workgroups per CU");
-    static_assert(kStages * kStage <= 0xFFFF * 2 && kStages * kStage >= kMaxLocal * 4, "the counters lie in the stages");
+    static_assert(kStages * kStage >= kMaxLocal * 4, "the counters lie in the stages");
     static_assert(kLayerMaxSlots <= 16 * 64 && kMaxLocal <= 1024, "16 bits for an item");
 };
 typedef __attribute__((address_space(3))) uint16_t *lds_half;
 typedef const __attribute__((address_space(3))) u32x2 *lds_pair;
+typedef const __attribute__((address_space(3))) uint32_t *lds_word;
 
 // The slots' experts, and per expert in use and 16 of its slots an item, experts in order.
-template <int FMT>
+template <typename L>
 __device__ __forceinline__ void ring_tables(const LayerArgs &a)
 {
-    typedef LayerRing<FMT> L;
     const int lane = threadIdx.x & (kWave - 1);
     for (int e = threadIdx.x; e < a.EL; e += blockDim.x)
         *lds_at<lds_int>(e * 4) = 0;
@@ -427,10 +444,9 @@ __device__ __forceinline__ void ring_tables(const LayerArgs &a)
 }
 
 // The slots of an item, in ascending order, to this wave's list; how many.
-template <int FMT>
+template <typename L>
 __device__ __forceinline__ int ring_slots(const LayerArgs &a, int item)
 {
-    typedef LayerRing<FMT> L;
     const int lane = threadIdx.x & (kWave - 1);
     const uint32_t list = L::kList + uniform(threadIdx.x / kWave) * 32;
     const int e = item >> 6, first = (item & 63) * 16;
@@ -451,7 +467,7 @@ __device__ __forceinline__ int ring_slots(const LayerArgs &a, int item)
 template <int FMT, bool UP>
 __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_ring(LayerArgs a)
 {
-    typedef LayerRing<FMT> L;
+    typedef LayerRing<FMT, UP> L;
     constexpr int C = kChunkCols<FMT>;
     extern __shared__ uint8_t ring_lds[]; // from 0, and the kernel's only LDS
     const int lane = threadIdx.x & (kWave - 1);
@@ -463,13 +479,12 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_ring(LayerArgs a)
         write_flags(a, reinterpret_cast<int *>(ring_lds));
         return;
     }
-    ring_tables<FMT>(a);
+    ring_tables<L>(a);
     const int K = UP ? a.H : a.I, N = UP ? 2 * a.I : a.H; // columns and rows of an expert's weights
     const int ntn = UP ? a.I / 64 : a.H / 128;
     const int tiles = uniform(*lds_at<lds_int>(L::kCount)) * ntn;
     const int stride = gridDim.x - (UP && a.flags ? 1 : 0);
-    const int steps = (K + L::kCols - 1) / L::kCols;
-    const bool half = K & (L::kCols - 1); // the last step has half of the columns (MXFP4)
+    const int steps = K / L::kCols; // (a whole number: H is a multiple of 256, I of 128)
     const uint32_t row_stride = static_cast<uint32_t>(row_bytes<FMT>(K)), row_blocks = K >> 5;
     const uint8_t *const weights = static_cast<const uint8_t *>(UP ? a.w1 : a.w2);
     const uint8_t *const scales = static_cast<const uint8_t *>(UP ? a.w1_scale : a.w2_scale);
@@ -477,9 +492,10 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_ring(LayerArgs a)
 
     // ---- loads: the tile and step to send for, and where it goes
     int to = blockIdx.x - stride, to_b = steps, to_stage = 0;
-    uint32_t woff[4], wrow = 0;
+    uint32_t woff[L::kWLoads], wrow = 0;
     const uint8_t *wbase = nullptr, *swbase = nullptr, *xrow[L::kXLoads] = {};
     bool with_x = true; // the newest loads have rows of bf16 among them
+    const int64_t to_rest = static_cast<int64_t>(a.slots) * K * 2;
     const auto send = [&]() {
         if (to >= tiles)
             return;
@@ -490,20 +506,23 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_ring(LayerArgs a)
             to_b = 0;
             const int which = to / ntn, ni = to - which * ntn;
             const int item = uniform(*lds_at<lds_half>(L::kItem + which * 2));
-            const int n = ring_slots<FMT>(a, item);
+            const int n = ring_slots<L>(a, item);
             const int64_t first = static_cast<int64_t>(item >> 6) * N +
                                   (UP ? ni * 64 + (wave >= 2 ? a.I : 0) + (wave & 1) * 32 : ni * 128 + wave * 32);
             wbase = weights + first * row_stride;
             if constexpr (FMT == kLayerMxfp4) {
                 swbase = scales + first * row_blocks;
-                wrow = (lane >> 1) * row_blocks;
+                // (a row's one or two words; of one, the upper lanes' are copies)
+                wrow = L::kChunks == 8 ? (lane >> 1) * row_blocks + (lane & 1) * 4 : (lane & 31) * row_blocks;
             } else if constexpr (FMT == kLayerFp8) { // (a run's rows lie in one block) lane j: run j % 2
                 const int row = UP ? (lane & 1) * a.I + ni * 64 : ni * 128;
                 swbase = scale_row<FMT>(scales, item >> 6, N, K, row);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                woff[i] = (i * 8 + (lane >> 3)) * row_stride;
+            for (int i = 0; i < L::kWLoads; ++i) {
+                const int r = i * L::kWRows + lane / L::kChunks;
+                woff[i] = r * row_stride + L::wplace(r, lane & (L::kChunks - 1)) * 16;
+            }
             with_x = wave * L::kXLoads * L::kXRows < n;
 #pragma unroll
             for (int i = 0; i < L::kXLoads; ++i) {
@@ -512,16 +531,12 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_ring(LayerArgs a)
                 xrow[i] = rows + static_cast<int64_t>(UP ? s / a.k : s) * K * 2;
             }
         }
-        const bool cut = half && to_b + 1 == steps;
         const uint32_t at = uniform(to_stage) * L::kStage;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            int c = place_of(wave * 32 + i * 8 + (lane >> 3), lane & 7);
-            c = cut ? c & 3 : c;
-            lds_load16(at + (wave * 4 + i) * 1024, wbase + to_b * 128 + (woff[i] + c * 16));
-        }
+        for (int i = 0; i < L::kWLoads; ++i)
+            lds_load16(at + (wave * L::kWLoads + i) * 1024, wbase + to_b * (16 * L::kChunks) + woff[i]);
         if constexpr (FMT == kLayerMxfp4)
-            lds_load4(at + L::kSW + wave * 256, swbase + to_b * 8 + (wrow + (cut ? 0 : (lane & 1) * 4)));
+            lds_load4(at + L::kSW + wave * 256, swbase + to_b * L::kChunks + wrow);
         else if constexpr (FMT == kLayerFp8)
             lds_load4(at + L::kSW + wave * 256, swbase + to_b * 4);
 #pragma unroll
@@ -529,9 +544,11 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_ring(LayerArgs a)
             if (!with_x)
                 break;
             const int r = (wave * L::kXLoads + i) * L::kXRows + lane * 16 / L::kXBytes;
-            int c = L::place(r, lane & (L::kXBytes / 16 - 1));
-            c = cut ? c & (L::kXBytes / 32 - 1) : c;
-            lds_load16(at + L::kX + (wave * L::kXLoads + i) * 1024, xrow[i] + to_b * L::kXBytes + c * 16);
+            const int c = L::place(r, lane & (L::kXBytes / 16 - 1));
+#pragma unroll
+            for (int p = 0; p < L::kPlanes; ++p)
+                lds_load16(at + L::kX + p * L::kPlane + (wave * L::kXLoads + i) * 1024,
+                           xrow[i] + p * to_rest + to_b * L::kXBytes + c * 16);
         }
         ++to_b;
         to_stage = to_stage + 1 == L::kStages ? 0 : to_stage + 1;
@@ -549,7 +566,7 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_ring(LayerArgs a)
             if (to >= tiles)
                 step_barrier<0>();
             else if (with_x)
-                step_barrier<(L::kStages - 2) * L::kLoads + L::kXLoads>(); // (of steps but the newest: at least)
+                step_barrier<(L::kStages - 2) * L::kLoads + L::kXLoads * L::kPlanes>(); // (of steps but the newest: at least)
             else
                 step_barrier<(L::kStages - 2) * L::kLoads>();
             send(); // over the stage before, which every wave is done with
@@ -561,28 +578,35 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_ring(LayerArgs a)
             for (int j = 0; j < 2; ++j) {
                 mine[j] = UP ? j * 64 + wave * 16 + l16 : wave * 32 + j * 16 + l16;
                 sc[j] = u32x2{0u, 0u};
-                if constexpr (FMT == kLayerMxfp4)
+                if constexpr (FMT == kLayerMxfp4 && L::kChunks == 8)
                     sc[j] = *lds_at<lds_pair>(at + L::kSW + mine[j] * 8);
+                else if constexpr (FMT == kLayerMxfp4)
+                    sc[j][0] = *lds_at<lds_word>(at + L::kSW + wave * 256 + (j * 16 + l16) * 4);
                 sum[j] = FMT == kLayerFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[j];
             }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) { // four chunks of a row
-                if (u == 1 && half && b + 1 == steps)
-                    break;
-                u32x4 x[C / 8];
+            for (int u = 0; u < L::kChunks / 4; ++u) { // four chunks of a row
+                u32x4 x[L::kPlanes][C / 8];
 #pragma unroll
-                for (int i = 0; i < C / 8; ++i)
-                    x[i] = *lds_at<lds_chunk>(at + L::kX + l16 * L::kXBytes +
-                                              L::place(l16, (u * 4 + quarter) * (C / 8) + i) * 16);
+                for (int p = 0; p < L::kPlanes; ++p)
+#pragma unroll
+                    for (int i = 0; i < C / 8; ++i)
+                        x[p][i] = *lds_at<lds_chunk>(at + L::kX + p * L::kPlane + l16 * L::kXBytes +
+                                                     L::place(l16, (u * 4 + quarter) * (C / 8) + i) * 16);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const u32x4 w = *lds_at<lds_chunk>(at + mine[j] * 128 + place_of(mine[j], u * 4 + quarter) * 16);
+                    const u32x4 w = *lds_at<lds_chunk>(at + mine[j] * (16 * L::kChunks) +
+                                                       L::wplace(mine[j], u * 4 + quarter) * 16);
                     const uint32_t word = sc[j][u];
                     const float f = mx_scale_operand((word >> (quarter * 8)) & 255u);
 #pragma unroll
-                    for (int i = 0; i < C / 8; ++i)
-                        sum[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, eight<FMT>(w, i, f)),
-                                                                         __builtin_bit_cast(bf16x8, x[i]), sum[j], 0, 0, 0);
+                    for (int i = 0; i < C / 8; ++i) {
+                        const bf16x8 v = __builtin_bit_cast(bf16x8, eight<FMT>(w, i, f));
+#pragma unroll
+                        for (int p = 0; p < L::kPlanes; ++p)
+                            sum[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8, x[p][i]),
+                                                                             sum[j], 0, 0, 0);
+                    }
                 }
             }
 #pragma unroll
@@ -600,7 +624,7 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_ring(LayerArgs a)
         }
         // acc[j][i]: weight row 4 quarter + i of run j, slot l16 of the tile
         const int which = t / ntn, ni = t - which * ntn;
-        const int n = ring_slots<FMT>(a, uniform(*lds_at<lds_half>(L::kItem + which * 2)));
+        const int n = ring_slots<L>(a, uniform(*lds_at<lds_half>(L::kItem + which * 2)));
         if (l16 < n) {
             const int64_t s = *lds_at<lds_half>(L::kList + wave * 32 + l16 * 2);
             if constexpr (UP) {
@@ -608,8 +632,11 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_ring(LayerArgs a)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     h[i] = gated(acc[0][i], acc[1][i]);
-                *reinterpret_cast<u32x2 *>(a.h + s * a.I + ni * 64 + wave * 16 + quarter * 4) =
-                    u32x2{pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3])};
+                uint16_t *o = a.h + s * a.I + ni * 64 + wave * 16 + quarter * 4;
+                const u32x2 top = {pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3])};
+                *reinterpret_cast<u32x2 *>(o) = top;
+                *reinterpret_cast<u32x2 *>(o + static_cast<int64_t>(a.slots) * a.I) =
+                    u32x2{rest_bf16(h[0], h[1], top[0]), rest_bf16(h[2], h[3], top[1])};
             } else {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
@@ -681,9 +708,9 @@ static hipError_t launch_layer_of(const LayerArgs &a, hipStream_t s)
     const int64_t items = layer_items(a.slots, a.EL);
     const int64_t up = items * (a.I / 64), down = items * (a.H / 128), most = 2 * kCus;
     launch(k_layer_ring<FMT, true>, dim3(static_cast<unsigned>(up < most ? up : most) + (a.flags ? 1 : 0)), blk,
-           LayerRing<FMT>::kBytes, s, a);
+           LayerRing<FMT, true>::kBytes, s, a);
     launch(k_layer_ring<FMT, false>, dim3(static_cast<unsigned>(down < most ? down : most)), blk,
-           LayerRing<FMT>::kBytes, s, a);
+           LayerRing<FMT, false>::kBytes, s, a);
     launch(k_layer_sum, dim3((a.T * (a.H / 4) + kLayerWaves * kWave - 1) / (kLayerWaves * kWave)), blk, 0, s, a);
     return hipGetLastError();
 }
