@@ -380,7 +380,7 @@ int check_layer(const moe_desc *desc, int32_t H, int32_t I)
     return MOE_OK;
 }
 
-// h (rounded, then what that left), then (slots that share weights) their fp32 outputs; more than none for no tokens.
+// h (4 bytes a value), then (slots that share weights) their fp32 outputs; more than none for no tokens.
 size_t layer_ws_bytes(const moe_desc *desc, int32_t H, int32_t I)
 {
     const size_t slots = static_cast<size_t>(desc->T) * desc->k;

@@ -2,7 +2,7 @@
 //
 //   h[s]   = silu(W1g[e] x[t]) * (W1u[e] x[t])          for every slot s = (t, j), e its expert
 //   out[t] = sum over t's local slots of w[s] * W2[e] h[s]
-// No rows are laid out: the first kernel writes h (two rows of bf16 per slot) to the
+// No rows are laid out: the first kernel writes h to the
 // workspace, the second one multiplies it and sums a token's slots (where slots
 // share weights a third one does).
 // The weights of the experts in use are what has to be read; tokens and h are
@@ -10,9 +10,10 @@
 // E2M1 codes are exact there, an E8M0 scale too) and multiplied with bf16 tokens
 // in fp32; the fp32 scale of a block of E4M3 weights enters after the products of
 // its columns.  Tokens that are not quantized cost nothing here: the rates of the
-// units are several times what the weights' bytes need.  h is two bf16 terms, its rounding and
-// the rest, about 16 bits in all (the outputs' error against 64 bits is then the final rounding's, 0.0017 instead of
-// 0.0024 relative).  Everything else stays in fp32 until out.
+// units are several times what the weights' bytes need.  Everything stays in fp32 until out, but h
+// where slots share weights, which is an operand of the matrix instructions: two bf16 terms, its rounding and the
+// rest, about 16 bits in all (the outputs' error against 64 bits is the final rounding's then, 0.0017 relative; with
+// one term 0.0024).
 //
 // There are two forms.  With few slots every slot is on its own (an
 // expert that two tokens share is read twice, the second time from the L2): a wave
@@ -137,7 +138,9 @@ __device__ void write_flags(const LayerArgs &a, int *flags)
 // The two kernels, us (bytes): one token, top-8 of 128, E4M3, H = 2048, I = 768 6.4 (25 MB)
 // and 5.6 (13 MB), MXFP4, H = 4096, I = 1024 8.1 (36 MB) and 6.1 (18 MB): latency counts
 // as much as HBM.  5 tokens, top-6 of 64, half of them local, bf16 14.8 (70 MB) and 8.6 (35 MB).
-// (The second ones with h rounded to bf16; the second term costs 0.4, 1.7 and 3.8 us.)
+// h is fp32, in the order in which the second kernel's lanes take it (row after row, lanes 128 bytes apart with
+// MXFP4: top-8 of 128, whole layer, T = 1, H = 4096, I = 1024 20.6 us instead of 16.9, T = 6, H = 2048, I = 768 40.0
+// instead of 32.5).
 
 // The sum over the wave's lanes, in lane 63: in rows of 16 lanes, then across them.
 template <int CTRL>
@@ -176,6 +179,35 @@ __device__ __forceinline__ float chunk_dot(const u32x4 &w, uint32_t scale, const
     return FMT == kLayerFp8 ? fmaf(q, __uint_as_float(scale), acc) : q;
 }
 
+// The same with columns of h, in fp32.
+template <int FMT>
+__device__ __forceinline__ float chunk_dot32(const u32x4 &w, uint32_t scale, const f32x4 (&h)[kChunkCols<FMT> / 4],
+                                             float acc)
+{
+    float q = FMT == kLayerFp8 ? 0.f : acc;
+    const float s = FMT == kLayerMxfp4 ? mx_scale_operand(scale) : 1.0f;
+#pragma unroll
+    for (int j = 0; j < kChunkCols<FMT> / 2; ++j) {
+        f32x2 v;
+        if constexpr (FMT == kLayerBf16) {
+            v[0] = __uint_as_float(w[j] << 16);
+            v[1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        } else if constexpr (FMT == kLayerFp8) {
+            v = j & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[j >> 1], 1.0f, true)
+                      : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[j >> 1], 1.0f, false);
+        } else {
+            const uint32_t word = w[j >> 2];
+            v = (j & 3) == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, s, 0)
+                : (j & 3) == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, s, 1)
+                : (j & 3) == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, s, 2)
+                               : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, s, 3);
+        }
+        q = fmaf(v[0], h[j >> 1][2 * (j & 1)], q);
+        q = fmaf(v[1], h[j >> 1][2 * (j & 1) + 1], q);
+    }
+    return FMT == kLayerFp8 ? fmaf(q, __uint_as_float(scale), acc) : q;
+}
+
 // The scale that chunk c of a row goes with.
 template <int FMT>
 __device__ __forceinline__ uint32_t chunk_scale(const uint8_t *scales, int c)
@@ -185,6 +217,14 @@ __device__ __forceinline__ uint32_t chunk_scale(const uint8_t *scales, int c)
     else if constexpr (FMT == kLayerFp8)
         return reinterpret_cast<const uint32_t *>(scales)[c >> 3];
     return 0;
+}
+
+// Where a slot's row of h has quad i of the columns that chunk c of a row of W2 is multiplied with:
+// lanes have consecutive chunks, and read consecutive quads.
+template <int FMT>
+__device__ __forceinline__ int h_quad(int I, int c, int i)
+{
+    return (i * (I / kChunkCols<FMT>) + c) * 4;
 }
 
 // A wave has one slot and N columns of h, N gate rows and N up rows.  Grid: [slots]
@@ -253,14 +293,9 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_up_slots(LayerArg
     for (int i = 0; i < N; ++i)
         h[i] = gated(acc[i], acc[N + i]);
     if (lane == kWave - 1) {
-        uint32_t *o = reinterpret_cast<uint32_t *>(a.h + static_cast<int64_t>(s) * a.I + n0);
-        uint32_t *rest = o + static_cast<int64_t>(a.slots) * a.I / 2;
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            const uint32_t top = pack_bf16(h[i], h[i + 1]);
-            o[i / 2] = top;
-            rest[i / 2] = rest_bf16(h[i], h[i + 1], top);
-        }
+        static_assert(N == 2, "columns of one quad");
+        float *o = reinterpret_cast<float *>(a.h) + static_cast<int64_t>(s) * a.I;
+        *reinterpret_cast<f32x2 *>(o + h_quad<FMT>(a.I, n0 / C, n0 % C >> 2) + (n0 & 3)) = f32x2{h[0], h[1]};
     }
 }
 
@@ -299,7 +334,8 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_slots(LayerA
     for (int i = 0; i < N; ++i)
         acc[i] = 0.f;
     for (int base = 0; base < total; base += U * kWave) {
-        u32x4 v[U][N], hv[U][C / 8], rest[U][C / 8];
+        u32x4 v[U][N];
+        f32x4 hv[U][C / 4];
         uint32_t sc[U][N];
         float f[U];
 #pragma unroll
@@ -310,17 +346,15 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_slots(LayerA
             f[u] = __shfl(weight, j);
             const uint8_t *wr = weight_row<FMT>(a.w2, e, a.H, a.I, n0) + c * 16;
             const uint8_t *sr = scale_row<FMT>(a.w2_scale, e, a.H, a.I, n0);
-            const uint16_t *h = a.h + static_cast<int64_t>(slot) * a.I + c * C;
+            const float *h = reinterpret_cast<const float *>(a.h) + static_cast<int64_t>(slot) * a.I;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 v[u][i] = *reinterpret_cast<const u32x4 *>(wr + i * stride);
                 sc[u][i] = chunk_scale<FMT>(sr + i * scale_stride, c);
             }
 #pragma unroll
-            for (int i = 0; i < C / 8; ++i) {
-                hv[u][i] = *reinterpret_cast<const u32x4 *>(h + i * 8);
-                rest[u][i] = *reinterpret_cast<const u32x4 *>(h + static_cast<int64_t>(a.slots) * a.I + i * 8);
-            }
+            for (int i = 0; i < C / 4; ++i)
+                hv[u][i] = *reinterpret_cast<const f32x4 *>(h + h_quad<FMT>(a.I, c, i));
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -328,7 +362,7 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_slots(LayerA
             const bool in = base + u * kWave + lane < total;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float q = chunk_dot<FMT>(v[u][i], sc[u][i], hv[u], chunk_dot<FMT>(v[u][i], sc[u][i], rest[u], 0.f));
+                const float q = chunk_dot32<FMT>(v[u][i], sc[u][i], hv[u], 0.f);
                 acc[i] = in ? fmaf(q, f[u], acc[i]) : acc[i];
             }
         }

@@ -245,7 +245,8 @@ struct LayerArgs {
     const uint16_t *x;      // [T,H] bf16
     const void *w1, *w1_scale; // [EL,2I,H] and its scales
     const void *w2, *w2_scale; // [EL,H,I] and its scales
-    uint16_t *h;            // workspace: [2][T*k,I] bf16, h rounded, then what that left
+    uint16_t *h;            // workspace: [2][T*k,I] bf16, h rounded, then what that left; [T*k,I] fp32 where
+                            // every slot is on its own
     float *y;               // workspace: [T*k,H] fp32, where slots share experts' weights
     uint16_t *out;          // [T,H] bf16
     int32_t *flags;         // one word or null

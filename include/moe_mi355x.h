@@ -507,8 +507,8 @@ int moe_expert_swiglu_mxfp4(const moe_desc *desc, const moe_handle *handle, cons
  *               a local slot.
  *   flags       device [1] int32 out or NULL: MOE_FLAG_BAD_ID, MOE_FLAG_DUPLICATE.
  * Tokens are not quantized: products of bf16 with the weights' values are summed in
- * fp32 (E4M3: each block's sum enters with its scale), h is two bf16 terms between the
- * products, about 16 bits.
+ * fp32 (E4M3: each block's sum enters with its scale), h is fp32 with two kernels
+ * and two bf16 terms, about 16 bits, with three.
  * (MXFP4 values past bf16's range, scale bytes of 253 and more, are infinite or NaN.)
  * The order of every sum is fixed by the sizes: equal calls give equal bits.  All
  * pointers but topk_idx, topk_w and flags must be 16-byte aligned; outputs must not

@@ -37,3 +37,10 @@ def run(fmt, shape, h_step):
 @pytest.mark.parametrize("shape", SHARED, ids=lambda s: "-".join(map(str, s)))
 def test_slots_that_share_experts_keep_two_terms_of_h(shape, fmt):
     run(fmt, shape, 2.0 ** -16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("shape", OWN, ids=lambda s: "-".join(map(str, s)))
+def test_slots_on_their_own_keep_h_in_fp32(shape, fmt):
+    run(fmt, shape, 0.0)
