@@ -10,7 +10,8 @@ The convenience functions at the bottom (``alloc_handle``, ``route``,
 ``combine_weighted``, ``combine_weighted_bwd``, ``expert_gemm_fp8``,
 ``expert_swiglu_fp8``, ``quantize_mxfp4``, ``dequantize_mxfp4``, ``dispatch_mxfp4``,
 ``expert_gemm_mxfp4``, ``expert_swiglu_mxfp4``, ``layer_tokens``) only add output
-allocation.  ``PreparedDispatch``,
+allocation, on the stream that they are given (inputs made on another stream are the
+caller's to order).  ``PreparedDispatch``,
 ``PreparedCombine``, ``PreparedCombineBwd``, ``PreparedCombineWeighted``,
 ``PreparedCombineWeightedBwd``, ``PreparedExpertGemmFp8``,
 ``PreparedExpertSwigluFp8``, ``PreparedExpertGemmMxfp4`` and
@@ -23,7 +24,10 @@ The library is loaded on first use; if it has not been built this raises
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
+import inspect
 import os
 import sys
 from dataclasses import dataclass
@@ -204,6 +208,41 @@ def _stream(stream) -> int:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _memory_of(stream):
+    """Tensors allocated inside are `stream`'s (None: the current one's), in its order: nothing orders a given
+    stream behind work queued on the current one that may still use a block freed there, and a block freed
+    later waits for what it was allocated for."""
+    if stream is None or not torch.cuda.is_available():
+        return contextlib.nullcontext()
+    if isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream)) if int(stream) else
+                             torch.cuda.default_stream())
+
+
+def _allocates(f):
+    """For a convenience function: given a stream, what it allocates is that stream's, and what it returns
+    stays until the caller's stream, too, is done with it."""
+    at = list(inspect.signature(f).parameters).index("stream")
+
+    @functools.wraps(f)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None or not torch.cuda.is_available():
+            return f(*args, **kw)
+        with _memory_of(stream):
+            out = f(*args, **kw)
+        cur = torch.cuda.current_stream()
+        if cur.cuda_stream != _stream(stream):
+            for t in out if isinstance(out, tuple) else (out,):
+                for x in vars(t).values() if isinstance(t, Handle) else (t,):
+                    if isinstance(x, torch.Tensor) and x.is_cuda:
+                        x.record_stream(cur)
+        return out
+
+    return call
 
 
 @dataclass
@@ -853,32 +892,25 @@ def moe_layer_tokens(desc: Desc, topk_idx: torch.Tensor, topk_w: torch.Tensor, x
 
 class PreparedLayerTokens:
     """moe_layer_tokens over buffers that a loop reuses on every step, checked once; it keeps its own
-    workspace.  The tensors must stay as they are (no resize_ or set_) while the object is in use; it
-    holds references to them.  It may be let go while calls are on their way: the workspace is not handed out
-    before its stream is done with it.  Calls of one object share its workspace: they must not overlap."""
+    workspace, of its stream's memory.  The tensors must stay as they are (no resize_ or set_) while the object is in
+    use; it holds references to them.  It may be let go while calls are on their way: the workspace is not handed
+    out before its stream is done with it.  Calls of one object share its workspace: they must not overlap."""
 
     def __init__(self, desc: Desc, topk_idx: torch.Tensor, topk_w: torch.Tensor, x: torch.Tensor,
                  w1: torch.Tensor, w2: torch.Tensor, out: torch.Tensor,
                  w1_scale: torch.Tensor | None = None, w2_scale: torch.Tensor | None = None,
                  flags: torch.Tensor | None = None, stream=None):
-        ws = _layer_workspace(desc, w2, w1_scale)
+        with _memory_of(stream):
+            ws = _layer_workspace(desc, w2, w1_scale)
         self._desc = Desc.from_buffer_copy(desc)
         self._args = (ctypes.byref(self._desc),
                       *_layer_args(self._desc, topk_idx, topk_w, x, w1, w2, out, w1_scale, w2_scale, ws,
                                    flags, stream))
         self._fn = lib().moe_layer_tokens
-        _used_on(ws, stream)
         self._keep = (topk_idx, topk_w, x, w1, w2, out, w1_scale, w2_scale, ws, flags)
 
     def __call__(self) -> int:
         return _check(self._fn(*self._args))
-
-
-def _used_on(t, stream):
-    """Tell the allocator that calls on `stream` (None: the one it has it for) use t, a fresh tensor."""
-    if stream is not None and t.is_cuda:
-        s = _stream(stream)
-        t.record_stream(torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream())
 
 
 def _layer_workspace(desc, w2, w1_scale):
@@ -1103,6 +1135,7 @@ class KernelTimer:
 # convenience wrappers that allocate outputs
 # ---------------------------------------------------------------------------
 
+@_allocates
 def route(desc: Desc, topk_idx: torch.Tensor, topk_w: torch.Tensor | None = None,
           want_probs: bool = False, with_map: bool = True, handle: Handle | None = None,
           stream=None):
@@ -1118,6 +1151,7 @@ def rows_for(desc: Desc, handle: Handle) -> int:
     return desc.capacity if desc.mode == MOE_SYNC_FREE else handle.total
 
 
+@_allocates
 def dispatch(desc: Desc, handle: Handle, x: torch.Tensor, topk_w: torch.Tensor | None = None,
              meta: bool = True, stream=None):
     """moe_dispatch with fresh outputs: (rows, row_w, row_token, row_expert)."""
@@ -1130,6 +1164,7 @@ def dispatch(desc: Desc, handle: Handle, x: torch.Tensor, topk_w: torch.Tensor |
     return rows, row_w, rt, re
 
 
+@_allocates
 def dispatch_fp8(desc: Desc, handle: Handle, x: torch.Tensor, topk_w: torch.Tensor | None = None,
                  meta: bool = True, stream=None):
     """moe_dispatch_fp8 with fresh outputs: (rows_q [R,H] float8_e4m3fn, row_scale [R,H/128],
@@ -1145,6 +1180,7 @@ def dispatch_fp8(desc: Desc, handle: Handle, x: torch.Tensor, topk_w: torch.Tens
     return rows_q, row_scale, row_w, rt, re
 
 
+@_allocates
 def combine(desc: Desc, handle: Handle, Y: torch.Tensor, out_dtype=torch.bfloat16, stream=None):
     R, H = Y.shape
     out = torch.empty((desc.T, H), dtype=out_dtype, device=Y.device)
@@ -1152,6 +1188,7 @@ def combine(desc: Desc, handle: Handle, Y: torch.Tensor, out_dtype=torch.bfloat1
     return out
 
 
+@_allocates
 def combine_bwd(desc: Desc, handle: Handle, grad_out: torch.Tensor, R: int,
                 expert_out: torch.Tensor | None = None, stream=None):
     H, dev = grad_out.shape[1], grad_out.device
@@ -1161,6 +1198,7 @@ def combine_bwd(desc: Desc, handle: Handle, grad_out: torch.Tensor, R: int,
     return grad_rows, dw
 
 
+@_allocates
 def dispatch_bwd(desc: Desc, handle: Handle, grad_rows: torch.Tensor,
                  grad_row_w: torch.Tensor | None = None, out_dtype=torch.bfloat16, stream=None):
     """moe_dispatch_bwd with fresh outputs: (grad_x, grad_topk_w or None)."""
@@ -1172,6 +1210,7 @@ def dispatch_bwd(desc: Desc, handle: Handle, grad_rows: torch.Tensor,
     return gx, gtw
 
 
+@_allocates
 def combine_weighted(desc: Desc, handle: Handle, Y: torch.Tensor, topk_w: torch.Tensor,
                      out_dtype=torch.bfloat16, stream=None):
     """moe_combine_weighted with a fresh output [T,H]."""
@@ -1181,6 +1220,7 @@ def combine_weighted(desc: Desc, handle: Handle, Y: torch.Tensor, topk_w: torch.
     return out
 
 
+@_allocates
 def combine_weighted_bwd(desc: Desc, handle: Handle, grad_out: torch.Tensor, Y: torch.Tensor,
                          topk_w: torch.Tensor, stream=None):
     """moe_combine_weighted_bwd with fresh outputs: (grad_rows, dw)."""
@@ -1191,6 +1231,7 @@ def combine_weighted_bwd(desc: Desc, handle: Handle, grad_out: torch.Tensor, Y: 
     return grad_rows, dw
 
 
+@_allocates
 def expert_gemm_fp8(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scale: torch.Tensor,
                     w_q: torch.Tensor, w_scale: torch.Tensor, stream=None):
     """moe_expert_gemm_fp8 with a fresh output [R,N] bf16 (its rows past the total are not written)."""
@@ -1201,6 +1242,7 @@ def expert_gemm_fp8(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scale:
     return out
 
 
+@_allocates
 def expert_swiglu_fp8(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scale: torch.Tensor,
                       w_q: torch.Tensor, w_scale: torch.Tensor, out_dtype=torch.float8_e4m3fn,
                       stream=None):
@@ -1218,6 +1260,7 @@ def expert_swiglu_fp8(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scal
     return out, out_scale
 
 
+@_allocates
 def quantize_mxfp4(x: torch.Tensor, stream=None):
     """moe_quantize_mxfp4 of x [...,K] bf16 or fp32 with fresh outputs: (q [...,K/2], scale
     [...,K/32]), uint8."""
@@ -1230,6 +1273,7 @@ def quantize_mxfp4(x: torch.Tensor, stream=None):
     return q, scale
 
 
+@_allocates
 def dequantize_mxfp4(q: torch.Tensor, scale: torch.Tensor, out_dtype=torch.bfloat16, stream=None):
     """moe_dequantize_mxfp4 with a fresh output [...,K]."""
     K = 2 * q.shape[-1]
@@ -1241,6 +1285,7 @@ def dequantize_mxfp4(q: torch.Tensor, scale: torch.Tensor, out_dtype=torch.bfloa
     return out
 
 
+@_allocates
 def dispatch_mxfp4(desc: Desc, handle: Handle, x: torch.Tensor, topk_w: torch.Tensor | None = None,
                    meta: bool = True, stream=None):
     """moe_dispatch_mxfp4 with fresh outputs: (rows_q [R,H/2], row_scale [R,H/32], row_w, row_token,
@@ -1256,6 +1301,7 @@ def dispatch_mxfp4(desc: Desc, handle: Handle, x: torch.Tensor, topk_w: torch.Te
     return rows_q, row_scale, row_w, rt, re
 
 
+@_allocates
 def expert_gemm_mxfp4(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scale: torch.Tensor,
                       w_q: torch.Tensor, w_scale: torch.Tensor, stream=None):
     """moe_expert_gemm_mxfp4 with a fresh output [R,N] bf16 (its rows past the total are not written)."""
@@ -1266,6 +1312,7 @@ def expert_gemm_mxfp4(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scal
     return out
 
 
+@_allocates
 def expert_swiglu_mxfp4(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_scale: torch.Tensor,
                         w_q: torch.Tensor, w_scale: torch.Tensor, out_dtype=torch.uint8,
                         stream=None):
@@ -1285,6 +1332,7 @@ def expert_swiglu_mxfp4(desc: Desc, handle: Handle, rows_q: torch.Tensor, row_sc
     return out, out_scale
 
 
+@_allocates
 def layer_tokens(desc: Desc, topk_idx: torch.Tensor, topk_w: torch.Tensor, x: torch.Tensor,
                  w1: torch.Tensor, w2: torch.Tensor, w1_scale: torch.Tensor | None = None,
                  w2_scale: torch.Tensor | None = None, flags: torch.Tensor | None = None, stream=None):
@@ -1293,7 +1341,6 @@ def layer_tokens(desc: Desc, topk_idx: torch.Tensor, topk_w: torch.Tensor, x: to
     ws = _layer_workspace(desc, w2, w1_scale)
     moe_layer_tokens(desc, topk_idx, topk_w, x, w1, w2, out, ws, w1_scale, w2_scale, flags,
                      stream=stream)
-    _used_on(ws, stream)  # (let go here, while that stream may still use it)
     return out
 
 
