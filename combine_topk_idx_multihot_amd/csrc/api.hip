@@ -380,11 +380,9 @@ int check_layer(const moe_desc *desc, int32_t H, int32_t I)
     return MOE_OK;
 }
 
-// h (4 bytes a value), then (slots that share weights) their fp32 outputs; more than none for no tokens.
 size_t layer_ws_bytes(const moe_desc *desc, int32_t H, int32_t I)
 {
-    const size_t slots = static_cast<size_t>(desc->T) * desc->k;
-    return 16 + slots * I * 4 + (moe::layer_singles(slots, desc->E, moe::kLayerMxfp4) ? 0 : slots * H * 4);
+    return moe::layer_ws_bytes(desc->T * desc->k, desc->E, H, I);
 }
 
 // Argument rules shared by the quantization to MXFP4 and the way back, and its
