@@ -11,15 +11,17 @@ constexpr int kLayerMaxSlots = 1024;  // T * k at most
 constexpr int kLayerMaxWidth = 65536; // H and I at most
 enum { kLayerBf16 = 0, kLayerFp8 = 1, kLayerMxfp4 = 2 }; // the weights' format
 
-// Whether every slot is on its own: up to 16 of them, or 7 (E4M3 5, MXFP4 3) for 8 experts.
-// Together / on its own, us: top-8 of 128, H = 2048, I = 768: bf16 T = 8 115 / 93, T = 12 142 / 134,
-// T = 16 161 / 169; E4M3 T = 8 54.9 / 52.3, T = 10 60.8 / 62.6, T = 12 69.9 / 73.7; MXFP4 T = 4 27.3 /
-// 22.4, T = 8 36.7 / 37.9, T = 10 39.9 / 45.1.  Top-2 of 32, H = 4096, I = 1024: bf16 T = 10 86.9 / 82.0, T =
-// 14 111 / 108; E4M3 42.2 / 40.9, 53.1 / 54.1; MXFP4 T = 10 29.0 / 37.0.  Top-2 of 8, H = I = 2048,
-// T = 8: 39.3 / 47.9, 29.1 / 25.9, 21.7 / 23.7.
+// Whether every slot is on its own: up to 16 of them, or 7 (E4M3 5, MXFP4 4) for 8 experts.
+// Together / on its own, us: top-8 of 128, H = 2048, I = 768: bf16 T = 8 107 / 93, T = 12 143 / 134, T = 14 149 / 155, T =
+// 16 161 / 174; E4M3 T = 8 57.9 / 53.3, T = 10 61.8 / 63.7, T = 12 71.5 / 74.2; MXFP4 T = 4 30.4 / 24.7, T = 7 39.7 / 37.0,
+// T = 8 41.6 / 40.8, T = 10 44.9 / 48.6.  Top-2 of 32, H = 4096, I = 1024: T = 10 bf16 84.5 / 81.3, E4M3 51.6 /
+// 45.4, MXFP4 35.0 / 42.6; T = 14 110 / 107, 66.2 / 59.4, 44.0 / 55.3.
+// 16 slots: top-2 of 8, H = I = 2048 bf16 53.0 / 53.7, E4M3 30.4 / 30.0, MXFP4 26.2 / 24.7; top-4 of 4, H = 4096, I = 1024
+// 40.8 / 46.3, 31.2 / 25.5, 24.3 / 21.7; top-2 of 32, H = 4096, I = 1024 72.6 / 66.8, 46.0 / 39.2, 32.1 / 36.0; of one
+// expert, H = I = 2048 30.7 / 26.3, 27.0 / 22.6, 24.3 / 27.9.
 inline bool layer_singles(int64_t slots, int64_t E, int fmt)
 {
-    return slots <= 16 || 8 * slots <= (fmt == kLayerBf16 ? 7 : fmt == kLayerFp8 ? 5 : 3) * E;
+    return slots <= 16 || 8 * slots <= (fmt == kLayerBf16 ? 7 : fmt == kLayerFp8 ? 5 : 4) * E;
 }
 
 // The most items that `slots` slots of EL experts make: one per expert in use, and

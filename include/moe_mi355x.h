@@ -481,7 +481,7 @@ int moe_expert_swiglu_mxfp4(const moe_desc *desc, const moe_handle *handle, cons
 
 /*
  * A whole MoE layer for a few tokens, ids to outputs, in two kernels, or in three where
- * T * k exceeds both 16 and 7 E / 8 (E4M3: 5 E / 8, MXFP4: 3 E / 8): with slot s = (t,j) of local expert e,
+ * T * k exceeds both 16 and 7 E / 8 (E4M3: 5 E / 8, MXFP4: E / 2): with slot s = (t,j) of local expert e,
  *   h[s]   = silu(gate) * up, gate = W1[e] rows 0 .. I-1 times x[t], up = rows I .. 2I-1
  *            times x[t],
  *   out[t] = sum over t's local slots of topk_w[s] * (W2[e] h[s]).
