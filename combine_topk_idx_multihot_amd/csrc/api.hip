@@ -257,7 +257,7 @@ moe::RowArgs dispatch_args(const moe_desc *desc, const moe_handle *handle, const
 
 // Argument rules shared by the experts' products on E4M3 and on MXFP4 rows.
 int check_product(const moe_desc *desc, const moe_handle *handle, const void *rows_q,
-                  const void *row_scale, int32_t K, int64_t R, const void *w_q, const void *w_scale)
+                  const void *row_scale, int32_t K, int64_t R, const void *w_q, const void *w_scale, bool mx)
 {
     int rc;
     if ((rc = check_desc(desc)) != MOE_OK)
@@ -269,13 +269,17 @@ int check_product(const moe_desc *desc, const moe_handle *handle, const void *ro
     if (K <= 0 || K % 128 != 0 || K > (1 << 23))
         return fail(MOE_ERR_ARG, "K must be a positive multiple of 128 up to 2^23 (got %d)", K);
     if (R > 0 && (!rows_q || !aligned16(rows_q)))
-        return fail(MOE_ERR_ARG, "rows_q must be a non-NULL, 16-byte aligned byte tensor of R rows");
+        return fail(MOE_ERR_ARG, "rows_q must be a non-NULL, 16-byte aligned %s tensor",
+                    mx ? "[R,K/2] byte" : "[R,K] byte");
     if (R > 0 && (!row_scale || !aligned16(row_scale)))
-        return fail(MOE_ERR_ARG, "row_scale must be a non-NULL, 16-byte aligned tensor of R rows");
+        return fail(MOE_ERR_ARG, "row_scale must be a non-NULL, 16-byte aligned %s tensor",
+                    mx ? "[R,K/32] byte" : "[R,K/128] fp32");
     if (R > 0 && (!w_q || !aligned16(w_q)))
-        return fail(MOE_ERR_ARG, "w_q must be a non-NULL, 16-byte aligned byte tensor of EL experts");
+        return fail(MOE_ERR_ARG, "w_q must be a non-NULL, 16-byte aligned %s tensor",
+                    mx ? "[EL,N,K/2] byte" : "[EL,N,K] byte");
     if (R > 0 && (!w_scale || !aligned16(w_scale)))
-        return fail(MOE_ERR_ARG, "w_scale must be a non-NULL, 16-byte aligned tensor of EL experts");
+        return fail(MOE_ERR_ARG, "w_scale must be a non-NULL, 16-byte aligned %s tensor",
+                    mx ? "[EL,N,K/32] byte" : "[EL,ceil(N/128),K/128] fp32");
     return MOE_OK;
 }
 
@@ -288,14 +292,15 @@ int check_gemm_out(int32_t N, int64_t R, const void *out)
     return MOE_OK;
 }
 
-int check_swiglu_out(int32_t I, int64_t R, const void *out, const void *out_scale)
+int check_swiglu_out(int32_t I, int64_t R, const void *out, const void *out_scale, bool mx)
 {
     if (I <= 0 || I % 128 != 0 || I > (1 << 29))
         return fail(MOE_ERR_ARG, "I must be a positive multiple of 128 up to 2^29 (got %d)", I);
     if (R > 0 && (!out || !aligned16(out)))
-        return fail(MOE_ERR_ARG, "out must be a non-NULL, 16-byte aligned [R,I] tensor");
+        return fail(MOE_ERR_ARG, "out must be a non-NULL, 16-byte aligned %s tensor",
+                    !out_scale ? "[R,I] bf16" : mx ? "[R,I/2] byte" : "[R,I] byte");
     if (out_scale && !aligned16(out_scale))
-        return fail(MOE_ERR_ARG, "out_scale must be 16-byte aligned");
+        return fail(MOE_ERR_ARG, "out_scale must be a 16-byte aligned %s tensor", mx ? "[R,I/32] byte" : "[R,I/128] fp32");
     return MOE_OK;
 }
 
@@ -1019,7 +1024,7 @@ int moe_expert_gemm_fp8(const moe_desc *desc, const moe_handle *handle, const ui
 {
     TimingScope timing_scope;
     int rc;
-    if ((rc = check_product(desc, handle, rows_q, row_scale, K, R, w_q, w_scale)) != MOE_OK)
+    if ((rc = check_product(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, false)) != MOE_OK)
         return rc;
     if ((rc = check_gemm_out(N, R, out)) != MOE_OK)
         return rc;
@@ -1033,9 +1038,9 @@ int moe_expert_swiglu_fp8(const moe_desc *desc, const moe_handle *handle, const 
 {
     TimingScope timing_scope;
     int rc;
-    if ((rc = check_product(desc, handle, rows_q, row_scale, K, R, w_q, w_scale)) != MOE_OK)
+    if ((rc = check_product(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, false)) != MOE_OK)
         return rc;
-    if ((rc = check_swiglu_out(I, R, out, out_scale)) != MOE_OK)
+    if ((rc = check_swiglu_out(I, R, out, out_scale, false)) != MOE_OK)
         return rc;
     return launch_product(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, I, true, out, out_scale, stream);
 }
@@ -1105,7 +1110,7 @@ int moe_expert_gemm_mxfp4(const moe_desc *desc, const moe_handle *handle, const 
 {
     TimingScope timing_scope;
     int rc;
-    if ((rc = check_product(desc, handle, rows_q, row_scale, K, R, w_q, w_scale)) != MOE_OK)
+    if ((rc = check_product(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, true)) != MOE_OK)
         return rc;
     if ((rc = check_gemm_out(N, R, out)) != MOE_OK)
         return rc;
@@ -1118,9 +1123,9 @@ int moe_expert_swiglu_mxfp4(const moe_desc *desc, const moe_handle *handle, cons
 {
     TimingScope timing_scope;
     int rc;
-    if ((rc = check_product(desc, handle, rows_q, row_scale, K, R, w_q, w_scale)) != MOE_OK)
+    if ((rc = check_product(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, true)) != MOE_OK)
         return rc;
-    if ((rc = check_swiglu_out(I, R, out, out_scale)) != MOE_OK)
+    if ((rc = check_swiglu_out(I, R, out, out_scale, true)) != MOE_OK)
         return rc;
     return launch_product_mx(desc, handle, rows_q, row_scale, K, R, w_q, w_scale, I, true, out, out_scale, stream);
 }
