@@ -136,8 +136,8 @@ __device__ void write_flags(const LayerArgs &a, int *flags)
 // and 4 chunks of columns, a chunk of MXFP4 needs four loads of the token beside
 // its own: one token, H = 4096, I = 1024 14.5 us for the first kernel.)
 // The two kernels, us (bytes): one token, top-8 of 128, E4M3, H = 2048, I = 768 6.4 (25 MB)
-// and 5.6 (13 MB), MXFP4, H = 4096, I = 1024 8.1 (36 MB) and 6.1 (18 MB): latency counts
-// as much as HBM.  5 tokens, top-6 of 64, half of them local, bf16 14.8 (70 MB) and 8.6 (35 MB).
+// and 5.7 (13 MB), MXFP4, H = 4096, I = 1024 8.4 (36 MB) and 7.1 (18 MB): latency counts
+// as much as HBM.  5 tokens, top-6 of 64, half of them local, bf16 15.2 (70 MB) and 9.6 (35 MB).
 // h is fp32, in the order in which the second kernel's lanes take it (row after row, lanes 128 bytes apart with
 // MXFP4: top-8 of 128, whole layer, T = 1, H = 4096, I = 1024 20.6 us instead of 16.9, T = 6, H = 2048, I = 768 40.0
 // instead of 32.5).
@@ -390,12 +390,12 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_slots(LayerA
 // has 32 weight rows for all columns: two runs of 16, in the first kernel gate and up rows
 // of the same columns of h.
 // (Weights from HBM to registers, a load taking 64 bytes of 16 rows, whose address units were busy
-// 72 % of the cycles with MXFP4: top-8 of 128, H = 2048, I = 768, 32 tokens MXFP4 86 us instead
+// 72 % of the cycles with MXFP4: with one term of h, top-8 of 128, H = 2048, I = 768, 32 tokens MXFP4 86 us instead
 // of 63, E4M3 123 / 109, bf16 206 / 218; 128 tokens 142 / 99, 181 / 139, 274 / 256; top-2 of 8, H =
 // I = 2048, 256 tokens 85 / 53, 104 / 68, 169 / 87.)
 //
-// Bound by HBM: 32 tokens with MXFP4 weights 41.5 and 23.6 us (186 and 95 MB: 4.5 and 4.0 TB/s), and
-// 4.8 us for the sums.
+// Bound by HBM, the second kernel by the bytes on their way: 32 tokens with MXFP4 weights 41.2 and 29.3 us (186 and
+// 95 MB: 4.5 and 3.2 TB/s), and 4.9 us for the sums.
 //
 // A stage: 128 weight rows, their scales (MXFP4 a byte per 32 columns; E4M3 each wave's two, of
 // its runs' blocks), and 16 rows of bf16: tokens, or rows of h, once for each term.  Where the tile has no slots for
@@ -404,9 +404,10 @@ __global__ void __launch_bounds__(kLayerWaves * kWave) k_layer_down_slots(LayerA
 //
 // The second kernel multiplies both terms of h with the weights that it has widened.  Top-8 of 128, H = 2048, I = 768, whole
 // layer, one term / two: MXFP4 T = 8 39.7 / 41.6, T = 32 68.6 / 72.9, T = 128 99.7 / 104.6; E4M3 T = 32 106.8 / 107.0,
-// T = 128 134 / 137; bf16 T = 32 215 / 212.  With MXFP4 weights and steps of 128 bytes, whose 1 KB per slot leaves room
-// for two stages, T = 16 to 256 take 1 us less with a last half step to treat apart; eight waves that share three such
-// stages, one workgroup per CU, 1 to 3 us more (fewer and larger tiles in the last round).
+// T = 128 134 / 137; bf16 T = 32 215 / 212.  MXFP4, T = 32, 64, 128 (73.7, 86.1, 106.2 here): steps of 128 bytes, whose
+// 1 KB per slot leaves room for two stages, 73.0, 84.3, 103.8, with a last half step to treat apart; tiles of 256 rows
+// and three stages 75.3, 83.5, 98.8, but top-2 of 8, H = I = 2048, T = 64 37.5 instead of 33.5; eight waves that share
+// three stages of 128 bytes, one workgroup per CU, 75.5, 86.0, 108.2.
 template <int FMT, bool UP>
 struct LayerRing {
     static constexpr int kPlanes = UP ? 1 : 2; // of rows of bf16: tokens, or h's two terms

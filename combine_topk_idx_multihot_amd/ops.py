@@ -570,6 +570,7 @@ def moe_layer_tokens(x, topk_idx, topk_w, w1, w2, num_experts, w1_scale=None, w2
                      local_begin=0):
     """The layer with SwiGLU experts for a few tokens (T * k <= 1024), in two or three kernels and
     without rows, a handle or a row count: safe to capture at every size.  x [T,H] bf16 is not quantized.
+    With more than two (MXFP4) or four (E4M3) slots per expert moe_layer_mxfp4 and moe_layer_fp8 are faster.
 
     Weights: w1 [EL,2I,H] (gate rows first) and w2 [EL,H,I], bf16 without scales, or E4M3 with one
     fp32 scale per 128 x 128 block as for moe_layer_fp8; or packed MXFP4 with E8M0 scales as for

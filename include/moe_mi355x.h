@@ -510,6 +510,9 @@ int moe_expert_swiglu_mxfp4(const moe_desc *desc, const moe_handle *handle, cons
  * fp32 (E4M3: each block's sum enters with its scale), h is fp32 with two kernels
  * and two bf16 terms, about 16 bits, with three.
  * (MXFP4 values past bf16's range, scale bytes of 253 and more, are infinite or NaN.)
+ * Made for a few slots per expert: top-8 of 128, H = 2048, I = 768, it is faster than route,
+ * dispatch, two products and combine one by one up to 32 tokens (MXFP4) or 64 (E4M3).
+ * Other widths are padded with zero columns by the caller.
  * The order of every sum is fixed by the sizes: equal calls give equal bits.  All
  * pointers but topk_idx, topk_w and flags must be 16-byte aligned; outputs must not
  * overlap inputs.  T == 0 launches nothing.
