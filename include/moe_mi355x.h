@@ -509,7 +509,8 @@ int moe_expert_swiglu_mxfp4(const moe_desc *desc, const moe_handle *handle, cons
  * Tokens are not quantized: products of bf16 with the weights' values are summed in
  * fp32 (E4M3: each block's sum enters with its scale), h is fp32 with two kernels
  * and two bf16 terms, about 16 bits, with three.
- * (MXFP4 values past bf16's range, scale bytes of 253 and more, are infinite or NaN.)
+ * (MXFP4 values past bf16's range, scale bytes of 253 and more, are infinite or NaN, as is an output that an
+ * infinite weight enters: the two terms of an h may have opposite signs.)
  * Made for a few slots per expert: top-8 of 128, H = 2048, I = 768, it is faster than route,
  * dispatch, two products and combine one by one up to 32 tokens (MXFP4) or 64 (E4M3).
  * Other widths are padded with zero columns by the caller.

@@ -44,3 +44,21 @@ def test_slots_that_share_experts_keep_two_terms_of_h(shape, fmt):
 @pytest.mark.parametrize("shape", OWN, ids=lambda s: "-".join(map(str, s)))
 def test_slots_on_their_own_keep_h_in_fp32(shape, fmt):
     run(fmt, shape, 0.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [OWN[0], SHARED[0]], ids=lambda s: "-".join(map(str, s)))
+def test_an_infinite_weight_stays_in_its_output(shape):
+    """Infinite or NaN for the tokens of that expert in that column, nothing else changed."""
+    T, k, E, lb, EL, H, I = shape
+    idx, w, x, (w1, _, _), (w2, _, _) = layer.make("bf16", *shape, seed=5)
+    d = B.make_desc(T, k, E, lb, EL)
+    idx, w, x, w1, w2 = (t.cuda() for t in (idx, w, x, w1, w2))
+    want = B.layer_tokens(d, idx, w, x, w1, w2)
+    e = int(idx[0, 0])
+    w2[e - lb, 7, 33] = float("inf")
+    got = B.layer_tokens(d, idx, w, x, w1, w2)
+    mine = (idx == e).any(1)
+    assert not torch.isfinite(got[mine, 7]).any()
+    got[mine, 7] = want[mine, 7]
+    assert torch.equal(got, want)
